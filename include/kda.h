@@ -380,6 +380,178 @@ kda_status kda_intra_chunk(const void *q, const void *k, const void *z,
                            float *Tm, float *Aqk, float *gamma, int B, int T,
                            int H, int d_k, kda_dtype dt, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Linear attention with a decay for each head: the layers of a hybrid stack
+ * whose heads keep a state S in R^{d_k x d_v} without the delta rule,
+ *
+ *   a   = exp(g_h)                    one constant per head
+ *   S_t = a S_{t-1} + k_t v_t^T
+ *   o_t = scale S_t^T q_t
+ *
+ * Conventions beyond those above (which hold here too, head sizes and the
+ * place of beta, A and z apart):
+ * - q, k [B, T, H_k, d_k]; v, o [B, T, H, d_v]; H_k divides H, and heads
+ *   h (H / H_k) .. (h + 1) (H / H_k) - 1 share head h of q and k.
+ * - (d_k, d_v): any of {32, 64, 128} each.  States [B, H, d_k, d_v] fp32, or
+ *   rows of a pool [n_slots, H, d_k, d_v] fp32 in the paged calls, whose slot
+ *   tables work as described under "Paged states".
+ * - g [H] fp32 is the log-decay of each head, a constant of the layer: it has
+ *   no gradient.  g <= 0 is expected; values below -10000 (also -infinity)
+ *   are taken as -10000, for which a is exactly 0 and a^0 is 1.
+ * - scale must be finite.
+ * - lens [B] int32 in device memory (NULL: all T) is each sequence's token
+ *   count in a batch padded to T.  Values are clamped to [0, T].  Tokens at
+ *   or past it are neither read nor written by any kernel (their rows of o,
+ *   or of the gradients, keep what they held), and the final state is the one
+ *   after the last real token: S0 itself for a length of 0.
+ * - Inputs must be finite: an infinity or NaN in one token can reach outputs
+ *   of up to 31 tokens before it as well as all later ones.
+ * - g and lens need 4-byte, the states 16-byte alignment. */
+
+/* Bytes of device workspace kda_linear_prefill and kda_linear_prefill_paged
+ * need for these sizes (0: none; also 0 for arguments they would reject). */
+size_t kda_linear_prefill_workspace_bytes(int B, int T, int H, int H_k, int d_k, int d_v,
+                                          kda_dtype dt);
+
+/* o for every token and, if S_T != NULL, the final state, from S0 (NULL:
+ * zero).  S_T may alias S0 exactly; no other overlap of an output or the
+ * workspace with another argument is allowed. */
+kda_status kda_linear_prefill(const void *q, const void *k, const void *v, const float *g,
+                              float scale, const float *S0, const int *lens, void *o,
+                              float *S_T, int B, int T, int H, int H_k, int d_k, int d_v,
+                              kda_dtype dt, void *workspace, size_t workspace_bytes,
+                              void *stream);
+
+/* kda_linear_prefill from pool row slots_in[b] (NULL: zero states) into pool
+ * row slots_out[b] (NULL: no state written). */
+kda_status kda_linear_prefill_paged(const void *q, const void *k, const void *v,
+                                    const float *g, float scale, float *pool, int n_slots,
+                                    const int *slots_in, const int *slots_out, const int *lens,
+                                    void *o, int B, int T, int H, int H_k, int d_k, int d_v,
+                                    kda_dtype dt, void *workspace, size_t workspace_bytes,
+                                    void *stream);
+
+/* Bytes of device workspace kda_linear_backward needs for these sizes (0:
+ * none; also 0 for arguments it would reject). */
+size_t kda_linear_backward_workspace_bytes(int B, int T, int H, int H_k, int d_k, int d_v,
+                                           kda_dtype dt);
+
+/* Gradients of kda_linear_prefill for L = sum(dO * o) + sum(dS_T * S_T): with
+ * Y_n = dS_T (NULL: zero) after the n tokens of a sequence,
+ *   R_t = scale q_t dO_t^T + Y_{t+1},  Y_t = a R_t,
+ *   dq_t = scale S_t dO_t,  dk_t = R_t v_t,  dv_t = R_t^T k_t,  dS0 = Y_0.
+ * dq, dk [B, T, H_k, d_k] (summed over the heads that share them) and dv
+ * [B, T, H, d_v] have element type dt, dS0 [B, H, d_k, d_v] is fp32 (NULL:
+ * not written; dS_T itself for a length of 0).  The states are recomputed
+ * from the forward call's inputs.  No output may overlap another argument. */
+kda_status kda_linear_backward(const void *q, const void *k, const void *v, const float *g,
+                               float scale, const float *S0, const int *lens, const void *dO,
+                               const float *dS_T, void *dq, void *dk, void *dv, float *dS0,
+                               int B, int T, int H, int H_k, int d_k, int d_v, kda_dtype dt,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+/* One token of every sequence: q, k [B, H_k, d_k], v, o [B, H, d_v]; the state
+ * S is read once and overwritten in place.  o must not overlap another
+ * argument, nor S the inputs. */
+kda_status kda_linear_decode_step(const void *q, const void *k, const void *v, const float *g,
+                                  float scale, float *S, void *o, int B, int H, int H_k,
+                                  int d_k, int d_v, kda_dtype dt, void *stream);
+
+/* kda_linear_decode_step on pool row slots[b], in place. */
+kda_status kda_linear_decode_step_paged(const void *q, const void *k, const void *v,
+                                        const float *g, float scale, float *pool, int n_slots,
+                                        const int *slots, void *o, int B, int H, int H_k,
+                                        int d_k, int d_v, kda_dtype dt, void *stream);
+
+/* Largest number of drafted tokens of one kda_linear_tree call. */
+#define KDA_MAX_TREE_TOKENS 64
+
+/* Outputs of a tree of T <= KDA_MAX_TREE_TOKENS drafted tokens per sequence,
+ * each continuing from its parent's state, with the state S before them read
+ * once and left as it is.  parent [B, T] int32 in device memory: -1 for a
+ * node that follows S directly, else the index of an earlier node, parent[t]
+ * < t.  With n_i the nodes from S to i, i included:
+ *   o_i = scale (a^{n_i} S^T q_i
+ *                + sum over j on the path to i, i included,
+ *                  of a^{n_i - n_j} (q_i . k_j) v_j)
+ * Any other parent value marks an absent node (a tree of fewer drafts is
+ * padded with them); a node below an absent one is absent too.  The o of an
+ * absent node is zero.  o must not overlap another argument. */
+kda_status kda_linear_tree(const void *q, const void *k, const void *v, const float *g,
+                           float scale, const float *S, const int *parent, void *o, int B,
+                           int T, int H, int H_k, int d_k, int d_v, kda_dtype dt,
+                           void *stream);
+
+/* kda_linear_tree from pool row slots[b]; the o of a skipped sequence is not
+ * written. */
+kda_status kda_linear_tree_paged(const void *q, const void *k, const void *v, const float *g,
+                                 float scale, const float *pool, int n_slots, const int *slots,
+                                 const int *parent, void *o, int B, int T, int H, int H_k,
+                                 int d_k, int d_v, kda_dtype dt, void *stream);
+
+/* The state after the path of a tree that was accepted: accepted [B] int32 in
+ * device memory names the last accepted node of each sequence (-1: none, the
+ * state stays),
+ *   S_out = a^n S + sum over the path's nodes j of a^{n - n_j} k_j v_j^T.
+ * S_out may be S itself (in place); no other overlap is allowed.  A sequence
+ * whose accepted node is absent or outside [-1, T) is skipped: its S_out is
+ * not written. */
+kda_status kda_linear_tree_commit(const void *k, const void *v, const float *g,
+                                  const int *parent, const int *accepted, const float *S,
+                                  float *S_out, int B, int T, int H, int H_k, int d_k, int d_v,
+                                  kda_dtype dt, void *stream);
+
+/* kda_linear_tree_commit from pool row slots_in[b] into pool row slots_out[b]
+ * (the same row commits in place). */
+kda_status kda_linear_tree_commit_paged(const void *k, const void *v, const float *g,
+                                        const int *parent, const int *accepted, float *pool,
+                                        int n_slots, const int *slots_in, const int *slots_out,
+                                        int B, int T, int H, int H_k, int d_k, int d_v,
+                                        kda_dtype dt, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The norm of each head's queries and keys with the position rotation in the
+ * same pass (the recurrences above use q and k as given).  For a row x of d
+ * elements of one head at position p:
+ *   n = x (c sum(x^2) + eps)^{-1/2},  c = 1 (KDA_NORM_L2) or 1 / d (KDA_NORM_RMS)
+ *   u = w n                           (w fp32 [d]; NULL: 1)
+ *   y = u with the pairs of its first `rot` elements turned by the angle
+ *       p inv_freq[i] (fp32 [rot / 2], i the pair): (y1, y2) = (u1 cos - u2 sin,
+ *       u2 cos + u1 sin); pair i is elements (i, i + rot / 2), or
+ *       (2 i, 2 i + 1) if interleaved.  The rest of u is y as it is.
+ * Angles are formed and reduced in 64 bits (positions of any int32 value).
+ * q, y_q [B, T, H, d], k, y_k [B, T, H_k, d] of element type dt; d in {32, 64,
+ * 128}, rot even in [0, d] (inv_freq and positions may be NULL for 0);
+ * positions [B, T] int32 in device memory; eps > 0 and finite (a row of
+ * zeros gives zeros). */
+enum { KDA_NORM_L2 = 0, KDA_NORM_RMS = 1 };
+
+/* y_q may be q itself and y_k may be k itself (in place); no other overlap of
+ * an output with another argument is allowed. */
+kda_status kda_qk_norm_rope(const void *q, const void *k, const float *w_q, const float *w_k,
+                            const int *positions, const float *inv_freq, int norm, float eps,
+                            int rot, int interleaved, void *y_q, void *y_k, int B, int T, int H,
+                            int H_k, int d, kda_dtype dt, void *stream);
+
+/* Bytes of device workspace kda_qk_norm_rope_backward needs for these sizes
+ * when a weight's gradient is asked for (0 for arguments it would reject). */
+size_t kda_qk_norm_rope_backward_workspace_bytes(int B, int T, int H, int H_k, int d,
+                                                 kda_dtype dt);
+
+/* Gradients of kda_qk_norm_rope from dy_q, dy_k (shapes and type of y_q, y_k)
+ * and the forward call's inputs (q and k before the norm): dq, dk of element
+ * type dt, and the weights' gradients dw_q, dw_k [d] fp32, summed over all
+ * rows in a fixed order (NULL: not wanted; they need w_q, w_k).  dq may be dy_q and dk may
+ * be dy_k; no other overlap is allowed.  workspace: at least the queried bytes
+ * if dw_q or dw_k is wanted, else it may be NULL. */
+kda_status kda_qk_norm_rope_backward(const void *q, const void *k, const float *w_q,
+                                     const float *w_k, const int *positions,
+                                     const float *inv_freq, int norm, float eps, int rot,
+                                     int interleaved, const void *dy_q, const void *dy_k,
+                                     void *dq, void *dk, float *dw_q, float *dw_k, int B, int T,
+                                     int H, int H_k, int d, kda_dtype dt, void *workspace,
+                                     size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

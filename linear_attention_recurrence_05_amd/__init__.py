@@ -29,6 +29,21 @@ Functions named like the C entry points take torch tensors in the layouts
 ``chunk_prefill``, ``chunk_prefill_segmented``, ``chunk_backward``, ``decode_step`` and
 ``decode_tokens`` additionally allocate the outputs (and
 the workspace) with ``torch.empty`` before calling the same entry points.
+
+Linear attention with a decay for each head, draft trees over its states, and the norm of
+queries and keys with the position rotation (each kda_X with its allocating helper X; paged
+forms take a pool and slot tables):
+
+    kda_linear_prefill(q, k, v, g, scale, S0, o, S_T, lens, workspace, stream)
+    kda_linear_backward(q, k, v, g, scale, S0, dO, dS_T, dq, dk, dv, dS0, lens, workspace, stream)
+    kda_linear_decode_step(q, k, v, g, scale, S, o, stream)
+    kda_linear_tree(q, k, v, g, scale, S, parent, o, stream)
+    kda_linear_tree_commit(k, v, g, parent, accepted, S, S_out, stream)
+    kda_linear_prefill_paged, kda_linear_decode_step_paged, kda_linear_tree_paged,
+    kda_linear_tree_commit_paged
+    kda_qk_norm_rope(q, k, w_q, w_k, positions, inv_freq, norm, eps, interleaved, y_q, y_k, stream)
+    kda_qk_norm_rope_backward(q, k, w_q, w_k, positions, inv_freq, norm, eps, interleaved, dy_q,
+                              dy_k, dq, dk, dw_q, dw_k, workspace, stream)
 """
 from __future__ import annotations
 
@@ -43,6 +58,15 @@ from ._lib import (KDA_BF16, KDA_CHUNK, KDA_F32, KDA_MAX_DECODE_TOKENS, KdaError
                    kda_decode_step, kda_decode_step_paged, kda_decode_tokens,
                    kda_decode_tokens_paged, kda_gate_chunk_cumsum, kda_intra_chunk, lib,
                    library_path, status_string)
+from ._linear import (KDA_MAX_TREE_TOKENS, KDA_NORM_L2, KDA_NORM_RMS, kda_linear_backward,
+                     kda_linear_backward_workspace_bytes, kda_linear_decode_step,
+                     kda_linear_decode_step_paged, kda_linear_prefill,
+                     kda_linear_prefill_paged, kda_linear_prefill_workspace_bytes,
+                     kda_linear_tree, kda_linear_tree_commit, kda_linear_tree_commit_paged,
+                     kda_linear_tree_paged, kda_qk_norm_rope, kda_qk_norm_rope_backward,
+                     kda_qk_norm_rope_backward_workspace_bytes, linear_backward,
+                     linear_decode_step, linear_prefill, linear_tree, linear_tree_commit,
+                     qk_norm_rope, qk_norm_rope_backward)
 
 __all__ = ["KDA_BF16", "KDA_CHUNK", "KDA_F32", "KDA_MAX_DECODE_TOKENS", "KdaError",
            "KdaLibraryMissing", "abi_version", "chunk_backward", "chunk_prefill",
@@ -53,4 +77,12 @@ __all__ = ["KDA_BF16", "KDA_CHUNK", "KDA_F32", "KDA_MAX_DECODE_TOKENS", "KdaErro
            "kda_chunk_prefill_workspace_bytes",
            "kda_decode_step", "kda_decode_step_paged", "kda_decode_tokens",
            "kda_decode_tokens_paged", "kda_gate_chunk_cumsum", "kda_intra_chunk", "lib",
-           "library_path", "status_string"]
+           "library_path", "status_string",
+           "KDA_MAX_TREE_TOKENS", "KDA_NORM_L2", "KDA_NORM_RMS", "kda_linear_backward",
+           "kda_linear_backward_workspace_bytes", "kda_linear_decode_step",
+           "kda_linear_decode_step_paged", "kda_linear_prefill", "kda_linear_prefill_paged",
+           "kda_linear_prefill_workspace_bytes", "kda_linear_tree", "kda_linear_tree_commit",
+           "kda_linear_tree_commit_paged", "kda_linear_tree_paged", "kda_qk_norm_rope",
+           "kda_qk_norm_rope_backward", "kda_qk_norm_rope_backward_workspace_bytes",
+           "linear_backward", "linear_decode_step", "linear_prefill", "linear_tree",
+           "linear_tree_commit", "qk_norm_rope", "qk_norm_rope_backward"]

@@ -12,7 +12,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = ["kda_api.hip", "kda_decode.hip", "kda_tokens.hip", "kda_prefill.hip", "kda_pair.hip", "kda_ring.hip",
-           "kda_backward.hip", "kda_bwd_chunk.hip", "kda_segscan.hip"]
+           "kda_backward.hip", "kda_bwd_chunk.hip", "kda_segscan.hip", "kda_linear_api.hip",
+           "kda_linear.hip", "kda_linear_decode.hip", "kda_linear_tree.hip", "kda_norm_rope.hip"]
 # Machine scheduler per source.  The fused prefill passes and the single-token
 # decode step run 2.5-4% faster under the ILP-first strategy (measured at B1
 # H32 T1,048,576 and B8 T32768, and at B = 256 with dense and pooled states);
