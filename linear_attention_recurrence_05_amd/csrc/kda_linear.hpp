@@ -13,6 +13,7 @@ namespace kda {
 // Log-decays below this are taken as this: exp of it, and of any multiple, is
 // exactly 0 in fp32, and 0 times it is 0 (0 times -infinity would be NaN).
 constexpr float kMinLogDecay = -1e4f;
+__device__ __forceinline__ float log_decay(float g) { return g < kMinLogDecay ? kMinLogDecay : g; }   // NaN stays
 
 // One tensor [B, T, n, d] that the H heads of a pass read or write; head h of
 // the pass uses head h / (H / n).

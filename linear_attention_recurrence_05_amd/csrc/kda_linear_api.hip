@@ -17,6 +17,10 @@ kda_status check_dtype(kda_dtype dt) {
     return KDA_OK;
 }
 
+// Most (b, h) of a linear-attention call: one workgroup of up to 512 threads
+// each, and a launch holds fewer than 2^32 threads.
+constexpr long long kMaxUnits = 1LL << 23;
+
 // Sizes of a linear-attention call, in elements.
 struct Sizes {
     size_t qk, vo, state, tok;   // q or k; v or o; all states; tokens B * T
@@ -31,6 +35,8 @@ kda_status check_sizes(int B, int T, int H, int H_k, int d_k, int d_v, kda_dtype
     if (!std::isfinite(scale)) return fail(KDA_ERR_INVALID_VALUE, "scale = %g is not finite", (double)scale);
     size_t nel, ntok;
     if ((s = check_shape(B, T, H, d_k > d_v ? d_k : d_v, nel, ntok)) != KDA_OK) return s;
+    if ((long long)B * H > kMaxUnits)
+        return fail(KDA_ERR_INVALID_SHAPE, "B*H = %lld is too large (limit 2^23)", (long long)B * H);
     if (H_k < 1 || H_k > H || H % H_k != 0)
         return fail(KDA_ERR_INVALID_SHAPE, "H_k=%d must divide H=%d", H_k, H);
     n.tok = (size_t)B * T;

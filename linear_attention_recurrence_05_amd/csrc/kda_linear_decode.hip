@@ -16,7 +16,7 @@ __global__ __launch_bounds__(256) void linear_decode_kernel(LinearDecode p) {
     if (p.S.skip(b)) return;
     const size_t unit = (size_t)b * p.H + h;
     const size_t row = (size_t)b * p.Hk + h / (p.H / p.Hk);
-    const float a = expf(fmaxf(p.g[h], kMinLogDecay));
+    const float a = expf(log_decay(p.g[h]));
     for (int i = tid; i < DK; i += 256) {
         s_q[i] = to_f32(((const E*)p.q)[row * DK + i]);
         s_k[i] = to_f32(((const E*)p.k)[row * DK + i]);

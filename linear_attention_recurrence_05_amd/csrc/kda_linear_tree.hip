@@ -46,7 +46,7 @@ __global__ __launch_bounds__(DV < 64 ? 64 : DV) void linear_tree_kernel(LinearTr
     const int b = blockIdx.x / p.H, h = blockIdx.x % p.H, c = threadIdx.x;
     if (p.S.skip(b)) return;
     const int hk = h / (p.H / p.Hk);
-    const float g = fmaxf(p.g[h], kMinLogDecay);
+    const float g = log_decay(p.g[h]);
     if (c < kWave) s_path[c] = tree_path(p.parent + (size_t)b * p.T, p.T);
     const float* S = p.S.in + ((size_t)(p.S.in_slot ? p.S.in_slot[b] : b) * p.H + h) * DK * DV;
     for (int i = 0; i < p.T; ++i) {
@@ -87,7 +87,7 @@ __global__ __launch_bounds__(256) void linear_commit_kernel(LinearTree p) {
     const int x = p.accepted[b];
     if (x < -1 || x >= p.T) return;
     const int hk = h / (p.H / p.Hk);
-    const float g = fmaxf(p.g[h], kMinLogDecay);
+    const float g = log_decay(p.g[h]);
     if (tid < kWave) s_path[tid] = tree_path(p.parent + (size_t)b * p.T, p.T);
     __syncthreads();
     const uint64_t path = x < 0 ? 0 : s_path[x];

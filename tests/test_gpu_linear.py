@@ -133,6 +133,24 @@ def test_prefill_in_place_state_and_continuation():
     check_prefill(x, o, S)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_prefill_in_place_state_of_long_sequences(dtype):
+    """Segments of one sequence run side by side; the final state may take the
+    initial one's place all the same."""
+    need_gpu()
+    import linear_attention_recurrence_05_amd as kda
+    x, _ = make(3, 2100, 2, 1, 64, 128, dtype, seed=17, lens=[2100, 700, 31])
+    args = (x["q"], x["k"], x["v"], x["g"], x["scale"])
+    o, S_T = kda.linear_prefill(*args, x["S0"], x["lens"])
+    ws = torch.empty(kda.kda_linear_prefill_workspace_bytes(3, 2100, 2, 1, 64, 128, dtype), dtype=torch.uint8,
+                     device="cuda")
+    for _ in range(5):
+        S, o2 = x["S0"].clone(), torch.zeros_like(o)
+        kda.kda_linear_prefill(*args, S, o2, S, x["lens"], ws)
+        torch.cuda.synchronize()
+        assert torch.equal(S, S_T) and torch.equal(o2, o)
+
+
 def bwd_ref(x):
     a = absolute(x)
     arg = ("q", "k", "v", "g", "scale", "dO", "S0", "dS_T", "lens")

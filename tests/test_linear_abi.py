@@ -78,7 +78,7 @@ def test_linear_calls_refuse(name):
         (dict(B=0), "KDA_ERR_INVALID_SHAPE"), (dict(H=0), "KDA_ERR_INVALID_SHAPE"),
         (dict(H_k=3), "KDA_ERR_INVALID_SHAPE"), (dict(H_k=0), "KDA_ERR_INVALID_SHAPE"),
         (dict(H_k=8), "KDA_ERR_INVALID_SHAPE"), (dict(T=0), "KDA_ERR_INVALID_SHAPE"),
-        (dict(B=1 << 26), "KDA_ERR_INVALID_SHAPE"), (dict(H=1 << 18, H_k=1 << 18), "KDA_ERR_INVALID_SHAPE"),
+        (dict(B=1 << 26), "KDA_ERR_INVALID_SHAPE"), (dict(B=(1 << 21) + 1, H=4), "KDA_ERR_INVALID_SHAPE"), (dict(H=1 << 18, H_k=1 << 18), "KDA_ERR_INVALID_SHAPE"),
         (dict(d_k=48), "KDA_ERR_UNSUPPORTED"), (dict(d_v=256), "KDA_ERR_UNSUPPORTED"),
         (dict(dt=2), "KDA_ERR_UNSUPPORTED"), (dict(scale=INF), "KDA_ERR_INVALID_VALUE"),
         (dict(scale=float("nan")), "KDA_ERR_INVALID_VALUE"), (dict(n_slots=0), "KDA_ERR_INVALID_SHAPE"),
