@@ -43,6 +43,9 @@ _lib._SIGNATURES.update({
                                   + [_vp, _z, _vp], _i),
 })
 
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+
 _F32 = torch.float32
 _I32 = torch.int32
 
@@ -102,12 +105,15 @@ class _Call:
         """Calls the entry point on `stream`, with the tensors' device current."""
         if self.dev.type != "cuda":
             raise ValueError(f"{self.where}: tensors must be on a CUDA device, got {self.dev}")
-        fn = getattr(lib(), name)
-        if self.dev.index == torch.cuda.current_device():
-            st = fn(*args, _raw(torch.cuda.current_stream() if stream is None else stream))
+        fn, i = getattr(lib(), name), self.dev.index
+        # torch's own bindings for the current stream and device: the public
+        # functions around them cost several times what the launch does
+        raw = _current_stream(i) if stream is None else _raw(stream)
+        if i == _current_device():
+            st = fn(*args, raw)
         else:
             with torch.cuda.device(self.dev):
-                st = fn(*args, _raw(torch.cuda.current_stream() if stream is None else stream))
+                st = fn(*args, raw)
         if st:
             _check(st, name)
 

@@ -20,79 +20,11 @@
 
 #include "kda_device.hpp"
 #include "kda_linear.hpp"
+#include "kda_linear_frag.hpp"
 
 namespace kda {
 
 constexpr int kLinChunk = 32;
-
-// ------------------------------------------------------------------ operands
-
-// Eight values of a lane, of 32 along a contraction: lane group g = lane / 16
-// holds eight of them (which ones is the caller's choice, the same for both
-// operands).
-template <typename E> struct Frag;
-template <> struct Frag<bf16> { bf16x8 v; };
-template <> struct Frag<float> { f32x4 lo, hi; };
-
-__device__ __forceinline__ f32x4 mma(const Frag<bf16>& a, const Frag<bf16>& b, f32x4 c) {
-    return mma_bf16_k32(a.v, b.v, c);
-}
-__device__ __forceinline__ f32x4 mma(const Frag<float>& a, const Frag<float>& b, f32x4 c) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c = mma_f32_k4(a.lo[i], b.lo[i], c);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c = mma_f32_k4(a.hi[i], b.hi[i], c);
-    return c;
-}
-
-template <typename E> __device__ __forceinline__ Frag<E> to_frag(f32x4 lo, f32x4 hi);
-template <> __device__ __forceinline__ Frag<bf16> to_frag<bf16>(f32x4 lo, f32x4 hi) { return {pack8(lo, hi)}; }
-template <> __device__ __forceinline__ Frag<float> to_frag<float>(f32x4 lo, f32x4 hi) { return {lo, hi}; }
-
-__device__ __forceinline__ void to_f32(const Frag<bf16>& a, f32x4& lo, f32x4& hi) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        lo[i] = (float)a.v[i];
-        hi[i] = (float)a.v[4 + i];
-    }
-}
-__device__ __forceinline__ void to_f32(const Frag<float>& a, f32x4& lo, f32x4& hi) {
-    lo = a.lo;
-    hi = a.hi;
-}
-
-// Eight consecutive elements of a row in LDS (16-byte aligned).
-template <typename E> __device__ __forceinline__ Frag<E> row_frag(const E* p);
-template <> __device__ __forceinline__ Frag<bf16> row_frag<bf16>(const bf16* p) {
-    return {*reinterpret_cast<const bf16x8*>(p)};
-}
-template <> __device__ __forceinline__ Frag<float> row_frag<float>(const float* p) {
-    return {*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 4)};
-}
-
-// Lane (j, g) = 16 g + j: column `col(j)` of rows 4 g + {0..3} and 16 + 4 g +
-// {0..3} of a [32][ld] tile in LDS, where col(j) = c0 + step (j / 4) + j % 4.
-// bf16: two transposing reads, for which a lane names row j / 4 and column
-// group j % 4 of its group's 4 x 16 block.
-template <typename E>
-__device__ __forceinline__ Frag<E> col_frag(const E* s, int ld, int c0, int step, int j, int g) {
-    Frag<E> f;
-    if constexpr (sizeof(E) == 2) {
-        typedef __attribute__((address_space(3))) i16x4 lds4;
-        const E* p = s + (4 * g + (j >> 2)) * ld + c0 + step * (j & 3);
-        const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)p);
-        const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p + 16 * ld));
-        f.v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-    } else {
-        const E* p = s + 4 * g * ld + c0 + step * (j >> 2) + (j & 3);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f.lo[i] = p[i * ld];
-            f.hi[i] = p[(16 + i) * ld];
-        }
-    }
-    return f;
-}
 
 // x in fp32 as a sum of bf16 terms: three hold its 24 bits, so a product with
 // a bf16 operand keeps fp32's accuracy.
@@ -114,11 +46,19 @@ __device__ __forceinline__ void split(f32x4 lo, f32x4 hi, Frag<float> (&out)[1])
 // workspace what each segment but the last adds to a zero state, the second
 // starts every segment from the initial state and the ones before it.
 struct LinearSegs {
-    float* ws;   // [unit][R][DA * DB]: R - 1 segments' states, then the initial one
     int R, len;  // segments of a sequence, their length in steps (a multiple of 32)
 };
 
-// One workgroup per (b, h, segment); NW waves, each with NC tiles of 16
+// Up to three passes of the same sizes in one launch (the gradients), each
+// with its workspace [unit][R][DA * DB]: R - 1 segments' states, then the
+// initial one.
+struct LinearJob {
+    LinearPass pass[3];
+    float* ws[3];
+    LinearSegs segs;
+};
+
+// One workgroup per (b, h, segment), one wave for each NC tiles of 16
 // columns of the state [DA, DB] in registers (MFMA accumulator layout).  A
 // state tile pair in that layout is an operand of M^T x without a move: rows
 // are mapped to channels so that a lane's rows of two tiles are eight
@@ -127,19 +67,24 @@ struct LinearSegs {
 // pair weights are computed transposed (keys x queries) by every wave, which
 // makes the product with u take them straight from the accumulators.
 // STATE: only the state of a segment from zero, into the workspace.
-template <typename E, typename O, int DA, int DB, int NW, int NC, bool STATE>
-__global__ __launch_bounds__(NW * 64, 2) void linear_chunk_kernel(LinearPass p, LinearSegs segs) {
-    constexpr int C = kLinChunk, NT = NW * 64, KM = DA / 32, NS = sizeof(E) == 2 ? 3 : 1;
+template <typename E, int DA, int DB, int NC, bool STATE>
+__global__ __launch_bounds__(DB / NC * 4, 2) void linear_chunk_kernel(LinearJob job) {
+    constexpr int C = kLinChunk, NT = DB / NC * 4, KM = DA / 32, NS = sizeof(E) == 2 ? 3 : 1;
     constexpr int PE = 16 / sizeof(E);                       // elements of 16 bytes
-    constexpr int LA = DA + PE, LB = DB + PE;                // padded LDS rows
+    // padded LDS rows: rows 12 (mod 16) banks apart for x and y, so that both 16
+    // rows of 16 bytes and the transposing reads of 8-byte groups 16 bytes apart
+    // spread over the banks; 8 (mod 16) apart for u
+    constexpr int LA = DA + (sizeof(E) == 2 ? 24 : 4), LB = DB + (sizeof(E) == 2 ? 16 : 4);
     constexpr int PA = C * DA / PE, PB = C * DB / PE;        // 16-byte pieces of a tile
     constexpr int RA = (PA + NT - 1) / NT, RB = (PB + NT - 1) / NT;
-    static_assert(NW * NC * 16 == DB, "waves cover the columns");
+    static_assert(DB % (16 * NC) == 0, "waves cover the columns");
     __shared__ __align__(16) E s_x[STATE ? 1 : 2][STATE ? 8 : C * LA];
     __shared__ __align__(16) E s_y[2][C * LA], s_u[2][C * LB];
 
-    const int units = p.B * p.H;
-    const int unit = blockIdx.x % units, seg = blockIdx.x / units;
+    const LinearSegs segs = job.segs;
+    const int units = job.pass[0].B * job.pass[0].H, nseg = STATE ? segs.R - 1 : segs.R;
+    const int unit = blockIdx.x % units, at = blockIdx.x / units, seg = at % nseg, role = at / nseg;
+    const LinearPass& p = job.pass[role];
     const int b = unit / p.H, h = unit % p.H;
     if (p.S.skip(b)) return;
     const int n = p.lens ? min(max(p.lens[b], 0), p.T) : p.T;
@@ -161,7 +106,7 @@ __global__ __launch_bounds__(NW * 64, 2) void linear_chunk_kernel(LinearPass p, 
     // initial one came from, so with several segments only the first launch
     // reads that, and copies it.
     auto slot = [&](int m) {
-        return reinterpret_cast<f32x4*>(segs.ws + ((size_t)unit * segs.R + m) * (DA * DB)) + wave * 2 * KM * NC * 64 + lane;
+        return reinterpret_cast<f32x4*>(job.ws[role] + ((size_t)unit * segs.R + m) * (DA * DB)) + wave * NC * 2 * KM * 64 + lane;
     };
     const bool direct = STATE || (seg == 0 && last);
     const float* in = p.S.in && (STATE ? seg == 0 : direct)
@@ -182,7 +127,6 @@ __global__ __launch_bounds__(NW * 64, 2) void linear_chunk_kernel(LinearPass p, 
             }
         }
     if (!direct) {
-        const float as = expf(lg * (float)segs.len);
         if (p.S.in) {
             const f32x4* w = slot(segs.R - 1);
 #pragma unroll
@@ -190,6 +134,7 @@ __global__ __launch_bounds__(NW * 64, 2) void linear_chunk_kernel(LinearPass p, 
 #pragma unroll
                 for (int ct = 0; ct < NC; ++ct) M[t][ct] = w[(t * NC + ct) * 64];
         }
+        const float as = expf(lg * (float)segs.len);
         for (int m = 0; m < seg; ++m) {
             const f32x4* w = slot(m);
 #pragma unroll
@@ -200,7 +145,7 @@ __global__ __launch_bounds__(NW * 64, 2) void linear_chunk_kernel(LinearPass p, 
     }
 
     // ---- weights of a chunk of c steps
-    float wd[4], wo[4], wi[2], wu[8], ac, ac_lo;
+    float wd[4], wo[4], wi[2], wu[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int d = j - 4 * g - i;                         // query - key within a 16 x 16 block
@@ -209,75 +154,109 @@ __global__ __launch_bounds__(NW * 64, 2) void linear_chunk_kernel(LinearPass p, 
     }
 #pragma unroll
     for (int q = 0; q < 2; ++q) wi[q] = p.so * expf(lg * (float)(16 * q + j + 1 - rev));
+    // a^c as an fp32 factor: the part of a^c that each rounding leaves out goes
+    // into the next chunk's factor, so the factors' product stays a^{steps}
+    // however many chunks there are.
+    double ac = 0, ac_inv = 0, ac_left = 0;
     auto chunk_weights = [&](int c) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int left = c - 1 - ((i & 4) * 4 + 4 * g + (i & 3));
             wu[i] = left >= 0 ? p.su * expf(lg * (float)(left + rev)) : 0.f;
         }
-        const double d = exp((double)lg * c);                // in two parts: their product with M
-        ac = (float)d;                                       // is a^c M to fp32, chunk after chunk
-        ac_lo = (float)(d - (double)ac);
+        ac = exp((double)lg * c);
+        ac_inv = ac > 1e-30 ? 1.0 / ac : 0.0;
+    };
+    auto chunk_decay = [&]() {
+        const double want = ac + ac * ac_left;
+        const float f = (float)want;
+        ac_left = (want - (double)f) * ac_inv;
+        return f;
     };
 
-    // ---- loads of a chunk: rows in step order, zero past its end
+    // ---- rows of a chunk in step order.  Thread offsets within a chunk are
+    // constant; the chunk's base (for a reverse pass 32 tokens below its first
+    // step, which may lie before the tensor) moves on.  Rows past the chunk's
+    // end get an offset past the buffer's: zero.
+    struct Rows {
+        const char* base;
+        int64_t step;
+        uint32_t bytes;
+        int ld;
+    };
+    const int os = p.out_f32 ? 4 : (int)sizeof(E);           // bytes of an element of out
+    auto rows_of = [&](const void* ptr, int heads, int head, int d, int es) {
+        const int ld = heads * d * es;
+        const int64_t t0 = (int64_t)b * p.T + (rev ? n - s0 - C : s0);
+        return Rows{(const char*)ptr + t0 * ld + (int64_t)head * d * es, (rev ? -C : C) * (int64_t)ld,
+                    (uint32_t)((C - 1) * ld + d * es), ld};
+    };
+    auto row_off = [&](int row, int ld) { return (rev ? C - 1 - row : row) * ld; };
+    constexpr int kPast = -16;                               // an offset past any buffer's end
+    Rows X = rows_of(p.x.p, p.x.n, hx, DA, sizeof(E)), Y = rows_of(p.y.p, p.y.n, hy, DA, sizeof(E)),
+         U = rows_of(p.u.p, p.u.n, hu, DB, sizeof(E)), Out = rows_of(p.out, p.n_out, ho, DB, os);
+    auto row_of = [&](int i, int d) { return (tid + i * NT) / (d / PE); };
+    int ox[RA], oy[RA], ou[RB], oo[2];
+#pragma unroll
+    for (int i = 0; i < RA; ++i) {
+        ox[i] = row_off(row_of(i, DA), X.ld) + (tid + i * NT) % (DA / PE) * 16;
+        oy[i] = row_off(row_of(i, DA), Y.ld) + (tid + i * NT) % (DA / PE) * 16;
+    }
+#pragma unroll
+    for (int i = 0; i < RB; ++i) ou[i] = row_off(row_of(i, DB), U.ld) + (tid + i * NT) % (DB / PE) * 16;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) oo[q] = row_off(16 * q + j, Out.ld) + (cbase + cstep * g) * os;
+
     u32x4 rx[RA], ry[RA], ru[RB];
-    auto load = [&](int s) {
-        const int c = min(C, s1 - s);
-        const size_t t0 = (size_t)b * p.T + (rev ? n - s - c : s);
-        auto rsrc = [&](const HeadTensor& t, int head, int d) {
-            const int ld = t.n * d * (int)sizeof(E);
-            return make_rsrc((const char*)t.p + t0 * ld + (size_t)head * d * sizeof(E), (c - 1) * (uint32_t)ld + d * sizeof(E));
-        };
-        auto tile = [&](Rsrc r, int ld, int d, int i) {
-            const int at = tid + i * NT, row = at / (d / PE), piece = at % (d / PE);
-            const int off = (rev ? c - 1 - row : row) * ld + piece * 16;
-            return buf_load<u32x4>(r, row < c ? off : -1 << 4);
-        };
-        const Rsrc x = rsrc(p.x, hx, DA), y = rsrc(p.y, hy, DA), u = rsrc(p.u, hu, DB);
+    // The next chunk, of c steps.  Past the last one (c <= 0) every offset is
+    // past the buffer: the loads are issued all the same, so that the number in
+    // flight is known at every wait (a branch around them made each wait one
+    // for the youngest load: 1.6 us a chunk).
+    auto load = [&](int c) {
+        const Rsrc x = make_rsrc(X.base, X.bytes), y = make_rsrc(Y.base, Y.bytes), u = make_rsrc(U.base, U.bytes);
 #pragma unroll
         for (int i = 0; i < RA; ++i) {
-            if (!STATE) rx[i] = tile(x, p.x.n * DA * (int)sizeof(E), DA, i);
-            ry[i] = tile(y, p.y.n * DA * (int)sizeof(E), DA, i);
+            const bool in = row_of(i, DA) < c;
+            if (!STATE) rx[i] = buf_load<u32x4>(x, in ? ox[i] : kPast);
+            ry[i] = buf_load<u32x4>(y, in ? oy[i] : kPast);
         }
 #pragma unroll
-        for (int i = 0; i < RB; ++i) ru[i] = tile(u, p.u.n * DB * (int)sizeof(E), DB, i);
+        for (int i = 0; i < RB; ++i) ru[i] = buf_load<u32x4>(u, row_of(i, DB) < c ? ou[i] : kPast);
+        X.base += X.step;
+        Y.base += Y.step;
+        U.base += U.step;
     };
-    auto stage = [&](int buf) {
+    auto stage = [&](auto set) {
+        constexpr int buf = decltype(set)::value;
 #pragma unroll
         for (int i = 0; i < RA; ++i) {
-            const int at = tid + i * NT, row = at / (DA / PE), piece = at % (DA / PE);
-            if (PA % NT == 0 || at < PA) {
-                if (!STATE) *reinterpret_cast<u32x4*>(&s_x[buf][row * LA + piece * PE]) = rx[i];
-                *reinterpret_cast<u32x4*>(&s_y[buf][row * LA + piece * PE]) = ry[i];
+            const int at = row_of(i, DA) * LA + (tid + i * NT) % (DA / PE) * PE;
+            if (PA % NT == 0 || tid + i * NT < PA) {
+                if (!STATE) *reinterpret_cast<u32x4*>(&s_x[STATE ? 0 : buf][at]) = rx[i];
+                *reinterpret_cast<u32x4*>(&s_y[buf][at]) = ry[i];
             }
         }
 #pragma unroll
         for (int i = 0; i < RB; ++i) {
-            const int at = tid + i * NT, row = at / (DB / PE), piece = at % (DB / PE);
-            if (PB % NT == 0 || at < PB) *reinterpret_cast<u32x4*>(&s_u[buf][row * LB + piece * PE]) = ru[i];
+            const int at = row_of(i, DB) * LB + (tid + i * NT) % (DB / PE) * PE;
+            if (PB % NT == 0 || tid + i * NT < PB) *reinterpret_cast<u32x4*>(&s_u[buf][at]) = ru[i];
         }
     };
 
-    if (s0 < s1) {
-        load(s0);
-        stage(0);
-        if (s0 + C < s1) load(s0 + C);
-        chunk_weights(C);
-    }
-    int buf = 0;
-    for (int s = s0; s < s1; s += C, buf ^= 1) {
+    // One chunk from LDS buffer k; the next is staged into the other buffer and
+    // the one after it set out for.
+    auto chunk = [&](auto set, int s) {
+        constexpr int k = decltype(set)::value;
+        constexpr std::integral_constant<int, 1 - k> other{};
         const int c = min(C, s1 - s);
         __syncthreads();                                     // this chunk is staged, the last one read
-        if (s + C < s1) {
-            stage(buf ^ 1);
-            if (s + 2 * C < s1) load(s + 2 * C);
-        }
+        stage(other);
+        load(s1 - s - 2 * C);
         if (c < C) chunk_weights(c);
-        const E *X = s_x[STATE ? 0 : buf], *Y = s_y[buf], *U = s_u[buf];
+        const E *sx = s_x[STATE ? 0 : k], *sy = s_y[k], *su = s_u[k];
         Frag<E> uf[NC];
 #pragma unroll
-        for (int ct = 0; ct < NC; ++ct) uf[ct] = col_frag<E>(U, LB, cbase + 4 * ct, cstep, j, g);
+        for (int ct = 0; ct < NC; ++ct) uf[ct] = col_frag<E>(su, LB, cbase + 4 * ct, cstep, j, g);
         if constexpr (!STATE) {
             f32x4 p00 = zero4(), p01 = zero4(), p11 = zero4(), o[NC][2];
 #pragma unroll
@@ -285,8 +264,8 @@ __global__ __launch_bounds__(NW * 64, 2) void linear_chunk_kernel(LinearPass p, 
 #pragma unroll
             for (int m = 0; m < KM; ++m) {
                 const int e = 32 * m + 8 * g;
-                const Frag<E> x0 = row_frag<E>(X + j * LA + e), x1 = row_frag<E>(X + (16 + j) * LA + e);
-                const Frag<E> y0 = row_frag<E>(Y + j * LA + e), y1 = row_frag<E>(Y + (16 + j) * LA + e);
+                const Frag<E> x0 = row_frag<E>(sx + j * LA + e), x1 = row_frag<E>(sx + (16 + j) * LA + e);
+                const Frag<E> y0 = row_frag<E>(sy + j * LA + e), y1 = row_frag<E>(sy + (16 + j) * LA + e);
                 p00 = mma(y0, x0, p00);
                 p01 = mma(y0, x1, p01);
                 p11 = mma(y1, x1, p11);
@@ -306,24 +285,26 @@ __global__ __launch_bounds__(NW * 64, 2) void linear_chunk_kernel(LinearPass p, 
             }
             // the pair weights rounded once to E for their product with u
             const Frag<E> w0 = to_frag<E>(p00, zero4()), w1 = to_frag<E>(p01, p11);
+            const Rsrc out = make_rsrc(Out.base, Out.bytes);
+            Out.base += Out.step;
 #pragma unroll
             for (int ct = 0; ct < NC; ++ct) {
                 o[ct][0] = mma(uf[ct], w0, wi[0] * o[ct][0]);
                 o[ct][1] = mma(uf[ct], w1, wi[1] * o[ct][1]);
             }
-            const size_t t0 = (size_t)b * p.T + (rev ? n - s - c : s);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const int r = 16 * q + j;
-                if (r < c) {
-                    O* dst = (O*)p.out + ((t0 + (rev ? c - 1 - r : r)) * p.n_out + ho) * DB + cbase + cstep * g;
-#pragma unroll
-                    for (int ct = 0; ct < NC; ++ct) {
-                        if constexpr (sizeof(O) == 2)
-                            *reinterpret_cast<bf16x4*>(dst + 4 * ct) = pack4(o[ct][q]);
-                        else
-                            *reinterpret_cast<f32x4*>(dst + 4 * ct) = o[ct][q];
+                const int off = 16 * q + j < c ? oo[q] : kPast;
+                if (os == 2) {
+                    if constexpr (NC == 2) {
+                        buf_store_u32x4(out, off, __builtin_bit_cast(u32x4, pack8(o[0][q], o[1][q])));
+                    } else {
+                        buf_store_u32x2(out, off, __builtin_bit_cast(u32x2, pack4(o[0][q])));
                     }
+                } else {
+#pragma unroll
+                    for (int ct = 0; ct < NC; ++ct)
+                        buf_store_u32x4(out, off == kPast ? kPast : off + 16 * ct, __builtin_bit_cast(u32x4, o[ct][q]));
                 }
             }
         }
@@ -339,16 +320,32 @@ __global__ __launch_bounds__(NW * 64, 2) void linear_chunk_kernel(LinearPass p, 
             }
             split(lo, hi, us[ct]);
         }
+        const float f = chunk_decay();
 #pragma unroll
         for (int t = 0; t < 2 * KM; ++t) {
-            const Frag<E> yt = col_frag<E>(Y, LA, 32 * (t >> 1) + 4 * (t & 1), 8, j, g);
+            const Frag<E> yt = col_frag<E>(sy, LA, 32 * (t >> 1) + 4 * (t & 1), 8, j, g);
 #pragma unroll
             for (int ct = 0; ct < NC; ++ct) {
-                f32x4 acc = M[t][ct] * ac_lo + M[t][ct] * ac;
+                f32x4 acc = f * M[t][ct];
 #pragma unroll
-                for (int k = 0; k < NS; ++k) acc = mma(yt, us[ct][k], acc);
+                for (int i = 0; i < NS; ++i) acc = mma(yt, us[ct][i], acc);
                 M[t][ct] = acc;
             }
+        }
+    };
+
+    if (s0 < s1) {
+        constexpr std::integral_constant<int, 0> set0{};
+        constexpr std::integral_constant<int, 1> set1{};
+        chunk_weights(C);
+        load(s1 - s0);
+        stage(set0);
+        load(s1 - s0 - C);
+        for (int s = s0;; s += 2 * C) {
+            chunk(set0, s);
+            if (s + C >= s1) break;
+            chunk(set1, s + C);
+            if (s + 2 * C >= s1) break;
         }
     }
 
@@ -370,120 +367,156 @@ __global__ __launch_bounds__(NW * 64, 2) void linear_chunk_kernel(LinearPass p, 
     }
 }
 
-// dst[row, hk] = the sum of src[row, h] over the heads h that share hk, in
-// order.  src fp32 [rows, H, d].
+// dq[row, hk], then dk: the sum of src[row, h] over the heads h that share hk,
+// in order.  src: dq's then dk's, each fp32 [rows, H, d]; count elements each.
 template <typename E>
-__global__ __launch_bounds__(256) void linear_share_kernel(const float* __restrict__ src, E* __restrict__ dst,
-                                                           const int* __restrict__ lens, int T, int Hk, int G,
-                                                           int d, size_t count) {
-    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < count; i += (size_t)gridDim.x * 256) {
+__global__ __launch_bounds__(256) void linear_share_kernel(const float* __restrict__ src, E* __restrict__ dq,
+                                                           E* __restrict__ dk, const int* __restrict__ lens, int T,
+                                                           int Hk, int G, int d, size_t count) {
+    for (size_t at = (size_t)blockIdx.x * 256 + threadIdx.x; at < 2 * count; at += (size_t)gridDim.x * 256) {
+        const size_t i = at < count ? at : at - count;
         const size_t tok = i / ((size_t)Hk * d), rest = i % ((size_t)Hk * d);
         if (lens && (int)(tok % T) >= lens[tok / T]) continue;
         const int hk = (int)(rest / d), e = (int)(rest % d);
+        const float* from = src + (at < count ? 0 : count * G) + (tok * Hk * G + (size_t)hk * G) * d + e;
         float s = 0.f;
-        for (int j = 0; j < G; ++j) s += src[(tok * Hk * G + (size_t)hk * G + j) * d + e];
-        dst[i] = from_f32<E>(s);
+        for (int j = 0; j < G; ++j) s += from[j * d];
+        (at < count ? dq : dk)[i] = from_f32<E>(s);
     }
 }
 
 // ------------------------------------------------------------------ launches
 
-// Segments of a sequence: as many as give the device 512 workgroups (two for
-// each CU), of 256 steps at least.
-static LinearSegs segments(int B, int T, int H, void* ws) {
-    const long long units = (long long)B * H;
-    int R = (int)((512 + units - 1) / units);
-    R = std::min({R, std::max(1, T / 256), 16});
-    int len = (T + R - 1) / R;
-    len = (len + kLinChunk - 1) / kLinChunk * kLinChunk;
-    R = (T + len - 1) / len;
-    return {(float*)ws, R, len};
+// Segments of a sequence.  One segment leaves CUs idle where there are few
+// (b, h); R of them cost a first launch over the tokens, and every workgroup
+// of the second reads the states before its own.  The estimate below, in us,
+// is taken for each R and the least wins.  Its constants are measured: a chunk
+// takes `out` us in the second launch and `state` us in the first (latency,
+// until a CU has several workgroups), the first launch 6 us of its own, and the
+// states move at 5 TB/s.  B1 H32 T4096 d128 bf16: 197 us with one segment, 92 with
+// 4, 63 with 8, 78 with 16; B8 H32 T8192: 492 with one, 640 with 2.
+static LinearSegs segments(int passes, int B, int T, int H, int da, int db, bool is_bf16) {
+    const double units = (double)B * H * passes, size = da * db / 16384.0;
+    const double out = is_bf16 ? 0.7 + 0.7 * size : 0.8 + 6.5 * size;
+    const double state = is_bf16 ? 0.4 + 0.35 * size : 0.4 + 2.6 * size;
+    LinearSegs best{1, (T + kLinChunk - 1) / kLinChunk * kLinChunk};
+    double least = 0;
+    for (int r = 1; r <= 32; ++r) {
+        const int chunks = ((T + r - 1) / r + kLinChunk - 1) / kLinChunk, len = chunks * kLinChunk;
+        const int R = (T + len - 1) / len;
+        if (R != r) continue;
+        const double busy = std::max(1.0, 0.65 * units * R / 256);
+        double us = chunks * out * busy;
+        if (R > 1) us += 6 + chunks * state * busy + units * da * db * 4 * (0.5 * R * (R - 1) + 2 * R) / 5e6;
+        if (r == 1 || us < least) {
+            least = us;
+            best = {R, len};
+        }
+    }
+    return best;
 }
 
-size_t linear_prefill_ws_bytes(int B, int T, int H, int da, int db, bool is_bf16) {
-    const int R = segments(B, T, H, nullptr).R;
+static size_t segs_bytes(int passes, int B, int T, int H, int da, int db, bool is_bf16) {
+    const int R = segments(passes, B, T, H, da, db, is_bf16).R;
     return R > 1 ? (size_t)B * H * R * da * db * sizeof(float) : 0;
 }
 
-template <typename E, typename O, int DA, int DB>
-static hipError_t launch_pass_d(const LinearPass& p, void* ws, hipStream_t stream) {
-    constexpr int NW = DB == 32 ? 2 : 4, NC = DB / 16 / NW;
-    const LinearSegs s = segments(p.B, p.T, p.H, ws);
-    const unsigned units = (unsigned)(p.B * p.H);
-    if (s.R > 1) {
-        hipLaunchKernelGGL((linear_chunk_kernel<E, O, DA, DB, NW, NC, true>), dim3(units * (s.R - 1)),
-                           dim3(NW * 64), 0, stream, p, s);
+template <typename E, int DA, int DB, int NC>
+static hipError_t launch_job_n(const LinearJob& job, int passes, hipStream_t stream) {
+    const unsigned groups = (unsigned)(job.pass[0].B * job.pass[0].H) * passes;
+    const dim3 block(DB / NC * 4);
+    if (job.segs.R > 1) {
+        hipLaunchKernelGGL((linear_chunk_kernel<E, DA, DB, NC, true>), dim3(groups * (job.segs.R - 1)), block, 0, stream,
+                           job);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((linear_chunk_kernel<E, O, DA, DB, NW, NC, false>), dim3(units * s.R), dim3(NW * 64), 0,
-                       stream, p, s);
+    hipLaunchKernelGGL((linear_chunk_kernel<E, DA, DB, NC, false>), dim3(groups * job.segs.R), block, 0, stream, job);
     return hipGetLastError();
 }
 
-template <typename E, typename O, int DA>
-static hipError_t launch_pass_a(const LinearPass& p, void* ws, hipStream_t stream) {
-    switch (p.db) {
-        case 32: return launch_pass_d<E, O, DA, 32>(p, ws, stream);
-        case 64: return launch_pass_d<E, O, DA, 64>(p, ws, stream);
-        default: return launch_pass_d<E, O, DA, 128>(p, ws, stream);
+// 128 columns as eight waves of one tile or four of two: eight hide a chunk's
+// latencies better (B1 H32 T1024 bf16 30 against 34 us), four form the pair
+// weights half as often, which counts where every CU has work throughout (B8
+// H32 T8192 519 against 492 us, gradients of B1 H32 T4096 165 against 151).
+template <typename E, int DA, int DB>
+static hipError_t launch_job_d(const LinearJob& job, int passes, hipStream_t stream) {
+    if constexpr (DB == 128) {
+        if ((long long)job.pass[0].B * job.pass[0].H * passes >= 96) return launch_job_n<E, DA, DB, 2>(job, passes, stream);
+    }
+    return launch_job_n<E, DA, DB, 1>(job, passes, stream);
+}
+
+template <typename E, int DA>
+static hipError_t launch_job_a(const LinearJob& job, int passes, hipStream_t stream) {
+    switch (job.pass[0].db) {
+        case 32: return launch_job_d<E, DA, 32>(job, passes, stream);
+        case 64: return launch_job_d<E, DA, 64>(job, passes, stream);
+        default: return launch_job_d<E, DA, 128>(job, passes, stream);
     }
 }
 
-template <typename E, typename O>
-static hipError_t launch_pass_e(const LinearPass& p, void* ws, hipStream_t stream) {
-    switch (p.da) {
-        case 32: return launch_pass_a<E, O, 32>(p, ws, stream);
-        case 64: return launch_pass_a<E, O, 64>(p, ws, stream);
-        default: return launch_pass_a<E, O, 128>(p, ws, stream);
+template <typename E>
+static hipError_t launch_job_e(const LinearJob& job, int passes, hipStream_t stream) {
+    switch (job.pass[0].da) {
+        case 32: return launch_job_a<E, 32>(job, passes, stream);
+        case 64: return launch_job_a<E, 64>(job, passes, stream);
+        default: return launch_job_a<E, 128>(job, passes, stream);
     }
 }
 
-static hipError_t launch_pass(const LinearPass& p, void* ws, hipStream_t stream) {
-    if (!p.is_bf16) return launch_pass_e<float, float>(p, ws, stream);
-    return p.out_f32 ? launch_pass_e<bf16, float>(p, ws, stream) : launch_pass_e<bf16, bf16>(p, ws, stream);
+static hipError_t launch_job(const LinearJob& job, int passes, hipStream_t stream) {
+    return job.pass[0].is_bf16 ? launch_job_e<bf16>(job, passes, stream) : launch_job_e<float>(job, passes, stream);
+}
+
+size_t linear_prefill_ws_bytes(int B, int T, int H, int da, int db, bool is_bf16) {
+    return segs_bytes(1, B, T, H, da, db, is_bf16);
 }
 
 hipError_t launch_linear_prefill(const LinearPass& p, void* ws, hipStream_t stream) {
-    return launch_pass(p, ws, stream);
+    return launch_job(LinearJob{{p}, {(float*)ws}, segments(1, p.B, p.T, p.H, p.da, p.db, p.is_bf16)}, 1, stream);
 }
 
-// The segments' states, then (shared heads) dq or dk of every head in fp32,
-// summed afterwards.
+// The three passes' segment states, then (shared heads) dq and dk of every
+// head in fp32, summed afterwards.
 size_t linear_backward_ws_bytes(int B, int T, int H, int Hk, int dk, int dv, bool is_bf16) {
-    return linear_prefill_ws_bytes(B, T, H, dk, dv, is_bf16) +
-           (H == Hk ? 0 : (size_t)B * T * H * dk * sizeof(float));
-}
-
-static hipError_t launch_share(const LinearBackward& a, const float* src, void* dst, hipStream_t stream) {
-    const size_t count = (size_t)a.B * a.T * a.Hk * a.dk_;
-    const dim3 grid((unsigned)std::min<size_t>((count + 255) / 256, 1 << 14));
-    if (a.is_bf16)
-        hipLaunchKernelGGL((linear_share_kernel<bf16>), grid, dim3(256), 0, stream, src, (bf16*)dst, a.lens, a.T,
-                           a.Hk, a.H / a.Hk, a.dk_, count);
-    else
-        hipLaunchKernelGGL((linear_share_kernel<float>), grid, dim3(256), 0, stream, src, (float*)dst, a.lens, a.T,
-                           a.Hk, a.H / a.Hk, a.dk_, count);
-    return hipGetLastError();
+    return 3 * segs_bytes(3, B, T, H, dk, dv, is_bf16) + (H == Hk ? 0 : 2 * (size_t)B * T * H * dk * sizeof(float));
 }
 
 hipError_t launch_linear_backward(const LinearBackward& a, void* ws, hipStream_t stream) {
     const bool shared = a.H != a.Hk;
     const int n = shared ? a.H : a.Hk;
-    float* part = (float*)((char*)ws + linear_prefill_ws_bytes(a.B, a.T, a.H, a.dk_, a.dv_, a.is_bf16));
-    LinearPass dq{{a.dO, a.H}, {a.v, a.H}, {a.k, a.Hk}, shared ? part : a.dq, n, shared, a.g, a.scale, 1.0f,
-                  dense_state(a.S0, nullptr), true, a.lens, false, a.B, a.T, a.H, a.dv_, a.dk_, a.is_bf16};
-    LinearPass dv{{a.k, a.Hk}, {a.q, a.Hk}, {a.dO, a.H}, a.dv, a.H, false, a.g, 1.0f, a.scale,
-                  dense_state(a.dST, a.dS0), false, a.lens, true, a.B, a.T, a.H, a.dk_, a.dv_, a.is_bf16};
-    LinearPass dk{{a.v, a.H}, {a.dO, a.H}, {a.q, a.Hk}, shared ? part : a.dk, n, shared, a.g, 1.0f, a.scale,
-                  dense_state(a.dST, nullptr), true, a.lens, true, a.B, a.T, a.H, a.dv_, a.dk_, a.is_bf16};
+    const size_t seg_bytes = segs_bytes(3, a.B, a.T, a.H, a.dk_, a.dv_, a.is_bf16);
+    float* seg[3];
+    for (int i = 0; i < 3; ++i) seg[i] = (float*)((char*)ws + i * seg_bytes);
+    float* part = (float*)((char*)ws + 3 * seg_bytes);
+    const size_t rows = (size_t)a.B * a.T;
+    const LinearPass dq{{a.dO, a.H}, {a.v, a.H}, {a.k, a.Hk}, shared ? part : a.dq, n, shared || !a.is_bf16, a.g,
+                        a.scale, 1.0f, dense_state(a.S0, nullptr), true, a.lens, false, a.B, a.T, a.H, a.dv_, a.dk_,
+                        a.is_bf16};
+    const LinearPass dk{{a.v, a.H}, {a.dO, a.H}, {a.q, a.Hk}, shared ? part + rows * a.H * a.dk_ : a.dk, n,
+                        shared || !a.is_bf16, a.g, 1.0f, a.scale, dense_state(a.dST, nullptr), true, a.lens, true,
+                        a.B, a.T, a.H, a.dv_, a.dk_, a.is_bf16};
+    const LinearPass dv{{a.k, a.Hk}, {a.q, a.Hk}, {a.dO, a.H}, a.dv, a.H, !a.is_bf16, a.g, 1.0f, a.scale,
+                        dense_state(a.dST, a.dS0), false, a.lens, true, a.B, a.T, a.H, a.dk_, a.dv_, a.is_bf16};
+    const LinearSegs segs = segments(3, a.B, a.T, a.H, a.dk_, a.dv_, a.is_bf16);
     hipError_t e;
-    if ((e = launch_pass(dq, ws, stream)) != hipSuccess) return e;
-    if (shared && (e = launch_share(a, part, a.dq, stream)) != hipSuccess) return e;
-    if ((e = launch_pass(dv, ws, stream)) != hipSuccess) return e;
-    if ((e = launch_pass(dk, ws, stream)) != hipSuccess) return e;
-    if (shared && (e = launch_share(a, part, a.dk, stream)) != hipSuccess) return e;
-    return hipSuccess;
+    if (a.dk_ == a.dv_) {                                    // one launch for the three
+        if ((e = launch_job(LinearJob{{dq, dk, dv}, {seg[0], seg[1], seg[2]}, segs}, 3, stream)) != hipSuccess) return e;
+    } else {
+        if ((e = launch_job(LinearJob{{dq, dk}, {seg[0], seg[1]}, segs}, 2, stream)) != hipSuccess) return e;
+        if ((e = launch_job(LinearJob{{dv}, {seg[2]}, segs}, 1, stream)) != hipSuccess) return e;
+    }
+    if (!shared) return hipSuccess;
+    const size_t count = rows * a.Hk * a.dk_;
+    const dim3 grid((unsigned)std::min<size_t>((2 * count + 255) / 256, 1 << 14));
+    if (a.is_bf16)
+        hipLaunchKernelGGL((linear_share_kernel<bf16>), grid, dim3(256), 0, stream, part, (bf16*)a.dq, (bf16*)a.dk,
+                           a.lens, a.T, a.Hk, a.H / a.Hk, a.dk_, count);
+    else
+        hipLaunchKernelGGL((linear_share_kernel<float>), grid, dim3(256), 0, stream, part, (float*)a.dq, (float*)a.dk,
+                           a.lens, a.T, a.Hk, a.H / a.Hk, a.dk_, count);
+    return hipGetLastError();
 }
 
 }  // namespace kda

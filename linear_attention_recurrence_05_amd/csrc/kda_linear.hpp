@@ -29,8 +29,7 @@ struct HeadTensor {
 //   reverse:  M <- M + su y_t u_t^T,    out_t = so M^T x_t,  M <- a M
 // x, y have rows of da elements, u and out of db.  M starts from the state
 // `S.in` (null: zero), read transposed if in_t, and ends in `S.out`.
-// out is of the inputs' element type, or fp32 if out_f32 (and then has H
-// heads).
+// out is of the inputs' element type, or fp32 if out_f32.
 struct LinearPass {
     HeadTensor x, y, u;
     void* out;

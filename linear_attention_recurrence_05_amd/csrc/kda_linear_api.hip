@@ -123,7 +123,7 @@ kda_status prefill(const char* where, const void* q, const void* k, const void* 
                      {"S_T", S_T, n.state * 4, 16, false, true, S0},
                      {"workspace", ws, need, 16, need > 0, true, nullptr}};
     if ((s = check_call(r, 12)) != KDA_OK || (s = check_workspace(ws_bytes, need)) != KDA_OK) return s;
-    const kda::LinearPass p{{q, H_k}, {k, H_k}, {v, H}, o, H, false, g, scale, 1.0f,
+    const kda::LinearPass p{{q, H_k}, {k, H_k}, {v, H}, o, H, dt == KDA_F32, g, scale, 1.0f,
                             paged ? pool_state(pool, n_slots, slots_in, slots_out)
                                   : kda::dense_state(S0, S_T),
                             false, lens, false, B, T, H, d_k, d_v, dt == KDA_BF16};

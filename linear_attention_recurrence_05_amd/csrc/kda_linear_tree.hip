@@ -4,9 +4,11 @@
 // With n_i the nodes from the state S to node i, i included, the state after
 // i is a^{n_i} S + sum over j on the path of a^{n_i - n_j} k_j v_j^T, so
 //   o_i = scale (a^{n_i} S^T q_i + sum_j a^{n_i - n_j} (q_i . k_j) v_j):
-// S is read once for all nodes and no state of a node is ever formed.
+// S is read once for all nodes and no state of a node is ever formed.  Both
+// kernels are bound by that one pass over S (and the commit's write).
 #include "kda_device.hpp"
 #include "kda_linear.hpp"
+#include "kda_linear_frag.hpp"
 
 namespace kda {
 
@@ -18,7 +20,7 @@ constexpr int kTree = 64;   // KDA_MAX_TREE_TOKENS: one lane of a wave per node
 // cover 64 nodes.  Called by one whole wave.
 __device__ __forceinline__ uint64_t tree_path(const int* __restrict__ parent, int T) {
     const int lane = lane_id();
-    int up = lane < T ? parent[lane] : -2;
+    const int up = lane < T ? parent[lane] : -2;
     bool bad = up < -1 || up >= lane;         // absent: no earlier node
     uint64_t set = 1ull << lane;
     int top = bad ? -1 : up;                  // the next node above the set (-1: S)
@@ -37,87 +39,190 @@ __device__ __forceinline__ uint64_t tree_path(const int* __restrict__ parent, in
     return bad ? 0 : set;
 }
 
-// One workgroup per (b, h), a thread per value column; node by node.
-template <typename E, int DK, int DV>
-__global__ __launch_bounds__(DV < 64 ? 64 : DV) void linear_tree_kernel(LinearTree p) {
-    constexpr int NT = DV < 64 ? 64 : DV;
-    __shared__ uint64_t s_path[kTree];
-    __shared__ float s_q[DK], s_w[kTree];
-    const int b = blockIdx.x / p.H, h = blockIdx.x % p.H, c = threadIdx.x;
+// One workgroup per (b, h), one wave per 16 value columns.  A wave's slab of S
+// is the operand of S^T q straight from its loads (rounded once to E); q, k
+// and v of the nodes lie in LDS, rows of absent nodes as zeros (they may hold
+// anything).  The weights of 32 keys for 16 queries are formed transposed by
+// every wave, so that they are the operand of the product with v as they are.
+// TN: nodes rounded up to 32 (the LDS taken).
+template <typename E, int DK, int DV, int TN>
+__global__ __launch_bounds__(DV * 4, 2) void linear_tree_kernel(LinearTree p) {
+    constexpr int NT = DV * 4, KM = DK / 32, PE = 16 / sizeof(E);
+    constexpr int LK = DK + PE, LV = DV + PE;                 // padded LDS rows
+    constexpr int PK = TN * DK / PE, PV = TN * DV / PE;       // 16-byte pieces
+    constexpr int RK = (PK + NT - 1) / NT, RV = (PV + NT - 1) / NT;
+    __shared__ __align__(16) E s_q[TN * LK], s_k[TN * LK], s_v[TN * LV];
+    __shared__ __align__(16) float s_n[TN];
+    const int b = blockIdx.x / p.H, h = blockIdx.x % p.H;
     if (p.S.skip(b)) return;
-    const int hk = h / (p.H / p.Hk);
-    const float g = log_decay(p.g[h]);
-    if (c < kWave) s_path[c] = tree_path(p.parent + (size_t)b * p.T, p.T);
-    const float* S = p.S.in + ((size_t)(p.S.in_slot ? p.S.in_slot[b] : b) * p.H + h) * DK * DV;
-    for (int i = 0; i < p.T; ++i) {
-        const size_t tok = (size_t)b * p.T + i;
-        __syncthreads();
-        for (int e = c; e < DK; e += NT) s_q[e] = to_f32(((const E*)p.q)[(tok * p.Hk + hk) * DK + e]);
-        __syncthreads();
-        const uint64_t path = s_path[i];
-        if (c < kTree) {
-            float w = 0.f;
-            if (path >> c & 1) {
-                for (int e = 0; e < DK; ++e)
-                    w += s_q[e] * to_f32(((const E*)p.k)[(((size_t)b * p.T + c) * p.Hk + hk) * DK + e]);
-                w *= expf(g * (float)(__popcll(path) - __popcll(s_path[c])));
+    const int tid = threadIdx.x, wave = wave_id(), lane = lane_id(), j = lane & 15, g = lane >> 4;
+    const int hk = h / (p.H / p.Hk), T = p.T, col = wave * 16 + j;
+
+    const float* S = p.S.in + ((size_t)(p.S.in_slot ? p.S.in_slot[b] : b) * p.H + h) * (DK * DV);
+    float st[KM][8];
+#pragma unroll
+    for (int m = 0; m < KM; ++m)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) st[m][i] = __builtin_nontemporal_load(&S[(32 * m + 8 * g + i) * DV + col]);
+    const size_t t0 = (size_t)b * T;
+    const uint64_t path = tree_path(p.parent + t0, T);        // of node `lane`
+    const uint64_t live = __ballot(path != 0);
+    {
+        u32x4 rq[RK], rk[RK], rv[RV];
+        const u32x4 none = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < RK; ++i) {
+            const int at = tid + i * NT, row = at / (DK / PE), e = at % (DK / PE) * PE;
+            const bool in = at < PK && row < T;
+            const size_t off = ((t0 + (in ? row : 0)) * p.Hk + hk) * DK + e;
+            rq[i] = *reinterpret_cast<const u32x4*>((const E*)p.q + off);
+            rk[i] = *reinterpret_cast<const u32x4*>((const E*)p.k + off);
+        }
+#pragma unroll
+        for (int i = 0; i < RV; ++i) {
+            const int at = tid + i * NT, row = at / (DV / PE), e = at % (DV / PE) * PE;
+            const bool in = at < PV && row < T;
+            rv[i] = *reinterpret_cast<const u32x4*>((const E*)p.v + ((t0 + (in ? row : 0)) * p.H + h) * DV + e);
+        }
+#pragma unroll
+        for (int i = 0; i < RK; ++i) {
+            const int at = tid + i * NT, row = at / (DK / PE), e = at % (DK / PE) * PE;
+            if (PK % NT == 0 || at < PK) {
+                const bool in = live >> row & 1;
+                *reinterpret_cast<u32x4*>(&s_q[row * LK + e]) = in ? rq[i] : none;
+                *reinterpret_cast<u32x4*>(&s_k[row * LK + e]) = in ? rk[i] : none;
             }
-            s_w[c] = w;
         }
-        __syncthreads();
-        if (c >= DV) continue;
-        float o = 0.f;
-        if (path) {
-            for (int e = 0; e < DK; ++e) o += s_q[e] * S[e * DV + c];
-            o *= expf(g * (float)__popcll(path));
-            for (int j = 0; j <= i; ++j)
-                if (path >> j & 1)
-                    o += s_w[j] * to_f32(((const E*)p.v)[(((size_t)b * p.T + j) * p.H + h) * DV + c]);
+#pragma unroll
+        for (int i = 0; i < RV; ++i) {
+            const int at = tid + i * NT, row = at / (DV / PE), e = at % (DV / PE) * PE;
+            if (PV % NT == 0 || at < PV) *reinterpret_cast<u32x4*>(&s_v[row * LV + e]) = live >> row & 1 ? rv[i] : none;
         }
-        ((E*)p.o)[(tok * p.H + h) * DV + c] = from_f32<E>(p.scale * o);
+    }
+    if (wave == 0 && lane < TN) s_n[lane] = (float)__popcll(path);
+    __syncthreads();
+
+    const float lg = log_decay(p.g[h]);
+    Frag<E> sf[KM];
+#pragma unroll
+    for (int m = 0; m < KM; ++m)
+        sf[m] = to_frag<E>(f32x4{st[m][0], st[m][1], st[m][2], st[m][3]}, f32x4{st[m][4], st[m][5], st[m][6], st[m][7]});
+    for (int qt = 0; qt * 16 < T; ++qt) {                     // 16 queries: lane j has query 16 qt + j
+        const int q = 16 * qt + j;
+        const float nq = s_n[q];
+        const uint32_t path_lo = __shfl((uint32_t)path, q), path_hi = __shfl((uint32_t)(path >> 32), q);
+        Frag<E> x[KM];
+        f32x4 o = zero4();
+#pragma unroll
+        for (int m = 0; m < KM; ++m) {
+            x[m] = row_frag<E>(&s_q[q * LK + 32 * m + 8 * g]);
+            o = mma(sf[m], x[m], o);
+        }
+        o *= p.scale * expf(lg * nq);
+#pragma unroll
+        for (int kb = 0; kb < TN / 32; ++kb) {                // 32 keys
+            if (2 * kb > qt) break;
+            const uint32_t bits = kb ? path_hi : path_lo;
+            f32x4 w[2];
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt) {
+                w[kt] = zero4();
+                if (2 * kb + kt > qt) continue;               // keys behind the queries
+#pragma unroll
+                for (int m = 0; m < KM; ++m)
+                    w[kt] = mma(row_frag<E>(&s_k[(32 * kb + 16 * kt + j) * LK + 32 * m + 8 * g]), x[m], w[kt]);
+                const f32x4 nk = *reinterpret_cast<const f32x4*>(&s_n[32 * kb + 16 * kt + 4 * g]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w[kt][i] = bits >> (16 * kt + 4 * g + i) & 1 ? w[kt][i] * (p.scale * expf(lg * (nq - nk[i]))) : 0.f;
+            }
+            // the weights rounded once to E
+            o = mma(col_frag<E>(&s_v[32 * kb * LV], LV, wave * 16, 4, j, g), to_frag<E>(w[0], w[1]), o);
+        }
+        if (q < T) {
+            if (nq == 0.f) o = zero4();
+            E* dst = (E*)p.o + ((t0 + q) * p.H + h) * DV + wave * 16 + 4 * g;
+            if constexpr (sizeof(E) == 2)
+                *reinterpret_cast<bf16x4*>(dst) = pack4(o);
+            else
+                *reinterpret_cast<f32x4*>(dst) = o;
+        }
     }
 }
 
+// One workgroup per (b, h); a thread holds 4 columns of RPT rows of S, read
+// before the path is known.  The path's k (weighted) and v pass through LDS in
+// blocks of kPathBlock nodes.
+constexpr int kPathBlock = 16;
 template <typename E, int DK, int DV>
-__global__ __launch_bounds__(256) void linear_commit_kernel(LinearTree p) {
-    constexpr int CG = DV / 4, RG = 256 / CG;
-    __shared__ uint64_t s_path[kTree];
+__global__ __launch_bounds__(DK * DV / 32 < 64 ? 64 : DK * DV / 32) void linear_commit_kernel(LinearTree p) {
+    constexpr int NT = DK * DV / 32 < 64 ? 64 : DK * DV / 32;
+    constexpr int CG = DV / 4, RG = NT / CG, RPT = DK / RG;
+    __shared__ __align__(16) float s_k[kPathBlock][DK], s_v[kPathBlock][DV];
+    __shared__ int s_node[kTree];                             // the path's nodes in order
     const int b = blockIdx.x / p.H, h = blockIdx.x % p.H, tid = threadIdx.x;
     if (p.S.skip(b)) return;
-    const int x = p.accepted[b];
+    const int cg = tid % CG, rg = tid / CG, hk = h / (p.H / p.Hk), x = p.accepted[b];
     if (x < -1 || x >= p.T) return;
-    const int hk = h / (p.H / p.Hk);
-    const float g = log_decay(p.g[h]);
-    if (tid < kWave) s_path[tid] = tree_path(p.parent + (size_t)b * p.T, p.T);
-    __syncthreads();
-    const uint64_t path = x < 0 ? 0 : s_path[x];
-    if (x >= 0 && path == 0) return;
-    const int n = __popcll(path), cg = tid % CG, rg = tid / CG;
-    const f32x4* S = (const f32x4*)(p.S.in + ((size_t)(p.S.in_slot ? p.S.in_slot[b] : b) * p.H + h) * DK * DV);
-    f32x4* So = (f32x4*)(p.S.out + ((size_t)(p.S.out_slot ? p.S.out_slot[b] : b) * p.H + h) * DK * DV);
-    const float an = expf(g * (float)n);
-    for (int c = rg; c < DK; c += RG) {
-        f32x4 s = S[c * CG + cg];
-        if (n) s *= an;
-        for (uint64_t rest = path; rest; rest &= rest - 1) {
-            const int j = __ffsll((unsigned long long)rest) - 1;
-            const size_t tok = (size_t)b * p.T + j;
-            const float kj = to_f32(((const E*)p.k)[(tok * p.Hk + hk) * DK + c]) *
-                             expf(g * (float)(n - __popcll(s_path[j])));
-            for (int e = 0; e < 4; ++e)
-                s[e] += kj * to_f32(((const E*)p.v)[(tok * p.H + h) * DV + 4 * cg + e]);
-        }
-        So[c * CG + cg] = s;
+    const f32x4* S = (const f32x4*)(p.S.in + ((size_t)(p.S.in_slot ? p.S.in_slot[b] : b) * p.H + h) * (DK * DV));
+    f32x4* So = (f32x4*)(p.S.out + ((size_t)(p.S.out_slot ? p.S.out_slot[b] : b) * p.H + h) * (DK * DV));
+    f32x4 st[RPT];
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) st[i] = __builtin_nontemporal_load(&S[(rg + RG * i) * CG + cg]);
+    // every wave finds the path by itself
+    const size_t t0 = (size_t)b * p.T;
+    const uint64_t all = tree_path(p.parent + t0, p.T);
+    const int from = x < 0 ? 0 : x;
+    const uint64_t found = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(all >> 32), from) << 32) |
+                    (uint32_t)__builtin_amdgcn_readlane((int)all, from);
+    const uint64_t path = x < 0 ? 0 : found;
+    if (x >= 0 && path == 0) return;                          // absent (uniform over the workgroup)
+    const int n = __popcll(path);
+    const float lg = log_decay(p.g[h]);
+    if (n > 0) {
+        const float an = expf(lg * (float)n);
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) st[i] *= an;
     }
+    const int me = lane_id();
+    if (wave_id() == 0 && (path >> me & 1)) s_node[__popcll(path & ((1ull << me) - 1))] = me;
+    constexpr int PE = 16 / sizeof(E), PR = (DK + DV) / PE;   // 16-byte pieces of a node's k and v
+    for (int n0 = 0; n0 < n; n0 += kPathBlock) {
+        const int nb = min(kPathBlock, n - n0);
+        __syncthreads();
+        for (int at = tid; at < nb * PR; at += NT) {
+            const int s = at / PR, e = at % PR * PE, node = s_node[n0 + s];
+            const bool isk = e < DK;
+            const E* src = isk ? (const E*)p.k + ((t0 + node) * p.Hk + hk) * DK + e
+                               : (const E*)p.v + ((t0 + node) * p.H + h) * DV + e - DK;
+            float* dst = isk ? &s_k[s][e] : &s_v[s][e - DK];
+            const float w = isk ? expf(lg * (float)(n - 1 - n0 - s)) : 1.0f;
+            E x[PE];
+            *reinterpret_cast<u32x4*>(x) = *reinterpret_cast<const u32x4*>(src);
+#pragma unroll
+            for (int i = 0; i < PE; ++i) dst[i] = w * to_f32(x[i]);
+        }
+        __syncthreads();
+        for (int s = 0; s < nb; ++s) {
+            const f32x4 v = *reinterpret_cast<const f32x4*>(&s_v[s][4 * cg]);
+#pragma unroll
+            for (int i = 0; i < RPT; ++i) st[i] += s_k[s][rg + RG * i] * v;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) __builtin_nontemporal_store(st[i], &So[(rg + RG * i) * CG + cg]);
 }
 
 template <typename E, int DK, int DV>
 static hipError_t launch_kv(const LinearTree& a, bool commit, hipStream_t stream) {
+    constexpr int NT = DK * DV / 32 < 64 ? 64 : DK * DV / 32;
     const dim3 grid((unsigned)(a.B * a.H));
     if (commit)
-        hipLaunchKernelGGL((linear_commit_kernel<E, DK, DV>), grid, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((linear_commit_kernel<E, DK, DV>), grid, dim3(NT), 0, stream, a);
+    else if (a.T <= 32)
+        hipLaunchKernelGGL((linear_tree_kernel<E, DK, DV, 32>), grid, dim3(DV * 4), 0, stream, a);
     else
-        hipLaunchKernelGGL((linear_tree_kernel<E, DK, DV>), grid, dim3(DV < 64 ? 64 : DV), 0, stream, a);
+        hipLaunchKernelGGL((linear_tree_kernel<E, DK, DV, 64>), grid, dim3(DV * 4), 0, stream, a);
     return hipGetLastError();
 }
 
