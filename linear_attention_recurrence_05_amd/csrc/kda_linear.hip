@@ -26,20 +26,6 @@ namespace kda {
 
 constexpr int kLinChunk = 32;
 
-// x in fp32 as a sum of bf16 terms: three hold its 24 bits, so a product with
-// a bf16 operand keeps fp32's accuracy.
-__device__ __forceinline__ void split(f32x4 lo, f32x4 hi, Frag<bf16> (&out)[3]) {
-#pragma unroll
-    for (int s = 0; s < 3; ++s) {
-        out[s] = to_frag<bf16>(lo, hi);
-        f32x4 a, b;
-        to_f32(out[s], a, b);
-        lo -= a;
-        hi -= b;
-    }
-}
-__device__ __forceinline__ void split(f32x4 lo, f32x4 hi, Frag<float> (&out)[1]) { out[0] = {lo, hi}; }
-
 // ------------------------------------------------------------------ the pass
 
 // Segments of a sequence run side by side: a first launch leaves in the
@@ -66,8 +52,10 @@ struct LinearJob {
 // one barrier a chunk, the chunk after the next in flight in registers).  The
 // pair weights are computed transposed (keys x queries) by every wave, which
 // makes the product with u take them straight from the accumulators.
-// STATE: only the state of a segment from zero, into the workspace.
-template <typename E, int DA, int DB, int NC, bool STATE>
+// NP: terms of E that the state and the pair weights are split into for their
+// products with x and u (see launch_job_d).  STATE: only the state of a segment
+// from zero, into the workspace.
+template <typename E, int DA, int DB, int NC, int NP, bool STATE>
 __global__ __launch_bounds__(DB / NC * 4, 2) void linear_chunk_kernel(LinearJob job) {
     constexpr int C = kLinChunk, NT = DB / NC * 4, KM = DA / 32, NS = sizeof(E) == 2 ? 3 : 1;
     constexpr int PE = 16 / sizeof(E);                       // elements of 16 bytes
@@ -271,10 +259,13 @@ __global__ __launch_bounds__(DB / NC * 4, 2) void linear_chunk_kernel(LinearJob 
                 p11 = mma(y1, x1, p11);
 #pragma unroll
                 for (int ct = 0; ct < NC; ++ct) {
-                    // the state rounded once to E for its product with x
-                    const Frag<E> mf = to_frag<E>(M[2 * m][ct], M[2 * m + 1][ct]);
-                    o[ct][0] = mma(mf, x0, o[ct][0]);
-                    o[ct][1] = mma(mf, x1, o[ct][1]);
+                    Frag<E> mf[NP];
+                    split(M[2 * m][ct], M[2 * m + 1][ct], mf);
+#pragma unroll
+                    for (int i = 0; i < NP; ++i) {
+                        o[ct][0] = mma(mf[i], x0, o[ct][0]);
+                        o[ct][1] = mma(mf[i], x1, o[ct][1]);
+                    }
                 }
             }
 #pragma unroll
@@ -283,14 +274,20 @@ __global__ __launch_bounds__(DB / NC * 4, 2) void linear_chunk_kernel(LinearJob 
                 p01[i] *= wo[i];
                 p11[i] *= wd[i];
             }
-            // the pair weights rounded once to E for their product with u
-            const Frag<E> w0 = to_frag<E>(p00, zero4()), w1 = to_frag<E>(p01, p11);
+            Frag<E> w0[NP], w1[NP];
+            split(p00, zero4(), w0);
+            split(p01, p11, w1);
             const Rsrc out = make_rsrc(Out.base, Out.bytes);
             Out.base += Out.step;
 #pragma unroll
             for (int ct = 0; ct < NC; ++ct) {
-                o[ct][0] = mma(uf[ct], w0, wi[0] * o[ct][0]);
-                o[ct][1] = mma(uf[ct], w1, wi[1] * o[ct][1]);
+                o[ct][0] *= wi[0];
+                o[ct][1] *= wi[1];
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    o[ct][0] = mma(uf[ct], w0[i], o[ct][0]);
+                    o[ct][1] = mma(uf[ct], w1[i], o[ct][1]);
+                }
             }
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -308,6 +305,7 @@ __global__ __launch_bounds__(DB / NC * 4, 2) void linear_chunk_kernel(LinearJob 
                 }
             }
         }
+        // the weighted u in three bf16 terms: the state keeps fp32's accuracy
         Frag<E> us[NC][NS];
 #pragma unroll
         for (int ct = 0; ct < NC; ++ct) {
@@ -421,17 +419,17 @@ static size_t segs_bytes(int passes, int B, int T, int H, int da, int db, bool i
     return R > 1 ? (size_t)B * H * R * da * db * sizeof(float) : 0;
 }
 
-template <typename E, int DA, int DB, int NC>
+template <typename E, int DA, int DB, int NC, int NP>
 static hipError_t launch_job_n(const LinearJob& job, int passes, hipStream_t stream) {
     const unsigned groups = (unsigned)(job.pass[0].B * job.pass[0].H) * passes;
     const dim3 block(DB / NC * 4);
     if (job.segs.R > 1) {
-        hipLaunchKernelGGL((linear_chunk_kernel<E, DA, DB, NC, true>), dim3(groups * (job.segs.R - 1)), block, 0, stream,
+        hipLaunchKernelGGL((linear_chunk_kernel<E, DA, DB, NC, 1, true>), dim3(groups * (job.segs.R - 1)), block, 0, stream,
                            job);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((linear_chunk_kernel<E, DA, DB, NC, false>), dim3(groups * job.segs.R), block, 0, stream, job);
+    hipLaunchKernelGGL((linear_chunk_kernel<E, DA, DB, NC, NP, false>), dim3(groups * job.segs.R), block, 0, stream, job);
     return hipGetLastError();
 }
 
@@ -439,12 +437,21 @@ static hipError_t launch_job_n(const LinearJob& job, int passes, hipStream_t str
 // latencies better (B1 H32 T1024 bf16 30 against 34 us), four form the pair
 // weights half as often, which counts where every CU has work throughout (B8
 // H32 T8192 519 against 492 us, gradients of B1 H32 T4096 165 against 151).
+// bf16: the state and the pair weights enter their products as one bf16 term
+// each, which leaves half a step of bf16 on each part of the output's sum
+// beside its own rounding.  A second term removes that and costs a fifth of a
+// chunk's arithmetic, which only a pass of a few chunks, latency for the most
+// part, has to spare.
 template <typename E, int DA, int DB>
 static hipError_t launch_job_d(const LinearJob& job, int passes, hipStream_t stream) {
     if constexpr (DB == 128) {
-        if ((long long)job.pass[0].B * job.pass[0].H * passes >= 96) return launch_job_n<E, DA, DB, 2>(job, passes, stream);
+        if ((long long)job.pass[0].B * job.pass[0].H * passes >= 96)
+            return launch_job_n<E, DA, DB, 2, 1>(job, passes, stream);
     }
-    return launch_job_n<E, DA, DB, 1>(job, passes, stream);
+    if constexpr (sizeof(E) == 2) {
+        if (job.segs.len <= 4 * kLinChunk) return launch_job_n<E, DA, DB, 1, 2>(job, passes, stream);
+    }
+    return launch_job_n<E, DA, DB, 1, 1>(job, passes, stream);
 }
 
 template <typename E, int DA>

@@ -74,4 +74,19 @@ __device__ __forceinline__ Frag<E> col_frag(const E* s, int ld, int c0, int step
     return f;
 }
 
+// x in fp32 as a sum of N terms of E: two bf16 hold 16 of its bits, three all 24,
+// so a product with a bf16 operand keeps that accuracy; one fp32 is x itself.
+template <int N>
+__device__ __forceinline__ void split(f32x4 lo, f32x4 hi, Frag<bf16> (&out)[N]) {
+#pragma unroll
+    for (int s = 0; s < N; ++s) {
+        out[s] = to_frag<bf16>(lo, hi);
+        f32x4 a, b;
+        to_f32(out[s], a, b);
+        lo -= a;
+        hi -= b;
+    }
+}
+__device__ __forceinline__ void split(f32x4 lo, f32x4 hi, Frag<float> (&out)[1]) { out[0] = {lo, hi}; }
+
 }  // namespace kda

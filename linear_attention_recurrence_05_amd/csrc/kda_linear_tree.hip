@@ -40,12 +40,16 @@ __device__ __forceinline__ uint64_t tree_path(const int* __restrict__ parent, in
 }
 
 // One workgroup per (b, h), one wave per 16 value columns.  A wave's slab of S
-// is the operand of S^T q straight from its loads (rounded once to E); q, k
+// is the operand of S^T q straight from its loads; q, k
 // and v of the nodes lie in LDS, rows of absent nodes as zeros (they may hold
 // anything).  The weights of 32 keys for 16 queries are formed transposed by
 // every wave, so that they are the operand of the product with v as they are.
-// TN: nodes rounded up to 32 (the LDS taken).
-template <typename E, int DK, int DV, int TN>
+// TN: nodes rounded up to 32 (the LDS taken).  NS: terms of E that the state and
+// the pair weights are split into for their products.  bf16 takes two, which
+// leaves only the output's own rounding, where the device is not full anyway,
+// and one, half a bf16 step on each part of the sum, where it is (B64 H32 T64
+// with its commit: 113 against 119 us).
+template <typename E, int DK, int DV, int TN, int NS>
 __global__ __launch_bounds__(DV * 4, 2) void linear_tree_kernel(LinearTree p) {
     constexpr int NT = DV * 4, KM = DK / 32, PE = 16 / sizeof(E);
     constexpr int LK = DK + PE, LV = DV + PE;                 // padded LDS rows
@@ -63,7 +67,7 @@ __global__ __launch_bounds__(DV * 4, 2) void linear_tree_kernel(LinearTree p) {
 #pragma unroll
     for (int m = 0; m < KM; ++m)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) st[m][i] = __builtin_nontemporal_load(&S[(32 * m + 8 * g + i) * DV + col]);
+        for (int i = 0; i < 8; ++i) st[m][i] = S[(32 * m + 8 * g + i) * DV + col];
     const size_t t0 = (size_t)b * T;
     const uint64_t path = tree_path(p.parent + t0, T);        // of node `lane`
     const uint64_t live = __ballot(path != 0);
@@ -103,10 +107,10 @@ __global__ __launch_bounds__(DV * 4, 2) void linear_tree_kernel(LinearTree p) {
     __syncthreads();
 
     const float lg = log_decay(p.g[h]);
-    Frag<E> sf[KM];
+    Frag<E> sf[KM][NS];
 #pragma unroll
     for (int m = 0; m < KM; ++m)
-        sf[m] = to_frag<E>(f32x4{st[m][0], st[m][1], st[m][2], st[m][3]}, f32x4{st[m][4], st[m][5], st[m][6], st[m][7]});
+        split(f32x4{st[m][0], st[m][1], st[m][2], st[m][3]}, f32x4{st[m][4], st[m][5], st[m][6], st[m][7]}, sf[m]);
     for (int qt = 0; qt * 16 < T; ++qt) {                     // 16 queries: lane j has query 16 qt + j
         const int q = 16 * qt + j;
         const float nq = s_n[q];
@@ -116,7 +120,8 @@ __global__ __launch_bounds__(DV * 4, 2) void linear_tree_kernel(LinearTree p) {
 #pragma unroll
         for (int m = 0; m < KM; ++m) {
             x[m] = row_frag<E>(&s_q[q * LK + 32 * m + 8 * g]);
-            o = mma(sf[m], x[m], o);
+#pragma unroll
+            for (int s = 0; s < NS; ++s) o = mma(sf[m][s], x[m], o);
         }
         o *= p.scale * expf(lg * nq);
 #pragma unroll
@@ -136,8 +141,11 @@ __global__ __launch_bounds__(DV * 4, 2) void linear_tree_kernel(LinearTree p) {
                 for (int i = 0; i < 4; ++i)
                     w[kt][i] = bits >> (16 * kt + 4 * g + i) & 1 ? w[kt][i] * (p.scale * expf(lg * (nq - nk[i]))) : 0.f;
             }
-            // the weights rounded once to E
-            o = mma(col_frag<E>(&s_v[32 * kb * LV], LV, wave * 16, 4, j, g), to_frag<E>(w[0], w[1]), o);
+            Frag<E> wf[NS];
+            split(w[0], w[1], wf);
+            const Frag<E> vf = col_frag<E>(&s_v[32 * kb * LV], LV, wave * 16, 4, j, g);
+#pragma unroll
+            for (int s = 0; s < NS; ++s) o = mma(vf, wf[s], o);
         }
         if (q < T) {
             if (nq == 0.f) o = zero4();
@@ -213,16 +221,25 @@ __global__ __launch_bounds__(DK * DV / 32 < 64 ? 64 : DK * DV / 32) void linear_
     for (int i = 0; i < RPT; ++i) __builtin_nontemporal_store(st[i], &So[(rg + RG * i) * CG + cg]);
 }
 
+template <typename E, int DK, int DV, int NS>
+static void launch_tree(const LinearTree& a, hipStream_t stream) {
+    const dim3 grid((unsigned)(a.B * a.H)), block(DV * 4);
+    if (a.T <= 32)
+        hipLaunchKernelGGL((linear_tree_kernel<E, DK, DV, 32, NS>), grid, block, 0, stream, a);
+    else
+        hipLaunchKernelGGL((linear_tree_kernel<E, DK, DV, 64, NS>), grid, block, 0, stream, a);
+}
+
 template <typename E, int DK, int DV>
 static hipError_t launch_kv(const LinearTree& a, bool commit, hipStream_t stream) {
     constexpr int NT = DK * DV / 32 < 64 ? 64 : DK * DV / 32;
     const dim3 grid((unsigned)(a.B * a.H));
     if (commit)
         hipLaunchKernelGGL((linear_commit_kernel<E, DK, DV>), grid, dim3(NT), 0, stream, a);
-    else if (a.T <= 32)
-        hipLaunchKernelGGL((linear_tree_kernel<E, DK, DV, 32>), grid, dim3(DV * 4), 0, stream, a);
+    else if (sizeof(E) == 2 && grid.x < 512)
+        launch_tree<E, DK, DV, sizeof(E) == 2 ? 2 : 1>(a, stream);
     else
-        hipLaunchKernelGGL((linear_tree_kernel<E, DK, DV, 64>), grid, dim3(DV * 4), 0, stream, a);
+        launch_tree<E, DK, DV, 1>(a, stream);
     return hipGetLastError();
 }
 

@@ -4,9 +4,9 @@
 //   du = Rot(-angle) dy;  dw = sum du n;  dn = w du;
 //   dx = r dn - c r^3 x (x . dn)
 //
-// Bound by the one read and one write of the rows.  A workgroup takes a token
-// at a time: its cos and sin are formed once, in LDS, and serve all heads of
-// q and k.  A row lies in d / VE neighbouring lanes of 16 bytes each, so a
+// Bound by the one read and one write of the rows (4096 tokens of 32 + 32
+// heads, bf16, d 128: 26 us, 5.1 TB/s).  A workgroup takes a token at a time: its
+// cos and sin are formed once, in LDS, and serve all heads of q and k.  A row lies in d / VE neighbouring lanes of 16 bytes each, so a
 // wave reads and writes 1 KB at a time, sums within the row's lanes, and gets
 // the other element of a pair from the same lane (interleaved), from a lane
 // rot / 2 elements away (halves of whole lanes), or through LDS (any other rot).
@@ -17,8 +17,11 @@
 
 namespace kda {
 
-constexpr int kNormMaxGroups = 2048;   // workgroups of a launch (8 a CU); more tokens loop
-constexpr int kNormDwGroups = 512;     // the same where each leaves a partial weight gradient
+// Most workgroups of a launch; more tokens loop, with the next rows in flight
+// (4096 tokens of H 32 + 32, bf16, d 128: 26 us forward with 1024, 35 with 512, 28
+// with 4096; 2002 tokens of H 32 + 8 backward, each workgroup leaving a partial
+// weight gradient: 22 us with 512 to 768, 25 with 1024, 28 with 256).
+constexpr int kNormGroups = 1024, kNormBwdGroups = 768;
 
 // cos and sin of pos * f.  The product is formed and reduced to a turn in
 // 64 bits: at position 10^6 a product in fp32 would be off by 0.03 radians.
@@ -29,12 +32,12 @@ __device__ __forceinline__ void angle(int pos, float f, float& c, float& s) {
 }
 
 // How a lane gets the other elements of its pairs.
-enum class Pairs { kNone, kLane, kShuffle, kLds };
+enum class Pairs { kNone, kLane, kLaneAny, kShuffle, kLds };
 
 template <typename E, int VE>
-__device__ __forceinline__ void load_row(const E* p, float (&x)[VE]) {
+__device__ __forceinline__ void unpack(u32x4 v, float (&x)[VE]) {
     E e[VE];
-    *reinterpret_cast<u32x4*>(e) = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+    *reinterpret_cast<u32x4*>(e) = v;
 #pragma unroll
     for (int i = 0; i < VE; ++i) x[i] = to_f32(e[i]);
 }
@@ -48,10 +51,18 @@ __device__ __forceinline__ void store_row(E* p, const float (&x)[VE]) {
     __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
 }
 
+// N consecutive floats of LDS (N of 2, 4 or 8, aligned to min(N, 4) of them).
+template <int N>
+__device__ __forceinline__ void copy(float (&x)[N], const float* p) {
+    typedef float vec __attribute__((ext_vector_type(N < 4 ? N : 4)));
+#pragma unroll
+    for (int i = 0; i < N; i += N < 4 ? N : 4) *reinterpret_cast<vec*>(&x[i]) = *reinterpret_cast<const vec*>(p + i);
+}
+
 template <typename E, int D, bool BWD, Pairs PAIRS>
 __global__ __launch_bounds__(256) void norm_rope_kernel(NormRope p, float* __restrict__ part) {
     constexpr int VE = 16 / sizeof(E), LR = D / VE, RW = kWave / LR;   // lanes of a row, rows of a wave
-    __shared__ __align__(16) float s_c[D / 2], s_s[D / 2];
+    __shared__ __align__(16) float s_cos[2][D / 2], s_sin[2][D / 2];
     __shared__ __align__(16) float s_x[PAIRS == Pairs::kLds ? 256 * VE : 4];
     __shared__ float s_dw[BWD ? 2 * D * (256 / LR) : 1];
     const int tid = threadIdx.x, lr = tid % LR, e0 = lr * VE, half = p.rot / 2;
@@ -64,28 +75,56 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(NormRope p, float* __res
         dwq[i] = dwk[i] = 0.f;
     }
     const int64_t tokens = (int64_t)p.B * p.T;
-    for (int64_t tok = blockIdx.x; tok < tokens; tok += gridDim.x) {
-        if (PAIRS != Pairs::kNone) {
-            __syncthreads();                                  // the last token's angles are used
-            if (tid < half) {
-                float cs, sn;
-                angle(p.positions[tok], p.inv_freq[tid], cs, sn);
-                s_c[tid] = cs;
-                s_s[tid] = BWD ? -sn : sn;
-            }
-            __syncthreads();
+    // rows 0 .. H - 1 are q's heads, the rest k's; the rows of one wave step end
+    // at H so that a step has one weight
+    // (a scalar wave index makes the choice of q or k a branch: 2 us faster
+    // forward, 4 slower backward)
+    const int wave = BWD ? tid / kWave : wave_id(), steps_q = (p.H + RW - 1) / RW, steps = steps_q + (p.Hk + RW - 1) / RW;
+    struct Row {
+        u32x4 x, dy;
+        size_t off;
+        bool in;
+    };
+    auto fetch = [&](int64_t tok, int step) {                 // this lane's part of its row of a step
+        Row r{};
+        if (tok >= tokens || step >= steps) return r;
+        const bool isk = step >= steps_q;
+        const int head = (isk ? step - steps_q : step) * RW + tid % kWave / LR, heads = isk ? p.Hk : p.H;
+        r.in = head < heads;
+        r.off = ((size_t)tok * heads + (r.in ? head : 0)) * D + e0;
+        r.x = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>((const E*)(isk ? p.k : p.q) + r.off));
+        if (BWD) r.dy = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>((const E*)(isk ? p.dy_k : p.dy_q) + r.off));
+        return r;
+    };
+    // The last wave (whose steps are the fewest) forms the next token's angles
+    // while the others use this one's; every wave has its next step's rows in
+    // flight.
+    const bool turns = PAIRS != Pairs::kNone && wave == 3 && tid % kWave < half;
+    const float freq = turns ? p.inv_freq[tid % kWave] : 0.f;
+    auto angles = [&](int64_t tok, int buf) {
+        if (turns && tok < tokens) {
+            float cs, sn;
+            angle(p.positions[tok], freq, cs, sn);
+            s_cos[buf][tid % kWave] = cs;
+            s_sin[buf][tid % kWave] = BWD ? -sn : sn;
         }
-        // rows 0 .. H - 1 are q's heads, the rest k's; the rows of one wave step
-        // end at H so that a step has one weight
-        const int steps_q = (p.H + RW - 1) / RW, steps = steps_q + (p.Hk + RW - 1) / RW;
-        for (int step = tid / kWave; step < steps; step += 4) {
+    };
+    Row next = fetch(blockIdx.x, wave);
+    angles(blockIdx.x, 0);
+    int buf = 0;
+    for (int64_t tok = blockIdx.x; tok < tokens; tok += gridDim.x, buf ^= 1) {
+        if (PAIRS != Pairs::kNone) __syncthreads();           // this token's angles are there, the last one's used
+        angles(tok + gridDim.x, buf ^ 1);
+        const float *s_c = s_cos[buf], *s_s = s_sin[buf];
+        for (int step = wave; step < steps; step += 4) {
             const bool isk = step >= steps_q;
-            const int head = (isk ? step - steps_q : step) * RW + tid % kWave / LR, heads = isk ? p.Hk : p.H;
-            const bool in = head < heads;
-            const size_t off = ((size_t)tok * heads + (in ? head : 0)) * D + e0;
+            const Row row = next;
+            next = step + 4 < steps ? fetch(tok, step + 4) : fetch(tok + gridDim.x, wave);
+            const bool in = row.in;
+            const size_t off = row.off;
             float x[VE], u[VE];
-            load_row<E, VE>((const E*)(isk ? p.k : p.q) + off, x);
-            if (BWD) load_row<E, VE>((const E*)(isk ? p.dy_k : p.dy_q) + off, u);
+            unpack<E, VE>(row.x, x);
+            if (BWD) unpack<E, VE>(row.dy, u);
             float sum = 0.f;
 #pragma unroll
             for (int i = 0; i < VE; ++i) sum += x[i] * x[i];
@@ -96,11 +135,22 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(NormRope p, float* __res
 #pragma unroll
                 for (int i = 0; i < VE; ++i) u[i] = x[i] * r * (isk ? wk[i] : wq[i]);
             }
-            if constexpr (PAIRS == Pairs::kLane) {
+            if constexpr (PAIRS == Pairs::kLane) {            // rot is a multiple of VE
                 if (e0 < p.rot) {
+                    float cs[VE / 2], sn[VE / 2];
+                    copy<VE / 2>(cs, &s_c[e0 / 2]);
+                    copy<VE / 2>(sn, &s_s[e0 / 2]);
 #pragma unroll
                     for (int i = 0; i < VE; i += 2) {
-                        if (e0 + i >= p.rot) break;
+                        const float a = u[i], b = u[i + 1];
+                        u[i] = a * cs[i / 2] - b * sn[i / 2];
+                        u[i + 1] = b * cs[i / 2] + a * sn[i / 2];
+                    }
+                }
+            } else if constexpr (PAIRS == Pairs::kLaneAny) {
+#pragma unroll
+                for (int i = 0; i < VE; i += 2) {
+                    if (e0 + i < p.rot) {
                         const float cs = s_c[(e0 + i) / 2], sn = s_s[(e0 + i) / 2], a = u[i], b = u[i + 1];
                         u[i] = a * cs - b * sn;
                         u[i + 1] = b * cs + a * sn;
@@ -115,14 +165,16 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(NormRope p, float* __res
                     for (int i = 0; i < VE; ++i) other[i] = __shfl(u[i], from);
                     if (e0 < p.rot) {
                         const int pr = first ? e0 : e0 - half;
+                        float cs[VE], sn[VE];
+                        copy<VE>(cs, &s_c[pr]);
+                        copy<VE>(sn, &s_s[pr]);
 #pragma unroll
-                        for (int i = 0; i < VE; ++i)
-                            u[i] = u[i] * s_c[pr + i] + (first ? -other[i] : other[i]) * s_s[pr + i];
+                        for (int i = 0; i < VE; ++i) u[i] = u[i] * cs[i] + (first ? -other[i] : other[i]) * sn[i];
                     }
                 } else {                                      // within the wave's own part of LDS
-                    float* row = s_x + tid / LR * D;
+                    float* part_row = s_x + tid / LR * D;
 #pragma unroll
-                    for (int i = 0; i < VE; ++i) row[e0 + i] = u[i];
+                    for (int i = 0; i < VE; ++i) part_row[e0 + i] = u[i];
                     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
                     __builtin_amdgcn_wave_barrier();
 #pragma unroll
@@ -131,7 +183,7 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(NormRope p, float* __res
                         if (e >= p.rot) continue;
                         const bool lo = e < half;
                         const int pr = lo ? e : e - half;
-                        const float o = row[lo ? e + half : pr];
+                        const float o = part_row[lo ? e + half : pr];
                         u[i] = u[i] * s_c[pr] + (lo ? -o : o) * s_s[pr];
                     }
                     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -179,7 +231,7 @@ __global__ __launch_bounds__(256) void norm_rope_dw_kernel(const float* __restri
     __shared__ float s_t[16][17];
     const int e = blockIdx.x * 16 + threadIdx.x % 16, row = threadIdx.x / 16;
     float t = 0.f;
-#pragma unroll 4
+#pragma unroll 16
     for (int i = row; i < n; i += 16) t += part[(size_t)i * 2 * d + e];
     s_t[row][threadIdx.x % 16] = t;
     __syncthreads();
@@ -195,12 +247,13 @@ template <typename E, int D, bool BWD>
 static hipError_t launch_d(const NormRope& a, float* part, int groups, hipStream_t stream) {
     constexpr int VE = 16 / sizeof(E);
     const Pairs pairs = a.rot == 0 ? Pairs::kNone
-                        : a.interleaved ? Pairs::kLane
+                        : a.interleaved ? (a.rot % VE == 0 ? Pairs::kLane : Pairs::kLaneAny)
                         : (a.rot / 2) % VE == 0 ? Pairs::kShuffle : Pairs::kLds;
     const dim3 grid((unsigned)groups), block(256);
     switch (pairs) {
         case Pairs::kNone: hipLaunchKernelGGL((norm_rope_kernel<E, D, BWD, Pairs::kNone>), grid, block, 0, stream, a, part); break;
         case Pairs::kLane: hipLaunchKernelGGL((norm_rope_kernel<E, D, BWD, Pairs::kLane>), grid, block, 0, stream, a, part); break;
+        case Pairs::kLaneAny: hipLaunchKernelGGL((norm_rope_kernel<E, D, BWD, Pairs::kLaneAny>), grid, block, 0, stream, a, part); break;
         case Pairs::kShuffle: hipLaunchKernelGGL((norm_rope_kernel<E, D, BWD, Pairs::kShuffle>), grid, block, 0, stream, a, part); break;
         case Pairs::kLds: hipLaunchKernelGGL((norm_rope_kernel<E, D, BWD, Pairs::kLds>), grid, block, 0, stream, a, part); break;
     }
@@ -219,16 +272,16 @@ static hipError_t launch_any(const NormRope& a, float* part, int groups, hipStre
 static int norm_groups(int B, int T, int most) { return (int)std::min<int64_t>((int64_t)B * T, most); }
 
 hipError_t launch_norm_rope(const NormRope& a, hipStream_t stream) {
-    return launch_any<false>(a, nullptr, norm_groups(a.B, a.T, kNormMaxGroups), stream);
+    return launch_any<false>(a, nullptr, norm_groups(a.B, a.T, kNormGroups), stream);
 }
 
 size_t norm_rope_backward_ws_bytes(int B, int T, int H, int Hk, int d) {
-    return (size_t)norm_groups(B, T, kNormDwGroups) * 2 * d * sizeof(float);
+    return (size_t)norm_groups(B, T, kNormBwdGroups) * 2 * d * sizeof(float);
 }
 
 hipError_t launch_norm_rope_backward(const NormRope& a, void* ws, hipStream_t stream) {
     const bool dw = a.dw_q || a.dw_k;
-    const int groups = norm_groups(a.B, a.T, dw ? kNormDwGroups : kNormMaxGroups);
+    const int groups = norm_groups(a.B, a.T, kNormBwdGroups);
     hipError_t e = launch_any<true>(a, dw ? (float*)ws : nullptr, groups, stream);
     if (e != hipSuccess || !dw) return e;
     hipLaunchKernelGGL(norm_rope_dw_kernel, dim3(2 * a.d / 16), dim3(256), 0, stream, (const float*)ws, groups, a.d,
