@@ -48,6 +48,7 @@ _current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 _F32 = torch.float32
 _I32 = torch.int32
+_CODES = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}
 
 
 def _refuse(where, name, t, dev, dtype, shape):
@@ -67,31 +68,36 @@ def _refuse(where, name, t, dev, dtype, shape):
 class _Call:
     """The checks of one call's tensors against the first one's device and type."""
 
+    __slots__ = ("where", "dev", "index", "dt", "code")
+
     def __init__(self, where, ref, ndim):
         self.where = where
         if not isinstance(ref, torch.Tensor):
             raise TypeError(f"{where}: expected a torch.Tensor, got {type(ref).__name__}")
-        if ref.device.type != _lib._DEVICE_TYPE:
-            raise ValueError(f"{where}: tensors must be on a CUDA device, got {ref.device}")
-        if ref.dtype is torch.bfloat16:
-            self.code = KDA_BF16
-        elif ref.dtype is _F32:
-            self.code = KDA_F32
-        else:
-            raise ValueError(f"{where}: q, k, v and o must be bfloat16 or float32, got {ref.dtype}")
+        self.dev = ref.device
+        if self.dev.type != _lib._DEVICE_TYPE:
+            raise ValueError(f"{where}: tensors must be on a CUDA device, got {self.dev}")
+        self.index, self.dt = ref.get_device(), ref.dtype
+        code = _CODES.get(self.dt)
+        if code is None:
+            raise ValueError(f"{where}: q, k, v and o must be bfloat16 or float32, got {self.dt}")
         if ref.dim() != ndim:
             raise ValueError(f"{where}: expected {ndim} dimensions, got shape {tuple(ref.shape)}")
-        self.dev, self.dt = ref.device, ref.dtype
+        self.code = code
 
     def __call__(self, name, t, shape, dtype=None, optional=False):
         """The tensor's address, after its checks."""
         if t is None and optional:
             return None
-        dtype = self.dt if dtype is None else dtype
-        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-                and t.device == self.dev and t.is_contiguous()):
-            _refuse(self.where, name, t, self.dev, dtype, shape)
-        return t.data_ptr()
+        if dtype is None:
+            dtype = self.dt
+        try:
+            if (t.dtype is dtype and t.shape == shape and t.get_device() == self.index
+                    and t.is_contiguous()):
+                return t.data_ptr()
+        except AttributeError:
+            pass
+        _refuse(self.where, name, t, self.dev, dtype, shape)
 
     def workspace(self, ws):
         """(address, bytes); any dtype, the library checks the size."""
@@ -103,38 +109,45 @@ class _Call:
 
     def run(self, name, stream, *args):
         """Calls the entry point on `stream`, with the tensors' device current."""
-        if self.dev.type != "cuda":
+        i = self.index
+        if i < 0:
             raise ValueError(f"{self.where}: tensors must be on a CUDA device, got {self.dev}")
-        fn, i = getattr(lib(), name), self.dev.index
         # torch's own bindings for the current stream and device: the public
-        # functions around them cost several times what the launch does
+        # functions around them cost several times what they do
         raw = _current_stream(i) if stream is None else _raw(stream)
         if i == _current_device():
-            st = fn(*args, raw)
+            st = _entry(name)(*args, raw)
         else:
             with torch.cuda.device(self.dev):
-                st = fn(*args, raw)
+                st = _entry(name)(*args, raw)
         if st:
             _check(st, name)
+
+
+_entries = {}
+
+
+def _entry(name):
+    fn = _entries.get(name)
+    if fn is None:
+        fn = _entries[name] = getattr(lib(), name)
+    return fn
 
 
 def _raw(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-@contextlib.contextmanager
-def _stream_of(dev, stream):
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev)
-    with torch.cuda.stream(stream):
-        yield
+_NO_STREAM = contextlib.nullcontext()
 
 
 def _on(t, stream):
     """Allocations inside belong to the stream that the call runs on."""
     if stream is None or not isinstance(t, torch.Tensor) or t.device.type != "cuda":
-        return contextlib.nullcontext()
-    return _stream_of(t.device, stream)
+        return _NO_STREAM
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+    return torch.cuda.stream(stream)
 
 
 def _code(dtype):
@@ -142,10 +155,11 @@ def _code(dtype):
 
 
 def _dims(c, q, v, ndim):
-    """(lead sizes, H, H_k, d_k, d_v) from q [.., H_k, d_k] and v [.., H, d_v]."""
+    """(lead sizes, H, d_v, H_k, d_k) from q [.., H_k, d_k] and v [.., H, d_v]."""
     if not isinstance(v, torch.Tensor) or v.dim() != ndim:
         raise ValueError(f"{c.where}: v must be a tensor with {ndim} dimensions")
-    return tuple(q.shape[:-2]), v.shape[-2], q.shape[-2], q.shape[-1], v.shape[-1]
+    *lead, Hk, dk = q.shape
+    return lead, *v.shape[-2:], Hk, dk
 
 
 def _pool(c, pool, H, dk, dv):
@@ -171,7 +185,7 @@ def kda_linear_backward_workspace_bytes(B, T, H, H_k, d_k, d_v, dtype) -> int:
 def kda_linear_prefill(q, k, v, g, scale, S0, o, S_T, lens=None, workspace=None, stream=None):
     """C entry point kda_linear_prefill."""
     c = _Call("kda_linear_prefill", q, 4)
-    (B, T), H, Hk, dk, dv = _dims(c, q, v, 4)
+    (B, T), H, dv, Hk, dk = _dims(c, q, v, 4)
     ws, nbytes = c.workspace(workspace)
     c.run("kda_linear_prefill", stream, c("q", q, (B, T, Hk, dk)), c("k", k, (B, T, Hk, dk)),
           c("v", v, (B, T, H, dv)), c("g", g, (H,), _F32), float(scale),
@@ -185,7 +199,7 @@ def kda_linear_prefill_paged(q, k, v, g, scale, pool, slots_in, slots_out, o, le
     """C entry point kda_linear_prefill_paged: states from pool[slots_in[b]] into
     pool[slots_out[b]] (either table may be None)."""
     c = _Call("kda_linear_prefill_paged", q, 4)
-    (B, T), H, Hk, dk, dv = _dims(c, q, v, 4)
+    (B, T), H, dv, Hk, dk = _dims(c, q, v, 4)
     pp, n_slots = _pool(c, pool, H, dk, dv)
     ws, nbytes = c.workspace(workspace)
     c.run("kda_linear_prefill_paged", stream, c("q", q, (B, T, Hk, dk)),
@@ -200,7 +214,7 @@ def linear_prefill(q, k, v, g, scale=1.0, S0=None, lens=None, want_state=True, o
     """kda_linear_prefill with S_T, the workspace and (unless given) o allocated;
     an allocated o is zero past the lengths.  Returns (o, S_T or None)."""
     c = _Call("linear_prefill", q, 4)
-    (B, T), H, Hk, dk, dv = _dims(c, q, v, 4)
+    (B, T), H, dv, Hk, dk = _dims(c, q, v, 4)
     with _on(q, stream):
         if o is None:
             new = torch.empty if lens is None else torch.zeros
@@ -215,7 +229,7 @@ def kda_linear_backward(q, k, v, g, scale, S0, dO, dS_T, dq, dk, dv, dS0, lens=N
                         workspace=None, stream=None):
     """C entry point kda_linear_backward."""
     c = _Call("kda_linear_backward", q, 4)
-    (B, T), H, Hk, dkk, dvv = _dims(c, q, v, 4)
+    (B, T), H, dvv, Hk, dkk = _dims(c, q, v, 4)
     qk, vo, st = (B, T, Hk, dkk), (B, T, H, dvv), (B, H, dkk, dvv)
     ws, nbytes = c.workspace(workspace)
     c.run("kda_linear_backward", stream, c("q", q, qk), c("k", k, qk), c("v", v, vo),
@@ -231,7 +245,7 @@ def linear_backward(q, k, v, g, dO, scale=1.0, S0=None, dS_T=None, lens=None, wa
     allocated; allocated ones are zero past the lengths.  Returns a dict with
     dq, dk, dv, dS0."""
     c = _Call("linear_backward", q, 4)
-    (B, T), H, Hk, dkk, dvv = _dims(c, q, v, 4)
+    (B, T), H, dvv, Hk, dkk = _dims(c, q, v, 4)
     with _on(q, stream):
         new = torch.empty_like if lens is None else torch.zeros_like
         dq = new(q) if dq is None else dq
@@ -247,7 +261,7 @@ def linear_backward(q, k, v, g, dO, scale=1.0, S0=None, dS_T=None, lens=None, wa
 def kda_linear_decode_step(q, k, v, g, scale, S, o, stream=None):
     """C entry point kda_linear_decode_step; S is updated in place."""
     c = _Call("kda_linear_decode_step", q, 3)
-    (B,), H, Hk, dk, dv = _dims(c, q, v, 3)
+    (B,), H, dv, Hk, dk = _dims(c, q, v, 3)
     c.run("kda_linear_decode_step", stream, c("q", q, (B, Hk, dk)), c("k", k, (B, Hk, dk)),
           c("v", v, (B, H, dv)), c("g", g, (H,), _F32), float(scale),
           c("S", S, (B, H, dk, dv), _F32), c("o", o, (B, H, dv)), B, H, Hk, dk, dv, c.code)
@@ -256,7 +270,7 @@ def kda_linear_decode_step(q, k, v, g, scale, S, o, stream=None):
 def kda_linear_decode_step_paged(q, k, v, g, scale, pool, slots, o, stream=None):
     """C entry point kda_linear_decode_step_paged: pool[slots[b]] updated in place."""
     c = _Call("kda_linear_decode_step_paged", q, 3)
-    (B,), H, Hk, dk, dv = _dims(c, q, v, 3)
+    (B,), H, dv, Hk, dk = _dims(c, q, v, 3)
     pp, n_slots = _pool(c, pool, H, dk, dv)
     c.run("kda_linear_decode_step_paged", stream, c("q", q, (B, Hk, dk)), c("k", k, (B, Hk, dk)),
           c("v", v, (B, H, dv)), c("g", g, (H,), _F32), float(scale), pp, n_slots,
@@ -276,7 +290,7 @@ def linear_decode_step(q, k, v, g, S, scale=1.0, stream=None):
 def kda_linear_tree(q, k, v, g, scale, S, parent, o, stream=None):
     """C entry point kda_linear_tree; parent int32 [B, T]."""
     c = _Call("kda_linear_tree", q, 4)
-    (B, T), H, Hk, dk, dv = _dims(c, q, v, 4)
+    (B, T), H, dv, Hk, dk = _dims(c, q, v, 4)
     c.run("kda_linear_tree", stream, c("q", q, (B, T, Hk, dk)), c("k", k, (B, T, Hk, dk)),
           c("v", v, (B, T, H, dv)), c("g", g, (H,), _F32), float(scale),
           c("S", S, (B, H, dk, dv), _F32), c("parent", parent, (B, T), _I32),
@@ -286,7 +300,7 @@ def kda_linear_tree(q, k, v, g, scale, S, parent, o, stream=None):
 def kda_linear_tree_paged(q, k, v, g, scale, pool, slots, parent, o, stream=None):
     """C entry point kda_linear_tree_paged: the states pool[slots[b]]."""
     c = _Call("kda_linear_tree_paged", q, 4)
-    (B, T), H, Hk, dk, dv = _dims(c, q, v, 4)
+    (B, T), H, dv, Hk, dk = _dims(c, q, v, 4)
     pp, n_slots = _pool(c, pool, H, dk, dv)
     c.run("kda_linear_tree_paged", stream, c("q", q, (B, T, Hk, dk)), c("k", k, (B, T, Hk, dk)),
           c("v", v, (B, T, H, dv)), c("g", g, (H,), _F32), float(scale), pp, n_slots,
@@ -305,7 +319,7 @@ def linear_tree(q, k, v, g, S, parent, scale=1.0, stream=None):
 def kda_linear_tree_commit(k, v, g, parent, accepted, S, S_out, stream=None):
     """C entry point kda_linear_tree_commit; accepted int32 [B], S_out may be S."""
     c = _Call("kda_linear_tree_commit", k, 4)
-    (B, T), H, Hk, dk, dv = _dims(c, k, v, 4)
+    (B, T), H, dv, Hk, dk = _dims(c, k, v, 4)
     c.run("kda_linear_tree_commit", stream, c("k", k, (B, T, Hk, dk)), c("v", v, (B, T, H, dv)),
           c("g", g, (H,), _F32), c("parent", parent, (B, T), _I32),
           c("accepted", accepted, (B,), _I32), c("S", S, (B, H, dk, dv), _F32),
@@ -317,7 +331,7 @@ def kda_linear_tree_commit_paged(k, v, g, parent, accepted, pool, slots_in, slot
     """C entry point kda_linear_tree_commit_paged: from pool[slots_in[b]] into
     pool[slots_out[b]]."""
     c = _Call("kda_linear_tree_commit_paged", k, 4)
-    (B, T), H, Hk, dk, dv = _dims(c, k, v, 4)
+    (B, T), H, dv, Hk, dk = _dims(c, k, v, 4)
     pp, n_slots = _pool(c, pool, H, dk, dv)
     c.run("kda_linear_tree_commit_paged", stream, c("k", k, (B, T, Hk, dk)),
           c("v", v, (B, T, H, dv)), c("g", g, (H,), _F32), c("parent", parent, (B, T), _I32),

@@ -17,6 +17,7 @@
 // >= 0, formed as exp of the product, so nothing overflows for g <= 0 and no
 // error builds up along a chunk.
 #include <algorithm>
+#include <cmath>
 
 #include "kda_device.hpp"
 #include "kda_linear.hpp"
@@ -52,22 +53,26 @@ struct LinearJob {
 // one barrier a chunk, the chunk after the next in flight in registers).  The
 // pair weights are computed transposed (keys x queries) by every wave, which
 // makes the product with u take them straight from the accumulators.
-// NP: terms of E that the state and the pair weights are split into for their
-// products with x and u (see launch_job_d).  STATE: only the state of a segment
+// Matrix operands are sums of bf16 terms: x, y and u are one if bf16, three if
+// fp32; NP is the number for the state and the pair weights in their products
+// with x and u (see launch_job_d).  STATE: only the state of a segment
 // from zero, into the workspace.
 template <typename E, int DA, int DB, int NC, int NP, bool STATE>
 __global__ __launch_bounds__(DB / NC * 4, 2) void linear_chunk_kernel(LinearJob job) {
-    constexpr int C = kLinChunk, NT = DB / NC * 4, KM = DA / 32, NS = sizeof(E) == 2 ? 3 : 1;
+    constexpr int C = kLinChunk, NT = DB / NC * 4, KM = DA / 32;
+    constexpr int NE = sizeof(E) == 2 ? 1 : 3;               // bf16 terms of x, y and u
     constexpr int PE = 16 / sizeof(E);                       // elements of 16 bytes
-    // padded LDS rows: rows 12 (mod 16) banks apart for x and y, so that both 16
-    // rows of 16 bytes and the transposing reads of 8-byte groups 16 bytes apart
-    // spread over the banks; 8 (mod 16) apart for u
-    constexpr int LA = DA + (sizeof(E) == 2 ? 24 : 4), LB = DB + (sizeof(E) == 2 ? 16 : 4);
+    // Padded LDS rows.  bf16: rows 12 (mod 16) banks apart for x and y, so that
+    // both 16 rows of 16 bytes and the transposing reads of 8-byte groups 16
+    // bytes apart spread over the banks; 8 (mod 16) apart for u.  fp32, as three
+    // bf16 planes: what fits the LDS.
+    constexpr int LA = DA + (NE == 1 ? 24 : 8), LB = DB + (NE == 1 ? 16 : 8);
+    constexpr int QA = C * LA, QB = C * LB;                  // elements of a plane
     constexpr int PA = C * DA / PE, PB = C * DB / PE;        // 16-byte pieces of a tile
     constexpr int RA = (PA + NT - 1) / NT, RB = (PB + NT - 1) / NT;
     static_assert(DB % (16 * NC) == 0, "waves cover the columns");
-    __shared__ __align__(16) E s_x[STATE ? 1 : 2][STATE ? 8 : C * LA];
-    __shared__ __align__(16) E s_y[2][C * LA], s_u[2][C * LB];
+    __shared__ __align__(16) bf16 s_x[STATE ? 1 : 2][STATE ? 8 : NE * QA];
+    __shared__ __align__(16) bf16 s_y[2][NE * QA], s_u[2][NE * QB];
 
     const LinearSegs segs = job.segs;
     const int units = job.pass[0].B * job.pass[0].H, nseg = STATE ? segs.R - 1 : segs.R;
@@ -214,20 +219,35 @@ __global__ __launch_bounds__(DB / NC * 4, 2) void linear_chunk_kernel(LinearJob 
         Y.base += Y.step;
         U.base += U.step;
     };
+    // A 16-byte piece to LDS: bf16 as it is, four fp32 values as their terms.
+    auto put = [](bf16* dst, int plane, u32x4 v) {
+        if constexpr (NE == 1) {
+            *reinterpret_cast<u32x4*>(dst) = v;
+        } else {
+            f32x4 x = __builtin_bit_cast(f32x4, v);
+#pragma unroll
+            for (int s = 0; s < NE; ++s) {
+                const bf16x4 h = pack4(x);
+                *reinterpret_cast<bf16x4*>(dst + s * plane) = h;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] -= (float)h[i];
+            }
+        }
+    };
     auto stage = [&](auto set) {
         constexpr int buf = decltype(set)::value;
 #pragma unroll
         for (int i = 0; i < RA; ++i) {
             const int at = row_of(i, DA) * LA + (tid + i * NT) % (DA / PE) * PE;
             if (PA % NT == 0 || tid + i * NT < PA) {
-                if (!STATE) *reinterpret_cast<u32x4*>(&s_x[STATE ? 0 : buf][at]) = rx[i];
-                *reinterpret_cast<u32x4*>(&s_y[buf][at]) = ry[i];
+                if (!STATE) put(&s_x[STATE ? 0 : buf][at], QA, rx[i]);
+                put(&s_y[buf][at], QA, ry[i]);
             }
         }
 #pragma unroll
         for (int i = 0; i < RB; ++i) {
             const int at = row_of(i, DB) * LB + (tid + i * NT) % (DB / PE) * PE;
-            if (PB % NT == 0 || tid + i * NT < PB) *reinterpret_cast<u32x4*>(&s_u[buf][at]) = ru[i];
+            if (PB % NT == 0 || tid + i * NT < PB) put(&s_u[buf][at], QB, ru[i]);
         }
     };
 
@@ -241,10 +261,10 @@ __global__ __launch_bounds__(DB / NC * 4, 2) void linear_chunk_kernel(LinearJob 
         stage(other);
         load(s1 - s - 2 * C);
         if (c < C) chunk_weights(c);
-        const E *sx = s_x[STATE ? 0 : k], *sy = s_y[k], *su = s_u[k];
-        Frag<E> uf[NC];
+        const bf16 *sx = s_x[STATE ? 0 : k], *sy = s_y[k], *su = s_u[k];
+        Terms<NE> uf[NC];
 #pragma unroll
-        for (int ct = 0; ct < NC; ++ct) uf[ct] = col_frag<E>(su, LB, cbase + 4 * ct, cstep, j, g);
+        for (int ct = 0; ct < NC; ++ct) uf[ct] = col_terms<NE>(su, QB, LB, cbase + 4 * ct, cstep, j, g);
         if constexpr (!STATE) {
             f32x4 p00 = zero4(), p01 = zero4(), p11 = zero4(), o[NC][2];
 #pragma unroll
@@ -252,20 +272,16 @@ __global__ __launch_bounds__(DB / NC * 4, 2) void linear_chunk_kernel(LinearJob 
 #pragma unroll
             for (int m = 0; m < KM; ++m) {
                 const int e = 32 * m + 8 * g;
-                const Frag<E> x0 = row_frag<E>(sx + j * LA + e), x1 = row_frag<E>(sx + (16 + j) * LA + e);
-                const Frag<E> y0 = row_frag<E>(sy + j * LA + e), y1 = row_frag<E>(sy + (16 + j) * LA + e);
+                const Terms<NE> x0 = row_terms<NE>(sx + j * LA + e, QA), x1 = row_terms<NE>(sx + (16 + j) * LA + e, QA);
+                const Terms<NE> y0 = row_terms<NE>(sy + j * LA + e, QA), y1 = row_terms<NE>(sy + (16 + j) * LA + e, QA);
                 p00 = mma(y0, x0, p00);
                 p01 = mma(y0, x1, p01);
                 p11 = mma(y1, x1, p11);
 #pragma unroll
                 for (int ct = 0; ct < NC; ++ct) {
-                    Frag<E> mf[NP];
-                    split(M[2 * m][ct], M[2 * m + 1][ct], mf);
-#pragma unroll
-                    for (int i = 0; i < NP; ++i) {
-                        o[ct][0] = mma(mf[i], x0, o[ct][0]);
-                        o[ct][1] = mma(mf[i], x1, o[ct][1]);
-                    }
+                    const Terms<NP> mf = to_terms<NP>(M[2 * m][ct], M[2 * m + 1][ct]);
+                    o[ct][0] = mma(mf, x0, o[ct][0]);
+                    o[ct][1] = mma(mf, x1, o[ct][1]);
                 }
             }
 #pragma unroll
@@ -274,20 +290,13 @@ __global__ __launch_bounds__(DB / NC * 4, 2) void linear_chunk_kernel(LinearJob 
                 p01[i] *= wo[i];
                 p11[i] *= wd[i];
             }
-            Frag<E> w0[NP], w1[NP];
-            split(p00, zero4(), w0);
-            split(p01, p11, w1);
+            const Terms<NP> w0 = to_terms<NP>(p00, zero4()), w1 = to_terms<NP>(p01, p11);
             const Rsrc out = make_rsrc(Out.base, Out.bytes);
             Out.base += Out.step;
 #pragma unroll
             for (int ct = 0; ct < NC; ++ct) {
-                o[ct][0] *= wi[0];
-                o[ct][1] *= wi[1];
-#pragma unroll
-                for (int i = 0; i < NP; ++i) {
-                    o[ct][0] = mma(uf[ct], w0[i], o[ct][0]);
-                    o[ct][1] = mma(uf[ct], w1[i], o[ct][1]);
-                }
+                o[ct][0] = mma(uf[ct], w0, wi[0] * o[ct][0]);
+                o[ct][1] = mma(uf[ct], w1, wi[1] * o[ct][1]);
             }
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -305,8 +314,7 @@ __global__ __launch_bounds__(DB / NC * 4, 2) void linear_chunk_kernel(LinearJob 
                 }
             }
         }
-        // the weighted u in three bf16 terms: the state keeps fp32's accuracy
-        Frag<E> us[NC][NS];
+        Terms<3> us[NC];                                     // the state keeps fp32's accuracy
 #pragma unroll
         for (int ct = 0; ct < NC; ++ct) {
             f32x4 lo, hi;
@@ -316,18 +324,15 @@ __global__ __launch_bounds__(DB / NC * 4, 2) void linear_chunk_kernel(LinearJob 
                 lo[i] *= wu[i];
                 hi[i] *= wu[4 + i];
             }
-            split(lo, hi, us[ct]);
+            us[ct] = to_terms<3>(lo, hi);
         }
         const float f = chunk_decay();
 #pragma unroll
         for (int t = 0; t < 2 * KM; ++t) {
-            const Frag<E> yt = col_frag<E>(sy, LA, 32 * (t >> 1) + 4 * (t & 1), 8, j, g);
+            const Terms<NE> yt = col_terms<NE>(sy, QA, LA, 32 * (t >> 1) + 4 * (t & 1), 8, j, g);
 #pragma unroll
             for (int ct = 0; ct < NC; ++ct) {
-                f32x4 acc = f * M[t][ct];
-#pragma unroll
-                for (int i = 0; i < NS; ++i) acc = mma(yt, us[ct][i], acc);
-                M[t][ct] = acc;
+                M[t][ct] = mma(yt, us[ct], f * M[t][ct]);
             }
         }
     };
@@ -390,20 +395,22 @@ __global__ __launch_bounds__(256) void linear_share_kernel(const float* __restri
 // of the second reads the states before its own.  The estimate below, in us,
 // is taken for each R and the least wins.  Its constants are measured: a chunk
 // takes `out` us in the second launch and `state` us in the first (latency,
-// until a CU has several workgroups), the first launch 6 us of its own, and the
-// states move at 5 TB/s.  B1 H32 T4096 d128 bf16: 197 us with one segment, 92 with
-// 4, 63 with 8, 78 with 16; B8 H32 T8192: 492 with one, 640 with 2.
+// until a CU has several workgroups; fp32's LDS leaves room for one, so they
+// run in rounds), the first launch 6 us of its own, and the states move at 5
+// TB/s.  B1 H32 T4096 d128 bf16: 197 us with one segment, 92 with 4, 63 with 8,
+// 78 with 16; B8 H32 T8192: 492 with one, 640 with 2; B4 H16 T2048 fp32: 328 with
+// one, 156 with 4, 202 with 16.
 static LinearSegs segments(int passes, int B, int T, int H, int da, int db, bool is_bf16) {
     const double units = (double)B * H * passes, size = da * db / 16384.0;
-    const double out = is_bf16 ? 0.7 + 0.7 * size : 0.8 + 6.5 * size;
-    const double state = is_bf16 ? 0.4 + 0.35 * size : 0.4 + 2.6 * size;
+    const double out = is_bf16 ? 0.7 + 0.7 * size : 1.1 + 4.0 * size;
+    const double state = is_bf16 ? 0.4 + 0.35 * size : 0.7 + 2.0 * size;
     LinearSegs best{1, (T + kLinChunk - 1) / kLinChunk * kLinChunk};
     double least = 0;
     for (int r = 1; r <= 32; ++r) {
         const int chunks = ((T + r - 1) / r + kLinChunk - 1) / kLinChunk, len = chunks * kLinChunk;
         const int R = (T + len - 1) / len;
         if (R != r) continue;
-        const double busy = std::max(1.0, 0.65 * units * R / 256);
+        const double load = units * R / 256, busy = is_bf16 ? std::max(1.0, 0.65 * load) : std::ceil(load);
         double us = chunks * out * busy;
         if (R > 1) us += 6 + chunks * state * busy + units * da * db * 4 * (0.5 * R * (R - 1) + 2 * R) / 5e6;
         if (r == 1 || us < least) {
@@ -444,14 +451,15 @@ static hipError_t launch_job_n(const LinearJob& job, int passes, hipStream_t str
 // part, has to spare.
 template <typename E, int DA, int DB>
 static hipError_t launch_job_d(const LinearJob& job, int passes, hipStream_t stream) {
+    constexpr int NP = sizeof(E) == 2 ? 1 : 3;
     if constexpr (DB == 128) {
         if ((long long)job.pass[0].B * job.pass[0].H * passes >= 96)
-            return launch_job_n<E, DA, DB, 2, 1>(job, passes, stream);
+            return launch_job_n<E, DA, DB, 2, NP>(job, passes, stream);
     }
     if constexpr (sizeof(E) == 2) {
         if (job.segs.len <= 4 * kLinChunk) return launch_job_n<E, DA, DB, 1, 2>(job, passes, stream);
     }
-    return launch_job_n<E, DA, DB, 1, 1>(job, passes, stream);
+    return launch_job_n<E, DA, DB, 1, NP>(job, passes, stream);
 }
 
 template <typename E, int DA>
