@@ -68,16 +68,19 @@ def _refuse(where, name, t, dev, dtype, shape):
 class _Call:
     """The checks of one call's tensors against the first one's device and type."""
 
-    __slots__ = ("where", "dev", "index", "dt", "code")
+    __slots__ = ("where", "index", "dt", "code")
+
+    @property
+    def dev(self):
+        return torch.device("cuda", self.index) if self.index >= 0 else torch.device("cpu")
 
     def __init__(self, where, ref, ndim):
         self.where = where
         if not isinstance(ref, torch.Tensor):
             raise TypeError(f"{where}: expected a torch.Tensor, got {type(ref).__name__}")
-        self.dev = ref.device
-        if self.dev.type != _lib._DEVICE_TYPE:
-            raise ValueError(f"{where}: tensors must be on a CUDA device, got {self.dev}")
-        self.index, self.dt = ref.get_device(), ref.dtype
+        self.index, self.dt = ref.get_device(), ref.dtype      # index -1: host memory
+        if not ref.is_cuda and _lib._DEVICE_TYPE == "cuda":
+            raise ValueError(f"{where}: tensors must be on a CUDA device, got {ref.device}")
         code = _CODES.get(self.dt)
         if code is None:
             raise ValueError(f"{where}: q, k, v and o must be bfloat16 or float32, got {self.dt}")
@@ -155,11 +158,16 @@ def _code(dtype):
 
 
 def _dims(c, q, v, ndim):
-    """(lead sizes, H, d_v, H_k, d_k) from q [.., H_k, d_k] and v [.., H, d_v]."""
+    """(lead sizes.., H, d_v, H_k, d_k) from q [.., H_k, d_k] and v [.., H, d_v]."""
     if not isinstance(v, torch.Tensor) or v.dim() != ndim:
         raise ValueError(f"{c.where}: v must be a tensor with {ndim} dimensions")
-    *lead, Hk, dk = q.shape
-    return lead, *v.shape[-2:], Hk, dk
+    if ndim == 3:
+        B, Hk, dk = q.shape
+        _, H, dv = v.shape
+        return B, H, dv, Hk, dk
+    B, T, Hk, dk = q.shape
+    _, _, H, dv = v.shape
+    return B, T, H, dv, Hk, dk
 
 
 def _pool(c, pool, H, dk, dv):
@@ -185,7 +193,7 @@ def kda_linear_backward_workspace_bytes(B, T, H, H_k, d_k, d_v, dtype) -> int:
 def kda_linear_prefill(q, k, v, g, scale, S0, o, S_T, lens=None, workspace=None, stream=None):
     """C entry point kda_linear_prefill."""
     c = _Call("kda_linear_prefill", q, 4)
-    (B, T), H, dv, Hk, dk = _dims(c, q, v, 4)
+    B, T, H, dv, Hk, dk = _dims(c, q, v, 4)
     ws, nbytes = c.workspace(workspace)
     c.run("kda_linear_prefill", stream, c("q", q, (B, T, Hk, dk)), c("k", k, (B, T, Hk, dk)),
           c("v", v, (B, T, H, dv)), c("g", g, (H,), _F32), float(scale),
@@ -199,7 +207,7 @@ def kda_linear_prefill_paged(q, k, v, g, scale, pool, slots_in, slots_out, o, le
     """C entry point kda_linear_prefill_paged: states from pool[slots_in[b]] into
     pool[slots_out[b]] (either table may be None)."""
     c = _Call("kda_linear_prefill_paged", q, 4)
-    (B, T), H, dv, Hk, dk = _dims(c, q, v, 4)
+    B, T, H, dv, Hk, dk = _dims(c, q, v, 4)
     pp, n_slots = _pool(c, pool, H, dk, dv)
     ws, nbytes = c.workspace(workspace)
     c.run("kda_linear_prefill_paged", stream, c("q", q, (B, T, Hk, dk)),
@@ -214,7 +222,7 @@ def linear_prefill(q, k, v, g, scale=1.0, S0=None, lens=None, want_state=True, o
     """kda_linear_prefill with S_T, the workspace and (unless given) o allocated;
     an allocated o is zero past the lengths.  Returns (o, S_T or None)."""
     c = _Call("linear_prefill", q, 4)
-    (B, T), H, dv, Hk, dk = _dims(c, q, v, 4)
+    B, T, H, dv, Hk, dk = _dims(c, q, v, 4)
     with _on(q, stream):
         if o is None:
             new = torch.empty if lens is None else torch.zeros
@@ -229,7 +237,7 @@ def kda_linear_backward(q, k, v, g, scale, S0, dO, dS_T, dq, dk, dv, dS0, lens=N
                         workspace=None, stream=None):
     """C entry point kda_linear_backward."""
     c = _Call("kda_linear_backward", q, 4)
-    (B, T), H, dvv, Hk, dkk = _dims(c, q, v, 4)
+    B, T, H, dvv, Hk, dkk = _dims(c, q, v, 4)
     qk, vo, st = (B, T, Hk, dkk), (B, T, H, dvv), (B, H, dkk, dvv)
     ws, nbytes = c.workspace(workspace)
     c.run("kda_linear_backward", stream, c("q", q, qk), c("k", k, qk), c("v", v, vo),
@@ -245,7 +253,7 @@ def linear_backward(q, k, v, g, dO, scale=1.0, S0=None, dS_T=None, lens=None, wa
     allocated; allocated ones are zero past the lengths.  Returns a dict with
     dq, dk, dv, dS0."""
     c = _Call("linear_backward", q, 4)
-    (B, T), H, dvv, Hk, dkk = _dims(c, q, v, 4)
+    B, T, H, dvv, Hk, dkk = _dims(c, q, v, 4)
     with _on(q, stream):
         new = torch.empty_like if lens is None else torch.zeros_like
         dq = new(q) if dq is None else dq
@@ -261,7 +269,7 @@ def linear_backward(q, k, v, g, dO, scale=1.0, S0=None, dS_T=None, lens=None, wa
 def kda_linear_decode_step(q, k, v, g, scale, S, o, stream=None):
     """C entry point kda_linear_decode_step; S is updated in place."""
     c = _Call("kda_linear_decode_step", q, 3)
-    (B,), H, dv, Hk, dk = _dims(c, q, v, 3)
+    B, H, dv, Hk, dk = _dims(c, q, v, 3)
     c.run("kda_linear_decode_step", stream, c("q", q, (B, Hk, dk)), c("k", k, (B, Hk, dk)),
           c("v", v, (B, H, dv)), c("g", g, (H,), _F32), float(scale),
           c("S", S, (B, H, dk, dv), _F32), c("o", o, (B, H, dv)), B, H, Hk, dk, dv, c.code)
@@ -270,7 +278,7 @@ def kda_linear_decode_step(q, k, v, g, scale, S, o, stream=None):
 def kda_linear_decode_step_paged(q, k, v, g, scale, pool, slots, o, stream=None):
     """C entry point kda_linear_decode_step_paged: pool[slots[b]] updated in place."""
     c = _Call("kda_linear_decode_step_paged", q, 3)
-    (B,), H, dv, Hk, dk = _dims(c, q, v, 3)
+    B, H, dv, Hk, dk = _dims(c, q, v, 3)
     pp, n_slots = _pool(c, pool, H, dk, dv)
     c.run("kda_linear_decode_step_paged", stream, c("q", q, (B, Hk, dk)), c("k", k, (B, Hk, dk)),
           c("v", v, (B, H, dv)), c("g", g, (H,), _F32), float(scale), pp, n_slots,
@@ -290,7 +298,7 @@ def linear_decode_step(q, k, v, g, S, scale=1.0, stream=None):
 def kda_linear_tree(q, k, v, g, scale, S, parent, o, stream=None):
     """C entry point kda_linear_tree; parent int32 [B, T]."""
     c = _Call("kda_linear_tree", q, 4)
-    (B, T), H, dv, Hk, dk = _dims(c, q, v, 4)
+    B, T, H, dv, Hk, dk = _dims(c, q, v, 4)
     c.run("kda_linear_tree", stream, c("q", q, (B, T, Hk, dk)), c("k", k, (B, T, Hk, dk)),
           c("v", v, (B, T, H, dv)), c("g", g, (H,), _F32), float(scale),
           c("S", S, (B, H, dk, dv), _F32), c("parent", parent, (B, T), _I32),
@@ -300,7 +308,7 @@ def kda_linear_tree(q, k, v, g, scale, S, parent, o, stream=None):
 def kda_linear_tree_paged(q, k, v, g, scale, pool, slots, parent, o, stream=None):
     """C entry point kda_linear_tree_paged: the states pool[slots[b]]."""
     c = _Call("kda_linear_tree_paged", q, 4)
-    (B, T), H, dv, Hk, dk = _dims(c, q, v, 4)
+    B, T, H, dv, Hk, dk = _dims(c, q, v, 4)
     pp, n_slots = _pool(c, pool, H, dk, dv)
     c.run("kda_linear_tree_paged", stream, c("q", q, (B, T, Hk, dk)), c("k", k, (B, T, Hk, dk)),
           c("v", v, (B, T, H, dv)), c("g", g, (H,), _F32), float(scale), pp, n_slots,
@@ -319,7 +327,7 @@ def linear_tree(q, k, v, g, S, parent, scale=1.0, stream=None):
 def kda_linear_tree_commit(k, v, g, parent, accepted, S, S_out, stream=None):
     """C entry point kda_linear_tree_commit; accepted int32 [B], S_out may be S."""
     c = _Call("kda_linear_tree_commit", k, 4)
-    (B, T), H, dv, Hk, dk = _dims(c, k, v, 4)
+    B, T, H, dv, Hk, dk = _dims(c, k, v, 4)
     c.run("kda_linear_tree_commit", stream, c("k", k, (B, T, Hk, dk)), c("v", v, (B, T, H, dv)),
           c("g", g, (H,), _F32), c("parent", parent, (B, T), _I32),
           c("accepted", accepted, (B,), _I32), c("S", S, (B, H, dk, dv), _F32),
@@ -331,7 +339,7 @@ def kda_linear_tree_commit_paged(k, v, g, parent, accepted, pool, slots_in, slot
     """C entry point kda_linear_tree_commit_paged: from pool[slots_in[b]] into
     pool[slots_out[b]]."""
     c = _Call("kda_linear_tree_commit_paged", k, 4)
-    (B, T), H, dv, Hk, dk = _dims(c, k, v, 4)
+    B, T, H, dv, Hk, dk = _dims(c, k, v, 4)
     pp, n_slots = _pool(c, pool, H, dk, dv)
     c.run("kda_linear_tree_commit_paged", stream, c("k", k, (B, T, Hk, dk)),
           c("v", v, (B, T, H, dv)), c("g", g, (H,), _F32), c("parent", parent, (B, T), _I32),
