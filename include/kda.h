@@ -405,7 +405,10 @@ kda_status kda_intra_chunk(const void *q, const void *k, const void *z,
  *   or of the gradients, keep what they held), and the final state is the one
  *   after the last real token: S0 itself for a length of 0.
  * - Inputs must be finite: an infinity or NaN in one token can reach outputs
- *   of up to 31 tokens before it as well as all later ones.
+ *   of up to 31 tokens before it as well as all later ones (and, in a tree,
+ *   of every node).
+ * - A pool row that one sequence of a paged call writes may be read by that
+ *   sequence alone: a second one naming it, as input or output, races.
  * - g and lens need 4-byte, the states 16-byte alignment. */
 
 /* Bytes of device workspace kda_linear_prefill and kda_linear_prefill_paged

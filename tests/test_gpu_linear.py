@@ -151,6 +151,77 @@ def test_prefill_in_place_state_of_long_sequences(dtype):
         assert torch.equal(S, S_T) and torch.equal(o2, o)
 
 
+def test_long_slow_decays_keep_their_factor():
+    """20,000 steps at decays near 1: the state's error stays that of fp32 sums.  Each of
+    625 chunk updates rounds the state by at most 2^-24 of itself, at random: about
+    sqrt(625) 2^-25 = 7.5e-7 of its norm, to which the weights add a few 2^-24; 4e-6
+    leaves a factor of four.  A factor a^32 rounded once and multiplied 625 times would
+    be off by up to 625 2^-25 = 1.9e-5."""
+    need_gpu()
+    import linear_attention_recurrence_05_amd as kda
+    x, _ = make(1, 20000, 4, 4, 32, 32, F32, seed=18)
+    x["g"] = torch.tensor([-1e-6, -3.1e-5, -1.7e-4, 0.0], device="cuda")
+    _, S_T = kda.linear_prefill(x["q"], x["k"], x["v"], x["g"], x["scale"], x["S0"])
+    torch.cuda.synchronize()
+    a = torch.exp(x["g"].double())[:, None, None]
+    S = x["S0"][0].double()
+    for t in range(20000):
+        S = a * S + x["k"][0, t].double()[:, :, None] * x["v"][0, t].double()[:, None]
+    err = torch.linalg.vector_norm(S_T[0].double() - S, dim=(1, 2)) / torch.linalg.vector_norm(S, dim=(1, 2))
+    assert (err < 4e-6).all(), err
+
+
+def test_tensors_past_32_bit_offsets():
+    """More than 2^31 elements a tensor: the last tokens against the same tokens alone,
+    whose state is what the 4,096 before them leave (a^4096 < e^-200)."""
+    need_gpu()
+    import linear_attention_recurrence_05_amd as kda
+    T, H, d, tail = 530000, 32, 128, 4160
+    assert T * H * d > 2 ** 31
+    gen = torch.Generator(device="cuda").manual_seed(19)
+    x = {n: torch.empty(1, T, H, d, dtype=BF, device="cuda").normal_(generator=gen) for n in "qkv"}
+    g = torch.full((H,), -0.05, device="cuda")
+    o, S_T = kda.linear_prefill(x["q"], x["k"], x["v"], g, 0.01)
+    end = {n: x[n][:, -tail:].contiguous() for n in "qkv"}
+    oe, Se = kda.linear_prefill(end["q"], end["k"], end["v"], g, 0.01)
+    torch.cuda.synchronize()
+    # both are the same sums in another order: rounding of the operands and the output
+    mag = kda.linear_prefill(end["q"].abs(), end["k"].abs(), end["v"].abs(), g, 0.01)
+    for a, b, m, tol in ((o[:, -64:], oe[:, -64:], mag[0][:, -64:], 2.0 ** -6), (S_T, Se, mag[1], 2.0 ** -14)):
+        assert ((a.double() - b.double()).abs() <= tol * m.double()).all()
+    del o, oe, mag, end
+    # gradients reach the first tokens from the end: the same on the first ones alone
+    dO = x["v"]
+    got = kda.linear_backward(x["q"], x["k"], x["v"], g, dO, 0.01, want_dS0=False)
+    head = {n: x[n][:, :tail].contiguous() for n in "qkv"}
+    want = kda.linear_backward(head["q"], head["k"], head["v"], g, head["v"], 0.01, want_dS0=False)
+    head = {n: t.abs() for n, t in head.items()}
+    mag = kda.linear_backward(head["q"], head["k"], head["v"], g, head["v"], 0.01, want_dS0=False)
+    torch.cuda.synchronize()
+    for n in ("dq", "dk", "dv"):
+        a, b, m = got[n][:, :64].double(), want[n][:, :64].double(), mag[n][:, :64].double()
+        assert ((a - b).abs() <= 2.0 ** -6 * m).all(), n
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_calls_on_a_given_stream(dtype):
+    """stream= as a torch stream and as its handle, with another one current."""
+    need_gpu()
+    import linear_attention_recurrence_05_amd as kda
+    x, gen = make(2, 700, 4, 2, 64, 64, dtype, seed=20)
+    dO = _rand(gen, *x["v"].shape).to(dtype)
+    args = (x["q"], x["k"], x["v"], x["g"])
+    want = [*kda.linear_prefill(*args, x["scale"], x["S0"]), *kda.linear_backward(*args, dO, x["scale"]).values()]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        got = [*kda.linear_prefill(*args, x["scale"], x["S0"], stream=stream),
+               *kda.linear_backward(*args, dO, x["scale"], stream=stream).values()]
+        s.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
 def bwd_ref(x):
     a = absolute(x)
     arg = ("q", "k", "v", "g", "scale", "dO", "S0", "dS_T", "lens")
