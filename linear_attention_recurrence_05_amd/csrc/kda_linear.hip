@@ -38,10 +38,14 @@ struct LinearSegs {
 
 // Up to three passes of the same sizes in one launch (the gradients), each
 // with its workspace [unit][R][DA * DB]: R - 1 segments' states, then the
-// initial one.
+// initial one, each as [DA / 4][DB] quads of rows (16 bytes a lane).  The first
+// launch runs the passes before `state`; a pass with ws_t reads the states of
+// another one, of [DB, DA], transposed.
 struct LinearJob {
     LinearPass pass[3];
     float* ws[3];
+    bool ws_t[3];
+    int passes, state;
     LinearSegs segs;
 };
 
@@ -98,8 +102,15 @@ __global__ __launch_bounds__(DB / NC * 4, 2) void linear_chunk_kernel(LinearJob 
     // ---- the state at the segment's start.  The final state may go where the
     // initial one came from, so with several segments only the first launch
     // reads that, and copies it.
-    auto slot = [&](int m) {
-        return reinterpret_cast<f32x4*>(job.ws[role] + ((size_t)unit * segs.R + m) * (DA * DB)) + wave * NC * 2 * KM * 64 + lane;
+    auto slot = [&](int m) { return job.ws[role] + ((size_t)unit * segs.R + m) * (DA * DB); };
+    // quad of rows of tile t in a slot, and the same rows of its transposed form
+    auto quad = [&](float* w, int t, int ct) -> f32x4& {
+        return reinterpret_cast<f32x4*>(w)[(8 * (t >> 1) + 2 * g + (t & 1)) * DB + col(ct)];
+    };
+    auto quad_t = [&](const float* w, int t, int ct) {
+        const int c = col(ct), row = 32 * (t >> 1) + 8 * g + 4 * (t & 1);
+        const float* q = w + ((size_t)(c >> 2) * DA + row) * 4 + (c & 3);
+        return f32x4{q[0], q[4], q[8], q[12]};
     };
     const bool direct = STATE || (seg == 0 && last);
     const float* in = p.S.in && (STATE ? seg == 0 : direct)
@@ -115,26 +126,28 @@ __global__ __launch_bounds__(DB / NC * 4, 2) void linear_chunk_kernel(LinearJob 
                 M[t][ct][i] = in ? in[p.in_t ? col(ct) * DA + ch : ch * DB + col(ct)] : 0.f;
             }
             if (STATE) {
-                if (in) slot(segs.R - 1)[(t * NC + ct) * 64] = M[t][ct];
+                if (in) quad(slot(segs.R - 1), t, ct) = M[t][ct];
                 M[t][ct] = zero4();
             }
         }
     if (!direct) {
-        if (p.S.in) {
-            const f32x4* w = slot(segs.R - 1);
-#pragma unroll
-            for (int t = 0; t < 2 * KM; ++t)
-#pragma unroll
-                for (int ct = 0; ct < NC; ++ct) M[t][ct] = w[(t * NC + ct) * 64];
-        }
         const float as = expf(lg * (float)segs.len);
-        for (int m = 0; m < seg; ++m) {
-            const f32x4* w = slot(m);
+        auto start = [&](auto transposed) {
+            auto add = [&](int m, float keep) {
+                float* w = slot(m);
 #pragma unroll
-            for (int t = 0; t < 2 * KM; ++t)
+                for (int t = 0; t < 2 * KM; ++t)
 #pragma unroll
-                for (int ct = 0; ct < NC; ++ct) M[t][ct] = as * M[t][ct] + w[(t * NC + ct) * 64];
-        }
+                    for (int ct = 0; ct < NC; ++ct)
+                        M[t][ct] = keep * M[t][ct] + (decltype(transposed)::value ? quad_t(w, t, ct) : quad(w, t, ct));
+            };
+            if (p.S.in) add(segs.R - 1, 0.f);
+            for (int m = 0; m < seg; ++m) add(m, as);
+        };
+        if (job.ws_t[role])
+            start(std::true_type{});
+        else
+            start(std::false_type{});
     }
 
     // ---- weights of a chunk of c steps
@@ -353,11 +366,11 @@ __global__ __launch_bounds__(DB / NC * 4, 2) void linear_chunk_kernel(LinearJob 
     }
 
     if constexpr (STATE) {
-        f32x4* w = slot(seg);
+        float* w = slot(seg);
 #pragma unroll
         for (int t = 0; t < 2 * KM; ++t)
 #pragma unroll
-            for (int ct = 0; ct < NC; ++ct) w[(t * NC + ct) * 64] = M[t][ct];
+            for (int ct = 0; ct < NC; ++ct) quad(w, t, ct) = M[t][ct];
     } else if (last && p.S.out) {
         float* out = p.S.out + ((size_t)(p.S.out_slot ? p.S.out_slot[b] : b) * p.H + h) * (DA * DB);
 #pragma unroll
@@ -396,23 +409,26 @@ __global__ __launch_bounds__(256) void linear_share_kernel(const float* __restri
 // is taken for each R and the least wins.  Its constants are measured: a chunk
 // takes `out` us in the second launch and `state` us in the first (latency,
 // until a CU has several workgroups; fp32's LDS leaves room for one, so they
-// run in rounds), the first launch 6 us of its own, and the states move at 5
-// TB/s.  B1 H32 T4096 d128 bf16: 197 us with one segment, 92 with 4, 63 with 8,
-// 78 with 16; B8 H32 T8192: 492 with one, 640 with 2; B4 H16 T2048 fp32: 328 with
-// one, 156 with 4, 202 with 16.
-static LinearSegs segments(int passes, int B, int T, int H, int da, int db, bool is_bf16) {
+// run in rounds), but a launch no less than its rows at 6 TB/s; the first
+// launch takes 6 us of its own, and the states move at 5 TB/s.  B1 H32 T4096 d128
+// bf16: 197 us with one segment, 92 with 4, 62 with 8, 78 with 16; B8 H32 T8192: 480
+// with one, 636 with 2; B4 H16 T2048 fp32: 328 with one, 156 with 4, 202 with 16.
+static LinearSegs segments(int passes, int states, int B, int T, int H, int da, int db, bool is_bf16) {
     const double units = (double)B * H * passes, size = da * db / 16384.0;
     const double out = is_bf16 ? 0.7 + 0.7 * size : 1.1 + 4.0 * size;
     const double state = is_bf16 ? 0.4 + 0.35 * size : 0.7 + 2.0 * size;
+    const double token = units * T * (da + db) * (is_bf16 ? 2 : 4) / 6e6;   // us to move y and u, or x and out
     LinearSegs best{1, (T + kLinChunk - 1) / kLinChunk * kLinChunk};
     double least = 0;
     for (int r = 1; r <= 32; ++r) {
         const int chunks = ((T + r - 1) / r + kLinChunk - 1) / kLinChunk, len = chunks * kLinChunk;
         const int R = (T + len - 1) / len;
         if (R != r) continue;
-        const double load = units * R / 256, busy = is_bf16 ? std::max(1.0, 0.65 * load) : std::ceil(load);
-        double us = chunks * out * busy;
-        if (R > 1) us += 6 + chunks * state * busy + units * da * db * 4 * (0.5 * R * (R - 1) + 2 * R) / 5e6;
+        auto busy = [&](double groups) { return is_bf16 ? std::max(1.0, 0.65 * groups / 256) : std::ceil(groups / 256); };
+        double us = std::max(chunks * out * busy(units * R), 2 * token);
+        if (R > 1)
+            us += 6 + std::max(chunks * state * busy(units * states / passes * (R - 1)), token * states / passes * (R - 1) / R) +
+                  units * da * db * 4 * (0.5 * R * (R - 1) + 2 * R) / 5e6;
         if (r == 1 || us < least) {
             least = us;
             best = {R, len};
@@ -421,22 +437,23 @@ static LinearSegs segments(int passes, int B, int T, int H, int da, int db, bool
     return best;
 }
 
-static size_t segs_bytes(int passes, int B, int T, int H, int da, int db, bool is_bf16) {
-    const int R = segments(passes, B, T, H, da, db, is_bf16).R;
+static size_t segs_bytes(int passes, int states, int B, int T, int H, int da, int db, bool is_bf16) {
+    const int R = segments(passes, states, B, T, H, da, db, is_bf16).R;
     return R > 1 ? (size_t)B * H * R * da * db * sizeof(float) : 0;
 }
 
 template <typename E, int DA, int DB, int NC, int NP>
-static hipError_t launch_job_n(const LinearJob& job, int passes, hipStream_t stream) {
-    const unsigned groups = (unsigned)(job.pass[0].B * job.pass[0].H) * passes;
+static hipError_t launch_job_n(const LinearJob& job, hipStream_t stream) {
+    const unsigned units = (unsigned)(job.pass[0].B * job.pass[0].H);
     const dim3 block(DB / NC * 4);
     if (job.segs.R > 1) {
-        hipLaunchKernelGGL((linear_chunk_kernel<E, DA, DB, NC, 1, true>), dim3(groups * (job.segs.R - 1)), block, 0, stream,
-                           job);
+        hipLaunchKernelGGL((linear_chunk_kernel<E, DA, DB, NC, 1, true>), dim3(units * job.state * (job.segs.R - 1)), block,
+                           0, stream, job);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((linear_chunk_kernel<E, DA, DB, NC, NP, false>), dim3(groups * job.segs.R), block, 0, stream, job);
+    hipLaunchKernelGGL((linear_chunk_kernel<E, DA, DB, NC, NP, false>), dim3(units * job.passes * job.segs.R), block, 0,
+                       stream, job);
     return hipGetLastError();
 }
 
@@ -450,61 +467,59 @@ static hipError_t launch_job_n(const LinearJob& job, int passes, hipStream_t str
 // chunk's arithmetic, which only a pass of a few chunks, latency for the most
 // part, has to spare.
 template <typename E, int DA, int DB>
-static hipError_t launch_job_d(const LinearJob& job, int passes, hipStream_t stream) {
+static hipError_t launch_job_d(const LinearJob& job, hipStream_t stream) {
     constexpr int NP = sizeof(E) == 2 ? 1 : 3;
     if constexpr (DB == 128) {
-        if ((long long)job.pass[0].B * job.pass[0].H * passes >= 96)
-            return launch_job_n<E, DA, DB, 2, NP>(job, passes, stream);
+        if ((long long)job.pass[0].B * job.pass[0].H * job.passes >= 96)
+            return launch_job_n<E, DA, DB, 2, NP>(job, stream);
     }
     if constexpr (sizeof(E) == 2) {
-        if (job.segs.len <= 4 * kLinChunk) return launch_job_n<E, DA, DB, 1, 2>(job, passes, stream);
+        if (job.segs.len <= 4 * kLinChunk) return launch_job_n<E, DA, DB, 1, 2>(job, stream);
     }
-    return launch_job_n<E, DA, DB, 1, NP>(job, passes, stream);
+    return launch_job_n<E, DA, DB, 1, NP>(job, stream);
 }
 
 template <typename E, int DA>
-static hipError_t launch_job_a(const LinearJob& job, int passes, hipStream_t stream) {
+static hipError_t launch_job_a(const LinearJob& job, hipStream_t stream) {
     switch (job.pass[0].db) {
-        case 32: return launch_job_d<E, DA, 32>(job, passes, stream);
-        case 64: return launch_job_d<E, DA, 64>(job, passes, stream);
-        default: return launch_job_d<E, DA, 128>(job, passes, stream);
+        case 32: return launch_job_d<E, DA, 32>(job, stream);
+        case 64: return launch_job_d<E, DA, 64>(job, stream);
+        default: return launch_job_d<E, DA, 128>(job, stream);
     }
 }
 
 template <typename E>
-static hipError_t launch_job_e(const LinearJob& job, int passes, hipStream_t stream) {
+static hipError_t launch_job_e(const LinearJob& job, hipStream_t stream) {
     switch (job.pass[0].da) {
-        case 32: return launch_job_a<E, 32>(job, passes, stream);
-        case 64: return launch_job_a<E, 64>(job, passes, stream);
-        default: return launch_job_a<E, 128>(job, passes, stream);
+        case 32: return launch_job_a<E, 32>(job, stream);
+        case 64: return launch_job_a<E, 64>(job, stream);
+        default: return launch_job_a<E, 128>(job, stream);
     }
 }
 
-static hipError_t launch_job(const LinearJob& job, int passes, hipStream_t stream) {
-    return job.pass[0].is_bf16 ? launch_job_e<bf16>(job, passes, stream) : launch_job_e<float>(job, passes, stream);
+static hipError_t launch_job(const LinearJob& job, hipStream_t stream) {
+    return job.pass[0].is_bf16 ? launch_job_e<bf16>(job, stream) : launch_job_e<float>(job, stream);
 }
 
 size_t linear_prefill_ws_bytes(int B, int T, int H, int da, int db, bool is_bf16) {
-    return segs_bytes(1, B, T, H, da, db, is_bf16);
+    return segs_bytes(1, 1, B, T, H, da, db, is_bf16);
 }
 
 hipError_t launch_linear_prefill(const LinearPass& p, void* ws, hipStream_t stream) {
-    return launch_job(LinearJob{{p}, {(float*)ws}, segments(1, p.B, p.T, p.H, p.da, p.db, p.is_bf16)}, 1, stream);
+    return launch_job(LinearJob{{p}, {(float*)ws}, {}, 1, 1, segments(1, 1, p.B, p.T, p.H, p.da, p.db, p.is_bf16)}, stream);
 }
 
-// The three passes' segment states, then (shared heads) dq and dk of every
+// The segment states of S and of R, then (shared heads) dq and dk of every
 // head in fp32, summed afterwards.
 size_t linear_backward_ws_bytes(int B, int T, int H, int Hk, int dk, int dv, bool is_bf16) {
-    return 3 * segs_bytes(3, B, T, H, dk, dv, is_bf16) + (H == Hk ? 0 : 2 * (size_t)B * T * H * dk * sizeof(float));
+    return 2 * segs_bytes(3, 2, B, T, H, dk, dv, is_bf16) + (H == Hk ? 0 : 2 * (size_t)B * T * H * dk * sizeof(float));
 }
 
 hipError_t launch_linear_backward(const LinearBackward& a, void* ws, hipStream_t stream) {
     const bool shared = a.H != a.Hk;
     const int n = shared ? a.H : a.Hk;
-    const size_t seg_bytes = segs_bytes(3, a.B, a.T, a.H, a.dk_, a.dv_, a.is_bf16);
-    float* seg[3];
-    for (int i = 0; i < 3; ++i) seg[i] = (float*)((char*)ws + i * seg_bytes);
-    float* part = (float*)((char*)ws + 3 * seg_bytes);
+    const size_t seg_bytes = segs_bytes(3, 2, a.B, a.T, a.H, a.dk_, a.dv_, a.is_bf16);
+    float *seg_s = (float*)ws, *seg_r = (float*)((char*)ws + seg_bytes), *part = (float*)((char*)ws + 2 * seg_bytes);
     const size_t rows = (size_t)a.B * a.T;
     const LinearPass dq{{a.dO, a.H}, {a.v, a.H}, {a.k, a.Hk}, shared ? part : a.dq, n, shared || !a.is_bf16, a.g,
                         a.scale, 1.0f, dense_state(a.S0, nullptr), true, a.lens, false, a.B, a.T, a.H, a.dv_, a.dk_,
@@ -514,14 +529,15 @@ hipError_t launch_linear_backward(const LinearBackward& a, void* ws, hipStream_t
                         a.B, a.T, a.H, a.dv_, a.dk_, a.is_bf16};
     const LinearPass dv{{a.k, a.Hk}, {a.q, a.Hk}, {a.dO, a.H}, a.dv, a.H, !a.is_bf16, a.g, 1.0f, a.scale,
                         dense_state(a.dST, a.dS0), false, a.lens, true, a.B, a.T, a.H, a.dk_, a.dv_, a.is_bf16};
-    const LinearSegs segs = segments(3, a.B, a.T, a.H, a.dk_, a.dv_, a.is_bf16);
+    // dk's states are dv's, transposed
+    const LinearSegs segs = segments(3, 2, a.B, a.T, a.H, a.dk_, a.dv_, a.is_bf16);
     hipError_t e;
     if (a.dk_ == a.dv_) {                                    // one launch for the three
-        if ((e = launch_job(LinearJob{{dq, dk, dv}, {seg[0], seg[1], seg[2]}, segs}, 3, stream)) != hipSuccess) return e;
-    } else {
-        if ((e = launch_job(LinearJob{{dq, dk}, {seg[0], seg[1]}, segs}, 2, stream)) != hipSuccess) return e;
-        if ((e = launch_job(LinearJob{{dv}, {seg[2]}, segs}, 1, stream)) != hipSuccess) return e;
+        e = launch_job(LinearJob{{dq, dv, dk}, {seg_s, seg_r, seg_r}, {false, false, true}, 3, 2, segs}, stream);
+    } else if ((e = launch_job(LinearJob{{dv}, {seg_r}, {}, 1, 1, segs}, stream)) == hipSuccess) {
+        e = launch_job(LinearJob{{dq, dk}, {seg_s, seg_r}, {false, true}, 2, 1, segs}, stream);
     }
+    if (e != hipSuccess) return e;
     if (!shared) return hipSuccess;
     const size_t count = rows * a.Hk * a.dk_;
     const dim3 grid((unsigned)std::min<size_t>((2 * count + 255) / 256, 1 << 14));
