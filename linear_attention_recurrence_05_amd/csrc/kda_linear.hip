@@ -45,7 +45,7 @@ struct LinearJob {
     LinearPass pass[3];
     float* ws[3];
     bool ws_t[3];
-    int passes, state;
+    int passes, state, shared;   // shared: heads that share one of q and k
     LinearSegs segs;
 };
 
@@ -80,7 +80,14 @@ __global__ __launch_bounds__(DB / NC * 4, 2) void linear_chunk_kernel(LinearJob 
 
     const LinearSegs segs = job.segs;
     const int units = job.pass[0].B * job.pass[0].H, nseg = STATE ? segs.R - 1 : segs.R;
-    const int unit = blockIdx.x % units, at = blockIdx.x / units, seg = at % nseg, role = at / nseg;
+    // The heads that share q and k, and the passes, of one segment follow each
+    // other on one XCD (workgroups go round the eight), whose L2 then serves what
+    // they read in common.
+    const int near = job.shared * (STATE ? job.state : job.passes), groups = units / job.shared * nseg;
+    const int whole = groups / 8 * 8, x = blockIdx.x, rest = x - whole * near;
+    const int group = rest < 0 ? x / 8 / near * 8 + x % 8 : whole + rest / near;
+    const int at = rest < 0 ? x / 8 % near : rest % near, role = at / job.shared;
+    const int seg = group / (units / job.shared), unit = group % (units / job.shared) * job.shared + at % job.shared;
     const LinearPass& p = job.pass[role];
     const int b = unit / p.H, h = unit % p.H;
     if (p.S.skip(b)) return;
@@ -403,32 +410,50 @@ __global__ __launch_bounds__(256) void linear_share_kernel(const float* __restri
 
 // ------------------------------------------------------------------ launches
 
+// Column tiles a wave holds.  128 columns as eight waves of one tile or four of
+// two: eight hide a chunk's latencies better (B1 H32 T1024 bf16 30 against 34
+// us), four form the pair weights half as often, which counts where every CU has
+// work throughout (B8 H32 T8192 519 against 492 us, gradients of B1 H32 T4096 165
+// against 151).
+static int wave_tiles(int passes, int B, int H, int db) {
+    return db == 128 && (long long)B * H * passes >= 96 ? 2 : 1;
+}
+
 // Segments of a sequence.  One segment leaves CUs idle where there are few
 // (b, h); R of them cost a first launch over the tokens, and every workgroup
 // of the second reads the states before its own.  The estimate below, in us,
 // is taken for each R and the least wins.  Its constants are measured: a chunk
-// takes `out` us in the second launch and `state` us in the first (latency,
-// until a CU has several workgroups; fp32's LDS leaves room for one, so they
-// run in rounds), but a launch no less than its rows at 6 TB/s; the first
-// launch takes 6 us of its own, and the states move at 5 TB/s.  B1 H32 T4096 d128
-// bf16: 197 us with one segment, 92 with 4, 62 with 8, 78 with 16; B8 H32 T8192: 480
-// with one, 636 with 2; B4 H16 T2048 fp32: 328 with one, 156 with 4, 202 with 16.
-static LinearSegs segments(int passes, int states, int B, int T, int H, int da, int db, bool is_bf16) {
-    const double units = (double)B * H * passes, size = da * db / 16384.0;
+// takes `out` us in the second launch and `state` us in the first where each CU
+// has one workgroup, 0.3 of that more for another on the CU (eight waves fit;
+// fp32's LDS takes one workgroup), and workgroups beyond that wait for a round
+// of their own; a launch takes no less than its rows at 5.2 TB/s, and as much
+// longer as the busiest CU has more than its share; the first one takes 6 us of
+// its own, and the states move at 8 TB/s.  Of a padded batch three fifths of the
+// workgroups are taken to have tokens.  B1 H32 T4096 d128 bf16: 197 us
+// with one segment, 93 with 4, 62 with 8, 92 with 10; its gradients: 204 with one,
+// 134 with 4, 116 with 5, 139 with 6; B8 H32 T8192: 477 with one, 636 with 2; B4 H16
+// T2048 fp32: 328 with one, 156 with 4, 202 with 16.
+static LinearSegs segments(int passes, int states, int B, int T, int H, int da, int db, bool is_bf16, bool padded) {
+    const double units = (double)B * H * passes * (padded ? 0.6 : 1.0), size = da * db / 16384.0;
     const double out = is_bf16 ? 0.7 + 0.7 * size : 1.1 + 4.0 * size;
     const double state = is_bf16 ? 0.4 + 0.35 * size : 0.7 + 2.0 * size;
-    const double token = units * T * (da + db) * (is_bf16 ? 2 : 4) / 6e6;   // us to move y and u, or x and out
+    const double token = units * T * (da + db) * (is_bf16 ? 2 : 4) / 5.2e6;   // us to move y and u, or x and out
+    const int fit = is_bf16 ? 8 * 16 * wave_tiles(passes, B, H, db) / db : 1;
+    auto busy = [&](double groups) {
+        const double round = 256.0 * fit, rounds = std::floor(groups / round), rest = groups - rounds * round;
+        return rounds * (1 + 0.3 * (fit - 1)) + (rest > 0 ? 1 + 0.3 * (std::ceil(rest / 256) - 1) : 0);
+    };
     LinearSegs best{1, (T + kLinChunk - 1) / kLinChunk * kLinChunk};
     double least = 0;
     for (int r = 1; r <= 32; ++r) {
         const int chunks = ((T + r - 1) / r + kLinChunk - 1) / kLinChunk, len = chunks * kLinChunk;
         const int R = (T + len - 1) / len;
         if (R != r) continue;
-        auto busy = [&](double groups) { return is_bf16 ? std::max(1.0, 0.65 * groups / 256) : std::ceil(groups / 256); };
-        double us = std::max(chunks * out * busy(units * R), 2 * token);
+        const double share = units * R / 256;
+        double us = std::max(chunks * out * busy(units * R), 2 * token * std::max(1.0, std::ceil(share) / share));
         if (R > 1)
             us += 6 + std::max(chunks * state * busy(units * states / passes * (R - 1)), token * states / passes * (R - 1) / R) +
-                  units * da * db * 4 * (0.5 * R * (R - 1) + 2 * R) / 5e6;
+                  units * da * db * 4 * (0.5 * R * (R - 1) + 2 * R) / 8e6;
         if (r == 1 || us < least) {
             least = us;
             best = {R, len};
@@ -437,8 +462,10 @@ static LinearSegs segments(int passes, int states, int B, int T, int H, int da, 
     return best;
 }
 
+// Workspace of one pass's segments, for a batch padded or not.
 static size_t segs_bytes(int passes, int states, int B, int T, int H, int da, int db, bool is_bf16) {
-    const int R = segments(passes, states, B, T, H, da, db, is_bf16).R;
+    const int R = std::max(segments(passes, states, B, T, H, da, db, is_bf16, false).R,
+                           segments(passes, states, B, T, H, da, db, is_bf16, true).R);
     return R > 1 ? (size_t)B * H * R * da * db * sizeof(float) : 0;
 }
 
@@ -457,10 +484,6 @@ static hipError_t launch_job_n(const LinearJob& job, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// 128 columns as eight waves of one tile or four of two: eight hide a chunk's
-// latencies better (B1 H32 T1024 bf16 30 against 34 us), four form the pair
-// weights half as often, which counts where every CU has work throughout (B8
-// H32 T8192 519 against 492 us, gradients of B1 H32 T4096 165 against 151).
 // bf16: the state and the pair weights enter their products as one bf16 term
 // each, which leaves half a step of bf16 on each part of the output's sum
 // beside its own rounding.  A second term removes that and costs a fifth of a
@@ -470,7 +493,7 @@ template <typename E, int DA, int DB>
 static hipError_t launch_job_d(const LinearJob& job, hipStream_t stream) {
     constexpr int NP = sizeof(E) == 2 ? 1 : 3;
     if constexpr (DB == 128) {
-        if ((long long)job.pass[0].B * job.pass[0].H * job.passes >= 96)
+        if (wave_tiles(job.passes, job.pass[0].B, job.pass[0].H, DB) == 2)
             return launch_job_n<E, DA, DB, 2, NP>(job, stream);
     }
     if constexpr (sizeof(E) == 2) {
@@ -506,7 +529,7 @@ size_t linear_prefill_ws_bytes(int B, int T, int H, int da, int db, bool is_bf16
 }
 
 hipError_t launch_linear_prefill(const LinearPass& p, void* ws, hipStream_t stream) {
-    return launch_job(LinearJob{{p}, {(float*)ws}, {}, 1, 1, segments(1, 1, p.B, p.T, p.H, p.da, p.db, p.is_bf16)}, stream);
+    return launch_job(LinearJob{{p}, {(float*)ws}, {}, 1, 1, p.H / p.x.n, segments(1, 1, p.B, p.T, p.H, p.da, p.db, p.is_bf16, p.lens != nullptr)}, stream);
 }
 
 // The segment states of S and of R, then (shared heads) dq and dk of every
@@ -530,12 +553,12 @@ hipError_t launch_linear_backward(const LinearBackward& a, void* ws, hipStream_t
     const LinearPass dv{{a.k, a.Hk}, {a.q, a.Hk}, {a.dO, a.H}, a.dv, a.H, !a.is_bf16, a.g, 1.0f, a.scale,
                         dense_state(a.dST, a.dS0), false, a.lens, true, a.B, a.T, a.H, a.dk_, a.dv_, a.is_bf16};
     // dk's states are dv's, transposed
-    const LinearSegs segs = segments(3, 2, a.B, a.T, a.H, a.dk_, a.dv_, a.is_bf16);
+    const LinearSegs segs = segments(3, 2, a.B, a.T, a.H, a.dk_, a.dv_, a.is_bf16, a.lens != nullptr);
     hipError_t e;
     if (a.dk_ == a.dv_) {                                    // one launch for the three
-        e = launch_job(LinearJob{{dq, dv, dk}, {seg_s, seg_r, seg_r}, {false, false, true}, 3, 2, segs}, stream);
-    } else if ((e = launch_job(LinearJob{{dv}, {seg_r}, {}, 1, 1, segs}, stream)) == hipSuccess) {
-        e = launch_job(LinearJob{{dq, dk}, {seg_s, seg_r}, {false, true}, 2, 1, segs}, stream);
+        e = launch_job(LinearJob{{dq, dv, dk}, {seg_s, seg_r, seg_r}, {false, false, true}, 3, 2, a.H / a.Hk, segs}, stream);
+    } else if ((e = launch_job(LinearJob{{dv}, {seg_r}, {}, 1, 1, a.H / a.Hk, segs}, stream)) == hipSuccess) {
+        e = launch_job(LinearJob{{dq, dk}, {seg_s, seg_r}, {false, true}, 2, 1, a.H / a.Hk, segs}, stream);
     }
     if (e != hipSuccess) return e;
     if (!shared) return hipSuccess;
