@@ -61,6 +61,11 @@ struct LinearJob {
 // fp32; NP is the number for the state and the pair weights in their products
 // with x and u (see launch_job_d).  STATE: only the state of a segment
 // from zero, into the workspace.
+// What bounds it: where every CU has a workgroup, the rows (B8 H32 T8192 d128
+// bf16 in 477 us, 2.19 GB moved, 4.6 TB/s against 4.8 of a large copy; the matrix
+// cores are busy a third of that); where sequences are few or short, a chunk's
+// own chain (stage, products, barrier: 1.4 us, of which MFMA and VALU issue fill
+// two thirds).
 template <typename E, int DA, int DB, int NC, int NP, bool STATE>
 __global__ __launch_bounds__(DB / NC * 4, 2) void linear_chunk_kernel(LinearJob job) {
     constexpr int C = kLinChunk, NT = DB / NC * 4, KM = DA / 32;
@@ -428,13 +433,13 @@ static int wave_tiles(int passes, int B, int H, int db) {
 // fp32's LDS takes one workgroup), and workgroups beyond that wait for a round
 // of their own; a launch takes no less than its rows at 5.2 TB/s, and as much
 // longer as the busiest CU has more than its share; the first one takes 6 us of
-// its own, and the states move at 8 TB/s.  Of a padded batch three fifths of the
+// its own, and the states move at 8 TB/s.  Of a padded batch three quarters of the
 // workgroups are taken to have tokens.  B1 H32 T4096 d128 bf16: 197 us
 // with one segment, 93 with 4, 62 with 8, 92 with 10; its gradients: 204 with one,
 // 134 with 4, 116 with 5, 139 with 6; B8 H32 T8192: 477 with one, 636 with 2; B4 H16
 // T2048 fp32: 328 with one, 156 with 4, 202 with 16.
 static LinearSegs segments(int passes, int states, int B, int T, int H, int da, int db, bool is_bf16, bool padded) {
-    const double units = (double)B * H * passes * (padded ? 0.6 : 1.0), size = da * db / 16384.0;
+    const double units = (double)B * H * passes * (padded ? 0.75 : 1.0), size = da * db / 16384.0;
     const double out = is_bf16 ? 0.7 + 0.7 * size : 1.1 + 4.0 * size;
     const double state = is_bf16 ? 0.4 + 0.35 * size : 0.7 + 2.0 * size;
     const double token = units * T * (da + db) * (is_bf16 ? 2 : 4) / 5.2e6;   // us to move y and u, or x and out
