@@ -9,9 +9,12 @@
 // pair step and its block are those of kda_pair.hpp, unchanged.
 //
 // For few sequence-heads (B * H <= CUs / 8), every unit u = (b, h) gets
-// D / 16 = 8 workgroups, one per 16-column tile of the state, all on the
-// XCD u mod 8 (workgroups are dispatched round-robin over the XCDs; each
-// workgroup checks the XCD it runs on).  The grid is at most one workgroup
+// D / 16 = 8 workgroups, one per 16-column tile of the state, with equal ids
+// mod 8 and so all on one XCD: workgroups are dispatched round-robin over the
+// XCDs, from an XCD that differs between hardware queues (and changes for a
+// queue as others come into use).  A workgroup on another XCD than the rest of
+// its unit would see none of their flags, which live in their L2: its waits,
+// and theirs for its pairs, would give up.  The grid is at most one workgroup
 // per CU and every workgroup fits a CU by itself, so the whole grid is
 // resident at once, which the waits between workgroups need.  A workgroup:
 //   waves 0..2  producers: pairs p = tile + 8 (w + 3 j) of the unit, each
@@ -78,11 +81,6 @@ struct RingCfg {
     static_assert(LDS <= 160 * 1024 - 64, "LDS of one workgroup");
     static_assert(P::BYTES % 16 == 0, "16-byte copies");
 };
-
-// The XCD this wave runs on (hardware register XCC_ID, bits 3:0).
-__device__ __forceinline__ int xcd_id() {
-    return __builtin_amdgcn_s_getreg(20 | (0 << 6) | ((4 - 1) << 11)) & 15;
-}
 
 // Zero the optimiser cannot see through, so an atomic add of it stays an
 // atomic (an add of a literal zero may become a plain load).
@@ -279,10 +277,9 @@ __global__ __launch_bounds__((RingCfg<E, D>::THREADS)) void pair_ring_kernel(
     // lready: last pair the gate saw published; lfree: last pair every tile
     // of the unit has taken (its slot may be refilled); ldone[c]: last pair
     // consumer c (0 chain, 1 output) has taken from the ring; uready / udone:
-    // the entries between chain and output wave; lbad: the workgroup is not
-    // on its unit's XCD (a gate that gives up stores kGaveUp to lready and
-    // lfree instead)
-    __shared__ int lready, lfree, ldone[2], uready, udone, lbad;
+    // the entries between chain and output wave (a gate that gives up stores
+    // kGaveUp to lready and lfree)
+    __shared__ int lready, lfree, ldone[2], uready, udone;
     int u, ct;
     if (!map_unit(NCT, B * H, u, ct)) return;   // uniform over the workgroup
     const int b = u / H, h = u % H;
@@ -299,7 +296,6 @@ __global__ __launch_bounds__((RingCfg<E, D>::THREADS)) void pair_ring_kernel(
         lready = lfree = -1;
         ldone[0] = ldone[1] = -1;
         uready = udone = -1;
-        lbad = xcd_id() != (int)(blockIdx.x & 7);
     }
     // the chain starts from the tile's initial state (read before the
     // barrier: S_T may alias S0)
@@ -429,7 +425,7 @@ __global__ __launch_bounds__((RingCfg<E, D>::THREADS)) void pair_ring_kernel(
         POps<E, D> c0, c1;
         u32x2 va0, vb0, va1, vb1;
         int seen_ready = -1, seen_udone = -1, ahead_ready = -1, ahead_udone = -1;
-        bool bad = __hip_atomic_load(&lbad, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) != 0;
+        bool bad = false;
         bool live = lds_wait_seen(&lready, 0, seen_ready, true, bad);
         // (pair 0's loads in the order a step issues them)
         ring_load_v<D>(v, b, h, T, H, col0, 0, va0, vb0);
@@ -499,7 +495,7 @@ __global__ __launch_bounds__((RingCfg<E, D>::THREADS)) void pair_ring_kernel(
     // ------------------------------------------------------------ outputs
     POps<E, D> c0, c1;
     int seen_ready = -1, seen_u = -1;
-    bool bad = __hip_atomic_load(&lbad, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) != 0;
+    bool bad = false;
     bool live = lds_wait_seen(&lready, 0, seen_ready, true, bad);
     ring_load_out<E, D>(c0, rring, 0);
     auto step = [&](POps<E, D>& c, POps<E, D>& cn, int s) {
