@@ -398,7 +398,7 @@ kda_status kda_intra_chunk(const void *q, const void *k, const void *z,
  * - g [H] fp32 is the log-decay of each head, a constant of the layer: it has
  *   no gradient.  g <= 0 is expected; values below -10000 (also -infinity)
  *   are taken as -10000, for which a is exactly 0 and a^0 is 1.
- * - B * H <= 2^23; scale must be finite.
+ * - B * H <= 2^22; scale must be finite.
  * - lens [B] int32 in device memory (NULL: all T) is each sequence's token
  *   count in a batch padded to T.  Values are clamped to [0, T].  Tokens at
  *   or past it are neither read nor written by any kernel (their rows of o,

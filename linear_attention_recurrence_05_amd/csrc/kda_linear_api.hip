@@ -18,8 +18,9 @@ kda_status check_dtype(kda_dtype dt) {
 }
 
 // Most (b, h) of a linear-attention call: one workgroup of up to 512 threads
-// each, and a launch holds fewer than 2^32 threads.
-constexpr long long kMaxUnits = 1LL << 23;
+// each, in the gradients three of up to 256 (so many are never split into
+// segments), and a launch holds fewer than 2^32 threads.
+constexpr long long kMaxUnits = 1LL << 22;
 
 // Sizes of a linear-attention call, in elements.
 struct Sizes {
@@ -36,7 +37,7 @@ kda_status check_sizes(int B, int T, int H, int H_k, int d_k, int d_v, kda_dtype
     size_t nel, ntok;
     if ((s = check_shape(B, T, H, d_k > d_v ? d_k : d_v, nel, ntok)) != KDA_OK) return s;
     if ((long long)B * H > kMaxUnits)
-        return fail(KDA_ERR_INVALID_SHAPE, "B*H = %lld is too large (limit 2^23)", (long long)B * H);
+        return fail(KDA_ERR_INVALID_SHAPE, "B*H = %lld is too large (limit 2^22)", (long long)B * H);
     if (H_k < 1 || H_k > H || H % H_k != 0)
         return fail(KDA_ERR_INVALID_SHAPE, "H_k=%d must divide H=%d", H_k, H);
     n.tok = (size_t)B * T;

@@ -569,3 +569,32 @@ def test_calls_repeat_bit_for_bit(dtype):
     for _ in range(3):
         for a, b in zip(first, run()):
             assert torch.equal(a, b)
+
+
+def test_the_most_sequences():
+    """2^22 sequences of one token, from no state: o = scale (q . k) v, dq = scale (v . dO) k,
+    dk = scale (v . dO) q, dv = scale (q . k) dO, and the same as a tree of one node over one slot
+    of zeros.  Inputs are small integers with d = 32, so every product and sum is exact and only
+    the output's rounding is left, at most half a step of bf16; of a tree, whose pair weight is
+    one bf16 value for so many sequences, that weight's rounding too (and the two's product)."""
+    need_gpu()
+    import linear_attention_recurrence_05_amd as kda
+    say("2^22 sequences")
+    B, d, scale = 1 << 22, 32, 0.25
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    q, k, v, dO = (torch.randint(-4, 5, (B, 1, 1, d), generator=gen, device="cuda").to(BF) for _ in range(4))
+    g = torch.zeros(1, device="cuda")
+    o, _ = kda.linear_prefill(q, k, v, g, scale, want_state=False)
+    grads = kda.linear_backward(q, k, v, g, dO, scale, want_dS0=False)
+    tree = torch.empty_like(v)
+    kda.kda_linear_tree_paged(q, k, v, g, scale, torch.zeros(1, 1, d, d, device="cuda"),
+                                     torch.zeros(B, dtype=torch.int32, device="cuda"),
+                                     torch.full((B, 1), -1, dtype=torch.int32, device="cuda"), tree)
+    qk = scale * (q.float() * k.float()).sum(-1, keepdim=True)
+    vo = scale * (v.float() * dO.float()).sum(-1, keepdim=True)
+    half = torch.finfo(BF).eps / 2
+    for name, got, want, tol in (("o", o, qk * v.float(), half), ("tree", tree, qk * v.float(), 2 * half + half ** 2),
+                                 ("dq", grads["dq"], vo * k.float(), half), ("dk", grads["dk"], vo * q.float(), half),
+                                 ("dv", grads["dv"], qk * dO.float(), half)):
+        worst = ((got.float() - want).abs() - want.abs() * tol).max().item()
+        assert worst <= 0, (name, worst)

@@ -218,3 +218,11 @@ def test_the_binding_refuses_tables_norms_and_dtypes(monkeypatch):
         args = {**dict(q=q, k=k, positions=pos, inv_freq=f), **kw}
         with pytest.raises(ValueError, match=match):
             kda.qk_norm_rope(**args)
+
+
+def test_more_sequences_than_a_launch_holds_are_refused():
+    for name in LINEAR:
+        refuse(name, "KDA_ERR_INVALID_SHAPE", B=(1 << 20) + 1, H=4, **({"T": 1} if "T" in CALLS[name] else {}))
+    for f in (kda.kda_linear_prefill_workspace_bytes, kda.kda_linear_backward_workspace_bytes):
+        assert f((1 << 22) + 1, 1, 1, 1, 32, 32, kda.KDA_BF16) == 0
+        assert f(1 << 22, 65, 1, 1, 128, 128, kda.KDA_BF16) == 0       # one segment: three workgroups each
