@@ -2,6 +2,7 @@
 // points of include/kda.h: argument validation (entirely on the host, before
 // any HIP call) and dispatch to the kernel launchers.
 #include <cmath>
+#include <cstring>
 
 #include "kda_host.hpp"
 #include "kda_linear.hpp"
@@ -55,7 +56,8 @@ kda_status check_pool(int n_slots, int H) {
 }
 
 // One pointer of a call.  Outputs (and the workspace) may overlap no other
-// range, but for an input that an output may equal exactly (in place).
+// range, but for the one input that an output may equal exactly (in place):
+// another input given the same address would be overwritten before it is read.
 struct Ptr {
     const char* name;
     const void* p;
@@ -63,7 +65,7 @@ struct Ptr {
     unsigned align;
     bool required;
     bool output;
-    const void* same;   // the input this output may equal exactly (null: none)
+    const char* same;   // the name of the input this output may equal exactly (null: none)
 };
 
 kda_status check_call(const Ptr* r, int n) {
@@ -78,9 +80,7 @@ kda_status check_call(const Ptr* r, int n) {
     for (int out = 0; out < n; ++out) {
         if (!r[out].output) continue;
         for (int i = 0; i < n; ++i) {
-            if (i == out || (r[out].same && r[i].p == r[out].same && r[out].p == r[out].same &&
-                             r[i].bytes == r[out].bytes && !r[i].output))
-                continue;
+            if (i == out || (r[out].same && r[i].p == r[out].p && !std::strcmp(r[i].name, r[out].same))) continue;
             if (overlap(Range{r[out].name, r[out].p, r[out].bytes, 1},
                         Range{r[i].name, r[i].p, r[i].bytes, 1}))
                 return fail(KDA_ERR_ALIASING, "%s overlaps %s", r[out].name, r[i].name);
@@ -121,7 +121,7 @@ kda_status prefill(const char* where, const void* q, const void* k, const void* 
                      {"slots_out", slots_out, (size_t)B * 4, 4, false, false, nullptr},
                      {"pool", pool, pool_bytes, 16, paged, true, nullptr},
                      {"o", o, n.vo * es, 16, true, true, nullptr},
-                     {"S_T", S_T, n.state * 4, 16, false, true, S0},
+                     {"S_T", S_T, n.state * 4, 16, false, true, "S0"},
                      {"workspace", ws, need, 16, need > 0, true, nullptr}};
     if ((s = check_call(r, 12)) != KDA_OK || (s = check_workspace(ws_bytes, need)) != KDA_OK) return s;
     const kda::LinearPass p{{q, H_k}, {k, H_k}, {v, H}, o, H, dt == KDA_F32, g, scale, 1.0f,
@@ -205,7 +205,7 @@ kda_status commit(const char* where, const void* k, const void* v, const float* 
                      {"slots_in", slots_in, (size_t)B * 4, 4, paged, false, nullptr},
                      {"slots_out", slots_out, (size_t)B * 4, 4, paged, false, nullptr},
                      {"S", paged ? nullptr : S, n.state * 4, 16, !paged, false, nullptr},
-                     {paged ? "pool" : "S_out", S_out, S_bytes, 16, true, true, paged ? nullptr : S}};
+                     {paged ? "pool" : "S_out", S_out, S_bytes, 16, true, true, paged ? nullptr : "S"}};
     if ((s = check_call(r, 9)) != KDA_OK) return s;
     kda::StateIO io = paged ? pool_state(S_out, n_slots, slots_in, slots_out) : kda::dense_state(S, S_out);
     const kda::LinearTree a{nullptr, k, v, g, 1.0f, io, parent, accepted, nullptr, B, T, H, H_k,
@@ -360,8 +360,8 @@ kda_status kda_qk_norm_rope(const void* q, const void* k, const float* w_q, cons
                      {"w_k", w_k, w, 4, false, false, nullptr},
                      {"positions", positions, (size_t)B * T * 4, 4, rot > 0, false, nullptr},
                      {"inv_freq", inv_freq, (size_t)rot * 2, 4, rot > 0, false, nullptr},
-                     {"y_q", y_q, nq * es, 16, true, true, q},
-                     {"y_k", y_k, nk * es, 16, true, true, k}};
+                     {"y_q", y_q, nq * es, 16, true, true, "q"},
+                     {"y_k", y_k, nk * es, 16, true, true, "k"}};
     if ((s = check_call(r, 8)) != KDA_OK) return s;
     const kda::NormRope a{q, k, w_q, w_k, positions, inv_freq, norm == KDA_NORM_RMS, eps, rot,
                           interleaved == 1, nullptr, nullptr, y_q, y_k, nullptr, nullptr,
@@ -396,8 +396,8 @@ kda_status kda_qk_norm_rope_backward(const void* q, const void* k, const float* 
                      {"inv_freq", inv_freq, (size_t)rot * 2, 4, rot > 0, false, nullptr},
                      {"dy_q", dy_q, nq * es, 16, true, false, nullptr},
                      {"dy_k", dy_k, nk * es, 16, true, false, nullptr},
-                     {"dq", dq, nq * es, 16, true, true, dy_q},
-                     {"dk", dk, nk * es, 16, true, true, dy_k},
+                     {"dq", dq, nq * es, 16, true, true, "dy_q"},
+                     {"dk", dk, nk * es, 16, true, true, "dy_k"},
                      {"dw_q", dw_q, w, 4, false, true, nullptr},
                      {"dw_k", dw_k, w, 4, false, true, nullptr},
                      {"workspace", workspace, need, 16, need > 0, true, nullptr}};

@@ -226,3 +226,15 @@ def test_more_sequences_than_a_launch_holds_are_refused():
     for f in (kda.kda_linear_prefill_workspace_bytes, kda.kda_linear_backward_workspace_bytes):
         assert f((1 << 22) + 1, 1, 1, 1, 32, 32, kda.KDA_BF16) == 0
         assert f(1 << 22, 65, 1, 1, 128, 128, kda.KDA_BF16) == 0       # one segment: three workgroups each
+
+
+def test_in_place_outputs_refuse_a_second_input_at_the_same_address():
+    """The output may be the input it replaces, not another one that shares its memory."""
+    same = dict(H=4, H_k=4)
+    refuse("kda_qk_norm_rope", "KDA_ERR_ALIASING", k=at(0), y_q=at(0), **same)
+    refuse("kda_qk_norm_rope", "KDA_ERR_ALIASING", k=at(0), y_k=at(0), **same)
+    refuse("kda_qk_norm_rope_backward", "KDA_ERR_ALIASING", dy_k=at(6), dq=at(6), **same)
+    refuse("kda_qk_norm_rope_backward", "KDA_ERR_ALIASING", q=at(6), dq=at(6))
+    sizes = dict(B=1, H=1, H_k=1, T=32, d_k=32, d_v=32, dt=kda.KDA_F32)     # q, v and a state: the same bytes
+    refuse("kda_linear_prefill", "KDA_ERR_ALIASING", S_T=at(4), v=at(4), **sizes)
+    refuse("kda_linear_tree_commit", "KDA_ERR_ALIASING", S_out=at(4), v=at(4), **sizes)
