@@ -202,7 +202,7 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(NormRope p, float* __res
                 }
 #pragma unroll
                 for (int o = 1; o < LR; o <<= 1) dot += __shfl_xor(dot, o);
-                const float f = c * r * r * dot;
+                const float f = c * r * (r * dot);              // r * r may overflow
 #pragma unroll
                 for (int i = 0; i < VE; ++i) u[i] = r * (u[i] - f * x[i]);
             }

@@ -121,3 +121,20 @@ def test_captured_calls_replay():
         torch.cuda.synchronize()
         for a, b in zip(held, work()):
             assert torch.equal(a, b)
+
+
+def test_gradients_of_zero_rows_under_the_smallest_eps():
+    """eps 2^-133 (exact in fp32): r is 2^66.5 on a row of zeros, its square past fp32."""
+    need_gpu()
+    import linear_attention_recurrence_05_amd as kda
+    x = make(1, 5, 2, 2, 64, 64, F32, True)
+    x["q"][0, 1:3] = 0
+    eps = 2.0 ** -133
+    got = kda.qk_norm_rope_backward(x["q"], x["k"], x["positions"], x["inv_freq"], x["dy_q"], x["dy_k"],
+                                    w_q=x["w_q"], w_k=x["w_k"], eps=eps)
+    torch.cuda.synchronize()
+    for n in "qk":
+        dx, mx, dw, mw = ref.norm_rope_backward(x[n], x["w_" + n], x["positions"], x["inv_freq"], x["dy_" + n],
+                                                "rms", eps, False)
+        ref.check("d" + n, got["d" + n], dx, mx, F32, 0, 2 * terms(64))
+        ref.check("dw_" + n, got["dw_" + n], dw, mw, F32, 0, terms(64, 10))
