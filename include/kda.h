@@ -404,9 +404,10 @@ kda_status kda_intra_chunk(const void *q, const void *k, const void *z,
  *   or past it are neither read nor written by any kernel (their rows of o,
  *   or of the gradients, keep what they held), and the final state is the one
  *   after the last real token: S0 itself for a length of 0.
- * - Inputs must be finite (fp32 ones below 3.38e38, bf16's range): an infinity or NaN in one token can reach outputs
- *   of up to 31 tokens before it as well as all later ones (and, in a tree,
- *   of every node).
+ * - Inputs must be finite (fp32 ones below 3.38e38, bf16's range): an infinity
+ *   or NaN in one token can reach outputs of up to 31 tokens before it as well
+ *   as all later ones (and, in a tree, of every node).  Padding, absent nodes
+ *   and skipped sequences may hold anything.
  * - A pool row that one sequence of a paged call writes may be read by that
  *   sequence alone: a second one naming it, as input or output, races.
  * - g and lens need 4-byte, the states 16-byte alignment. */
