@@ -39,8 +39,14 @@ __device__ __forceinline__ uint64_t tree_path(const int* __restrict__ parent, in
     return bad ? 0 : set;
 }
 
-// One workgroup per (b, h), one wave per 16 value columns.  A wave's slab of S
-// is the operand of S^T q straight from its loads; q, k
+// Tiles of 16 value columns that a wave holds.  Of 128 columns two: four waves
+// form the pair weights and read the keys half as often as eight, and rows of S
+// come in whole 128-byte lines (B64 H32 d128 bf16, T64: 50 against 79 us; T16: 33
+// against 35; B2 T13: 6.5 both).  Of 64 columns one (B64 T64: 37 against 40 us).
+template <int DV> constexpr int tree_tiles() { return DV == 128 ? 2 : 1; }
+
+// One workgroup per (b, h), one wave per NC tiles of value columns.  A wave's
+// slab of S is the operand of S^T q straight from its loads; q, k
 // and v of the nodes lie in LDS, rows of absent nodes as zeros (they may hold
 // anything).  The weights of 32 keys for 16 queries are formed transposed by
 // every wave, so that they are the operand of the product with v as they are.
@@ -48,10 +54,12 @@ __device__ __forceinline__ uint64_t tree_path(const int* __restrict__ parent, in
 // the pair weights are split into for their products.  bf16 takes two, which
 // leaves only the output's own rounding, where the device is not full anyway,
 // and one, half a bf16 step on each part of the sum, where it is (B64 H32 T64
-// with its commit: 113 against 119 us).
+// d128: 50 against 58 us).  Three waves a SIMD, so three workgroups of 53 KB of
+// LDS a CU, where the registers suffice: B64 H32 T64 moves 267 MB in 43 us with
+// its inputs cached in part (50 among others).
 template <typename E, int DK, int DV, int TN, int NS>
-__global__ __launch_bounds__(DV * 4, 2) void linear_tree_kernel(LinearTree p) {
-    constexpr int NT = DV * 4, KM = DK / 32, PE = 16 / sizeof(E);
+__global__ __launch_bounds__(DV * 4 / tree_tiles<DV>(), DV == 128 && sizeof(E) == 2 && NS == 1 ? 3 : 2) void linear_tree_kernel(LinearTree p) {
+    constexpr int NC = tree_tiles<DV>(), NT = DV * 4 / NC, KM = DK / 32, PE = 16 / sizeof(E);
     constexpr int LK = DK + PE, LV = DV + PE;                 // padded LDS rows
     constexpr int PK = TN * DK / PE, PV = TN * DV / PE;       // 16-byte pieces
     constexpr int RK = (PK + NT - 1) / NT, RV = (PV + NT - 1) / NT;
@@ -60,14 +68,23 @@ __global__ __launch_bounds__(DV * 4, 2) void linear_tree_kernel(LinearTree p) {
     const int b = blockIdx.x / p.H, h = blockIdx.x % p.H;
     if (p.S.skip(b)) return;
     const int tid = threadIdx.x, wave = wave_id(), lane = lane_id(), j = lane & 15, g = lane >> 4;
-    const int hk = h / (p.H / p.Hk), T = p.T, col = wave * 16 + j;
+    const int hk = h / (p.H / p.Hk), T = p.T, cbase = wave * NC * 16;
 
     const float* S = p.S.in + ((size_t)(p.S.in_slot ? p.S.in_slot[b] : b) * p.H + h) * (DK * DV);
-    float st[KM][8];
+    float st[NC][KM][8];                                      // tile ct: columns cbase + NC j + ct
 #pragma unroll
     for (int m = 0; m < KM; ++m)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) st[m][i] = S[(32 * m + 8 * g + i) * DV + col];
+        for (int i = 0; i < 8; ++i) {
+            const float* at = S + (32 * m + 8 * g + i) * DV + cbase + NC * j;
+            if constexpr (NC == 2) {
+                const f32x2 x = *reinterpret_cast<const f32x2*>(at);
+                st[0][m][i] = x[0];
+                st[1][m][i] = x[1];
+            } else {
+                st[0][m][i] = *at;
+            }
+        }
     const size_t t0 = (size_t)b * T;
     const uint64_t path = tree_path(p.parent + t0, T);        // of node `lane`
     const uint64_t live = __ballot(path != 0);
@@ -100,30 +117,56 @@ __global__ __launch_bounds__(DV * 4, 2) void linear_tree_kernel(LinearTree p) {
 #pragma unroll
         for (int i = 0; i < RV; ++i) {
             const int at = tid + i * NT, row = at / (DV / PE), e = at % (DV / PE) * PE;
-            if (PV % NT == 0 || at < PV) *reinterpret_cast<u32x4*>(&s_v[row * LV + e]) = live >> row & 1 ? rv[i] : none;
+            if (PV % NT == 0 || at < PV) {
+                const u32x4 v = live >> row & 1 ? rv[i] : none;
+                if constexpr (NC == 1) {
+                    *reinterpret_cast<u32x4*>(&s_v[row * LV + e]) = v;
+                } else {                                      // of 32 columns the even ones, then the odd ones
+                    E* dst = &s_v[row * LV + (e & ~31) + (e & 31) / 2];
+                    u32x2 even, odd;
+                    if constexpr (sizeof(E) == 2) {
+                        even = u32x2{(v[0] & 0xffff) | v[1] << 16, (v[2] & 0xffff) | v[3] << 16};
+                        odd = u32x2{v[0] >> 16 | (v[1] & 0xffff0000), v[2] >> 16 | (v[3] & 0xffff0000)};
+                    } else {
+                        even = u32x2{v[0], v[2]};
+                        odd = u32x2{v[1], v[3]};
+                    }
+                    *reinterpret_cast<u32x2*>(dst) = even;
+                    *reinterpret_cast<u32x2*>(dst + 16) = odd;
+                }
+            }
         }
     }
     if (wave == 0 && lane < TN) s_n[lane] = (float)__popcll(path);
     __syncthreads();
 
     const float lg = log_decay(p.g[h]);
-    Frag<E> sf[KM][NS];
+    Frag<E> sf[NC][KM][NS];
 #pragma unroll
-    for (int m = 0; m < KM; ++m)
-        split(f32x4{st[m][0], st[m][1], st[m][2], st[m][3]}, f32x4{st[m][4], st[m][5], st[m][6], st[m][7]}, sf[m]);
+    for (int ct = 0; ct < NC; ++ct)
+#pragma unroll
+        for (int m = 0; m < KM; ++m) {
+            const float* x = st[ct][m];
+            split(f32x4{x[0], x[1], x[2], x[3]}, f32x4{x[4], x[5], x[6], x[7]}, sf[ct][m]);
+        }
     for (int qt = 0; qt * 16 < T; ++qt) {                     // 16 queries: lane j has query 16 qt + j
         const int q = 16 * qt + j;
         const float nq = s_n[q];
         const uint32_t path_lo = __shfl((uint32_t)path, q), path_hi = __shfl((uint32_t)(path >> 32), q);
         Frag<E> x[KM];
-        f32x4 o = zero4();
+        f32x4 o[NC];
+#pragma unroll
+        for (int ct = 0; ct < NC; ++ct) o[ct] = zero4();
 #pragma unroll
         for (int m = 0; m < KM; ++m) {
             x[m] = row_frag<E>(&s_q[q * LK + 32 * m + 8 * g]);
 #pragma unroll
-            for (int s = 0; s < NS; ++s) o = mma(sf[m][s], x[m], o);
+            for (int ct = 0; ct < NC; ++ct)
+#pragma unroll
+                for (int s = 0; s < NS; ++s) o[ct] = mma(sf[ct][m][s], x[m], o[ct]);
         }
-        o *= p.scale * expf(lg * nq);
+#pragma unroll
+        for (int ct = 0; ct < NC; ++ct) o[ct] *= p.scale * expf(lg * nq);
 #pragma unroll
         for (int kb = 0; kb < TN / 32; ++kb) {                // 32 keys
             if (2 * kb > qt) break;
@@ -143,17 +186,32 @@ __global__ __launch_bounds__(DV * 4, 2) void linear_tree_kernel(LinearTree p) {
             }
             Frag<E> wf[NS];
             split(w[0], w[1], wf);
-            const Frag<E> vf = col_frag<E>(&s_v[32 * kb * LV], LV, wave * 16, 4, j, g);
 #pragma unroll
-            for (int s = 0; s < NS; ++s) o = mma(vf, wf[s], o);
+            for (int ct = 0; ct < NC; ++ct) {
+                const Frag<E> vf = col_frag<E>(&s_v[32 * kb * LV], LV, cbase + 16 * ct, 4, j, g);
+#pragma unroll
+                for (int s = 0; s < NS; ++s) o[ct] = mma(vf, wf[s], o[ct]);
+            }
         }
         if (q < T) {
-            if (nq == 0.f) o = zero4();
-            E* dst = (E*)p.o + ((t0 + q) * p.H + h) * DV + wave * 16 + 4 * g;
-            if constexpr (sizeof(E) == 2)
-                *reinterpret_cast<bf16x4*>(dst) = pack4(o);
-            else
-                *reinterpret_cast<f32x4*>(dst) = o;
+            float y[4 * NC];                                  // columns in order
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int ct = 0; ct < NC; ++ct) y[NC * i + ct] = nq == 0.f ? 0.f : o[ct][i];
+            E* dst = (E*)p.o + ((t0 + q) * p.H + h) * DV + cbase + 4 * NC * g;
+            if constexpr (sizeof(E) == 2 && NC == 2) {
+                *reinterpret_cast<bf16x8*>(dst) = pack8(f32x4{y[0], y[1], y[2], y[3]}, f32x4{y[4], y[5], y[6], y[7]});
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4 * NC; i += 4) {
+                    const f32x4 part = {y[i], y[i + 1], y[i + 2], y[i + 3]};
+                    if constexpr (sizeof(E) == 2)
+                        *reinterpret_cast<bf16x4*>(dst + i) = pack4(part);
+                    else
+                        *reinterpret_cast<f32x4*>(dst + i) = part;
+                }
+            }
         }
     }
 }
@@ -223,7 +281,7 @@ __global__ __launch_bounds__(DK * DV / 32 < 64 ? 64 : DK * DV / 32) void linear_
 
 template <typename E, int DK, int DV, int NS>
 static void launch_tree(const LinearTree& a, hipStream_t stream) {
-    const dim3 grid((unsigned)(a.B * a.H)), block(DV * 4);
+    const dim3 grid((unsigned)(a.B * a.H)), block(DV * 4 / tree_tiles<DV>());
     if (a.T <= 32)
         hipLaunchKernelGGL((linear_tree_kernel<E, DK, DV, 32, NS>), grid, block, 0, stream, a);
     else
