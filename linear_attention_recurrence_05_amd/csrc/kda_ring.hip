@@ -12,9 +12,11 @@
 // D / 16 = 8 workgroups, one per 16-column tile of the state, with equal ids
 // mod 8 and so all on one XCD: workgroups are dispatched round-robin over the
 // XCDs, from an XCD that differs between hardware queues (and changes for a
-// queue as others come into use).  A workgroup on another XCD than the rest of
-// its unit would see none of their flags, which live in their L2: its waits,
-// and theirs for its pairs, would give up.  The grid is at most one workgroup
+// queue as others come into use).  The handover below holds within one L2
+// only: across two, a flag could be written back, and seen, before the block
+// it announces.  So the unit's workgroups compare their XCDs at device scope
+// before the first pair is taken, and all of them give up if they differ.
+// The grid is at most one workgroup
 // per CU and every workgroup fits a CU by itself, so the whole grid is
 // resident at once, which the waits between workgroups need.  A workgroup:
 //   waves 0..2  producers: pairs p = tile + 8 (w + 3 j) of the unit, each
@@ -75,12 +77,34 @@ struct RingCfg {
     // flags of a unit (ints): ready[R] (last pair published in each slot),
     // done[NCT] (last pair every consumer of the tile has taken); the gate
     // reads both with one atomic per lane (ready on lanes 0 .. R-1, done on
-    // lanes 32 .. 32 + NCT - 1)
-    static constexpr int FL_READY = 0, FL_DONE = 32, FL_INTS = 64;
-    static_assert(R <= 32 && NCT <= 32, "flag layout");
+    // lanes 32 .. 32 + NCT - 1), and xcd[NCT] (the XCD each tile runs on)
+    static constexpr int FL_READY = 0, FL_DONE = 32, FL_XCD = 48, FL_INTS = 64;
+    static_assert(R <= 32 && NCT <= 16, "flag layout");
     static_assert(LDS <= 160 * 1024 - 64, "LDS of one workgroup");
     static_assert(P::BYTES % 16 == 0, "16-byte copies");
 };
+
+// The XCD this wave runs on (hardware register XCC_ID, bits 3:0).
+__device__ __forceinline__ int xcd_id() {
+    return __builtin_amdgcn_s_getreg(20 | (0 << 6) | ((4 - 1) << 11)) & 15;
+}
+
+// Whether the NCT workgroups of a unit run on one XCD: each posts its own and
+// reads the others', at device scope, which unlike the flags' scope holds
+// across the XCDs' L2s.  All of them find the same.  Called by one wave while
+// the producers make the first pairs (B1 H32 T4096: 120 us with and without).
+template <int NCT>
+__device__ __forceinline__ bool unit_on_one_xcd(int* ids, int ct) {
+    const int lane = lane_id(), me = xcd_id();
+    if (lane == 0) __hip_atomic_store(ids + ct, me, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (int it = 0; it < kSpinLimit; ++it) {
+        const int got = lane < NCT ? __hip_atomic_load(ids + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : me;
+        if (__builtin_amdgcn_ballot_w64(got >= 0 && got != me)) return false;
+        if (!__builtin_amdgcn_ballot_w64(got < 0)) return true;
+        __builtin_amdgcn_s_sleep(2);
+    }
+    return false;
+}
 
 // Zero the optimiser cannot see through, so an atomic add of it stays an
 // atomic (an add of a literal zero may become a plain load).
@@ -277,8 +301,8 @@ __global__ __launch_bounds__((RingCfg<E, D>::THREADS)) void pair_ring_kernel(
     // lready: last pair the gate saw published; lfree: last pair every tile
     // of the unit has taken (its slot may be refilled); ldone[c]: last pair
     // consumer c (0 chain, 1 output) has taken from the ring; uready / udone:
-    // the entries between chain and output wave (a gate that gives up stores
-    // kGaveUp to lready and lfree)
+    // the entries between chain and output wave (a gate that gives up, also
+    // where the unit is not on one XCD, stores kGaveUp to lready and lfree)
     __shared__ int lready, lfree, ldone[2], uready, udone;
     int u, ct;
     if (!map_unit(NCT, B * H, u, ct)) return;   // uniform over the workgroup
@@ -357,7 +381,8 @@ __global__ __launch_bounds__((RingCfg<E, D>::THREADS)) void pair_ring_kernel(
         // flags, lanes 32 .. 32 + NCT - 1 the tiles' done flags; the run of
         // published pairs from p on is forwarded in one step
         int p = 0, published = -1, freed = -1, idle = 0;
-        while (p < NP) {
+        bool live = unit_on_one_xcd<NCT>(fl + Cfg::FL_XCD, ct);
+        while (live && p < NP) {
             const int d = min(__hip_atomic_load(&ldone[0], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP),
                               __hip_atomic_load(&ldone[1], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP));
             if (d > published) {
@@ -387,16 +412,14 @@ __global__ __launch_bounds__((RingCfg<E, D>::THREADS)) void pair_ring_kernel(
                 idle = 0;
                 continue;
             }
-            if (++idle > kSpinLimit) {
-                // give up: every wait of the workgroup ends and its results
-                // are poisoned
-                if (lane == 0) {
-                    __hip_atomic_store(&lfree, kGaveUp, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-                    __hip_atomic_store(&lready, kGaveUp, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-                }
-                break;
-            }
+            live = ++idle <= kSpinLimit;
             __builtin_amdgcn_s_sleep(2);
+        }
+        if (!live && lane == 0) {
+            // give up: every wait of the workgroup ends and its results are
+            // poisoned
+            __hip_atomic_store(&lfree, kGaveUp, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+            __hip_atomic_store(&lready, kGaveUp, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
         }
         return;
     }
