@@ -527,7 +527,9 @@ kda_status kda_linear_tree_commit_paged(const void *k, const void *v, const floa
  * q, y_q [B, T, H, d], k, y_k [B, T, H_k, d] of element type dt; d in {32, 64,
  * 128}, rot even in [0, d] (inv_freq and positions may be NULL for 0);
  * positions [B, T] int32 in device memory; eps > 0 and finite (a row of
- * zeros gives zeros). */
+ * zeros gives zeros).  Rows may hold any finite values, also ones whose squares
+ * fp32 does not hold; an infinity or NaN reaches its own row and the weights'
+ * gradients only. */
 enum { KDA_NORM_L2 = 0, KDA_NORM_RMS = 1 };
 
 /* y_q may be q itself and y_k may be k itself (in place); no other overlap of

@@ -2,7 +2,7 @@
 // position rotation in the same pass, and its gradients.
 //   n = x r,  r = (c sum x^2 + eps)^{-1/2};  u = w n;  y = Rot(angle) u
 //   du = Rot(-angle) dy;  dw = sum du n;  dn = w du;
-//   dx = r dn - c r^3 x (x . dn)
+//   dx = r (dn - c n (n . dn))
 //
 // Bound by the one read and one write of the rows (4096 tokens of 32 + 32
 // heads, bf16, d 128: 26 us, 5.1 TB/s).  A workgroup takes a token at a time: its
@@ -22,6 +22,12 @@ namespace kda {
 // with 4096; 2002 tokens of H 32 + 8 backward, each workgroup leaving a partial
 // weight gradient: 22 us with 512 to 768, 25 with 1024, 28 with 256).
 constexpr int kNormGroups = 1024, kNormBwdGroups = 768;
+
+// Outside these means of squares (eps included) fp32 has lost squares to
+// infinity, or some that count to its lower end, and the row is taken times
+// 2^-80 or 2^80.  The sum of its squares is then within 2^103 or 2^67, and the
+// mean at least 2^-32 or (eps being at least 2^-149) 2^11.
+constexpr float kLeastMean = 0x1p-100f, kMostMean = 0x1.fffffep127f, kDown = 0x1p-80f;
 
 // cos and sin of pos * f.  The product is formed and reduced to a turn in
 // 64 bits: at position 10^6 a product in fp32 would be off by 0.03 radians.
@@ -125,12 +131,23 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(NormRope p, float* __res
             float x[VE], u[VE];
             unpack<E, VE>(row.x, x);
             if (BWD) unpack<E, VE>(row.dy, u);
-            float sum = 0.f;
+            auto mean = [&](float eps) {                      // the same in all lanes of a row
+                float sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < VE; ++i) sum += x[i] * x[i];
+                for (int i = 0; i < VE; ++i) sum += x[i] * x[i];
 #pragma unroll
-            for (int o = 1; o < LR; o <<= 1) sum += __shfl_xor(sum, o);
-            const float r = 1.0f / sqrtf(c * sum + p.eps);
+                for (int o = 1; o < LR; o <<= 1) sum += __shfl_xor(sum, o);
+                return c * sum + eps;
+            };
+            float m = mean(p.eps), scale = 1.0f;
+            const bool scaled = __any(!(m >= kLeastMean && m <= kMostMean));   // some row of the wave's
+            if (__builtin_expect(scaled, false)) {            // from here on x is the row times scale
+                if (!(m >= kLeastMean && m <= kMostMean)) scale = m > 1.0f ? kDown : 1.0f / kDown;
+#pragma unroll
+                for (int i = 0; i < VE; ++i) x[i] *= scale;
+                m = mean(p.eps * scale * scale);
+            }
+            const float r = 1.0f / sqrtf(m);
             if (!BWD) {
 #pragma unroll
                 for (int i = 0; i < VE; ++i) u[i] = x[i] * r * (isk ? wk[i] : wq[i]);
@@ -191,20 +208,27 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(NormRope p, float* __res
                 }
             }
             if (BWD) {
+                // of n = r x throughout: products of dy with x may overflow where
+                // the gradient does not
                 float dot = 0.f;
                 const float keep = in ? r : 0.f;
 #pragma unroll
                 for (int i = 0; i < VE; ++i) {
-                    const float dw = u[i] * x[i] * keep;
+                    x[i] *= keep;
+                    const float dw = u[i] * x[i];
                     if (isk) dwk[i] += dw; else dwq[i] += dw;
                     u[i] *= isk ? wk[i] : wq[i];
                     dot += u[i] * x[i];
                 }
 #pragma unroll
                 for (int o = 1; o < LR; o <<= 1) dot += __shfl_xor(dot, o);
-                const float f = c * r * (r * dot);              // r * r may overflow
+                dot *= c;
 #pragma unroll
-                for (int i = 0; i < VE; ++i) u[i] = r * (u[i] - f * x[i]);
+                for (int i = 0; i < VE; ++i) u[i] = r * (u[i] - dot * x[i]);
+                if (__builtin_expect(scaled, false)) {
+#pragma unroll
+                    for (int i = 0; i < VE; ++i) u[i] *= scale;
+                }
             }
             if (in) store_row<E, VE>((E*)(isk ? p.y_k : p.y_q) + off, u);
         }
