@@ -91,3 +91,35 @@ def test_tree(size, dtype):
     args = ("q", "k", "v", "g", "scale", "S0")
     ref.check("o", o, pairs.tree(*(x[n] for n in args), parent), pairs.tree(*(a[n] for n in args), parent), dtype,
               1 if dtype == BF else 0, terms(T, dk))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dv", [64, 128])
+@pytest.mark.parametrize("Hk", [4, 1])
+def test_padded_gradients_in_several_segments(Hk, dv, dtype):
+    """Sequences that end in the first, a middle and the last of four or more segments, one of no
+    tokens and one of a single one; their padding holds NaN and is neither read nor written."""
+    need_gpu()
+    import linear_attention_recurrence_05_amd as kda
+    lens = [700, 0, 1, 97, 256, 333]
+    B, T, H, dk = len(lens), 700, 4, 64
+    say("padded segments", Hk, dv, dtype)
+    assert kda.kda_linear_backward_workspace_bytes(B, T, H, H, dk, dv, dtype) > 0      # segments' states
+    x, gen = make(B, T, H, Hk, dk, dv, dtype, seed=Hk + dv, lens=lens)
+    x["dO"], x["dS_T"] = _rand(gen, *x["v"].shape).to(dtype), _rand(gen, B, H, dk, dv)
+    for b, n in enumerate(lens):
+        for t in ("q", "k", "v", "dO"):
+            x[t][b, n:] = float("nan")
+    out = {n: torch.full_like(x[n[1:]], 7.0) for n in ("dq", "dk", "dv")}
+    got = kda.linear_backward(x["q"], x["k"], x["v"], x["g"], x["dO"], x["scale"], x["S0"], x["dS_T"], x["lens"], **out)
+    o = torch.full_like(x["v"], 7.0)
+    _, S_T = kda.linear_prefill(x["q"], x["k"], x["v"], x["g"], x["scale"], x["S0"], x["lens"], o=o)
+    torch.cuda.synchronize()
+    for b, n in enumerate(lens):
+        for t in (*out.values(), o):
+            assert (t[b, n:] == 7.0).all()
+            t[b, n:] = 0
+    assert torch.equal(got["dS0"][1], x["dS_T"][1]) and torch.equal(S_T[1], x["S0"][1])
+    n = terms(2 * T, dv, H // Hk)
+    compare(got, pairs.backward, x, ("dq", "dk", "dv", "dS0"), BWD, dtype, ("dS0",), n)
+    compare(dict(o=o, S_T=S_T), pairs.prefill, x, ("o", "S_T"), FWD, dtype, ("S_T",), n)
