@@ -61,6 +61,8 @@
 extern "C" {
 #endif
 
+/* Raised by changes that callers have to follow.  Entry points that were added
+ * since are found by their names (dlsym). */
 #define KDA_ABI_VERSION 1
 /* Tokens per chunk of the chunkwise prefill (the pages' 16-token tiles). */
 #define KDA_CHUNK 16
@@ -410,6 +412,18 @@ kda_status kda_intra_chunk(const void *q, const void *k, const void *z,
  *   and skipped sequences may hold anything.
  * - A pool row that one sequence of a paged call writes may be read by that
  *   sequence alone: a second one naming it, as input or output, races.
+ * - Precision.  Sums and states are fp32, and states keep its accuracy whatever
+ *   dt (a few 1e-7 of their norm); so do fp32 outputs and gradients, whose
+ *   products leave out what lies below 2^-24 of the operands.  With bf16, the
+ *   state and the weights of pairs of tokens are rounded to bf16 once on their
+ *   way into an output, up to half a bf16 step on each part of its sum beside
+ *   the output's own rounding (2.3e-3 of the norm in all, 1.7e-3 without).
+ *   Single tokens have none of that, nor do calls that leave the device room:
+ *   trees of fewer than 512 sequences x heads, and short prefills and gradients
+ *   of few.  A sequence's results may therefore differ by these roundings (fp32
+ *   ones and states by the order of fp32 sums) between calls that hold it among
+ *   more or fewer others, or padded to another T; the same call gives the same
+ *   bits.
  * - g and lens need 4-byte, the states 16-byte alignment. */
 
 /* Bytes of device workspace kda_linear_prefill and kda_linear_prefill_paged

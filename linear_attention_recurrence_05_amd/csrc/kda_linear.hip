@@ -61,11 +61,12 @@ struct LinearJob {
 // fp32; NP is the number for the state and the pair weights in their products
 // with x and u (see launch_job_d).  STATE: only the state of a segment
 // from zero, into the workspace.
-// What bounds it: where every CU has a workgroup, the rows (B8 H32 T8192 d128
-// bf16 in 477 us, 2.19 GB moved, 4.6 TB/s against 4.8 of a large copy; the matrix
-// cores are busy a third of that); where sequences are few or short, a chunk's
-// own chain (stage, products, barrier: 1.4 us, of which MFMA and VALU issue fill
-// two thirds).
+// What bounds it: where every CU has a workgroup, its instructions and its rows
+// alike (B8 H32 T8192 d128 bf16 in 479 us: one wave a SIMD issues in 57 % of its
+// cycles, VALU 42 %, and waits in 20 %, the matrix cores are busy in 33 %; 2.19 GB
+// at 4.6 TB/s, a large copy's rate, where the decode step reaches 5.85); where
+// sequences are few or short, a chunk's own chain (stage, products, barrier: 1.4
+// us, of which MFMA and VALU issue fill two thirds).
 template <typename E, int DA, int DB, int NC, int NP, bool STATE>
 __global__ __launch_bounds__(DB / NC * 4, 2) void linear_chunk_kernel(LinearJob job) {
     constexpr int C = kLinChunk, NT = DB / NC * 4, KM = DA / 32;
@@ -491,9 +492,12 @@ static hipError_t launch_job_n(const LinearJob& job, hipStream_t stream) {
 
 // bf16: the state and the pair weights enter their products as one bf16 term
 // each, which leaves half a step of bf16 on each part of the output's sum
-// beside its own rounding.  A second term removes that and costs a fifth of a
-// chunk's arithmetic, which only a pass of a few chunks, latency for the most
-// part, has to spare.
+// beside its own rounding (2.3e-3 of the norm against 1.7e-3).  A second term
+// removes that and costs a fifth and more of a chunk's arithmetic (everywhere: B1
+// H32 T4096 75 against 64 us, B8 H32 T8192 617 against 487, gradients of B1 H32
+// T4096 150 against 124), which only a pass of a few chunks and one tile a wave,
+// latency for the most part, has to spare: with two tiles a wave the CUs are
+// full, whatever the length.  So a sequence's rounding depends on the batch.
 template <typename E, int DA, int DB>
 static hipError_t launch_job_d(const LinearJob& job, hipStream_t stream) {
     constexpr int NP = sizeof(E) == 2 ? 1 : 3;

@@ -54,7 +54,7 @@ template <int DV> constexpr int tree_tiles() { return DV == 128 ? 2 : 1; }
 // the pair weights are split into for their products.  bf16 takes two, which
 // leaves only the output's own rounding, where the device is not full anyway,
 // and one, half a bf16 step on each part of the sum, where it is (B64 H32 T64
-// d128: 50 against 58 us).  Three waves a SIMD, so three workgroups of 53 KB of
+// d128: 50 against 58 us; with its commit 94 against 98).  Three waves a SIMD, so three workgroups of 53 KB of
 // LDS a CU, where the registers suffice: B64 H32 T64 moves 267 MB in 43 us with
 // its inputs cached in part (50 among others).
 template <typename E, int DK, int DV, int TN, int NS>

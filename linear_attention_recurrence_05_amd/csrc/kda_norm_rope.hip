@@ -4,9 +4,13 @@
 //   du = Rot(-angle) dy;  dw = sum du n;  dn = w du;
 //   dx = r (dn - c n (n . dn))
 //
-// Bound by the one read and one write of the rows (4096 tokens of 32 + 32
-// heads, bf16, d 128: 26 us, 5.1 TB/s).  A workgroup takes a token at a time: its
-// cos and sin are formed once, in LDS, and serve all heads of q and k.  A row lies in d / VE neighbouring lanes of 16 bytes each, so a
+// Bound, over many heads, by the one read and one write of the rows (4096 tokens
+// of 32 + 32 heads, bf16, d 128: 26 us, 5.1 TB/s).  A workgroup takes a token at a
+// time: its cos and sin are formed once, in LDS, and serve all heads of q and k.
+// With few heads most of its row places stay empty (65,536 tokens of 1 + 1 heads of
+// 32: 53 us, 0.3 TB/s), and the gradients' three or four tokens a workgroup do not
+// fill the device's memory (2002 tokens of 32 + 8 heads: 19 us, 3.3 TB/s).
+// A row lies in d / VE neighbouring lanes of 16 bytes each, so a
 // wave reads and writes 1 KB at a time, sums within the row's lanes, and gets
 // the other element of a pair from the same lane (interleaved), from a lane
 // rot / 2 elements away (halves of whole lanes), or through LDS (any other rot).
