@@ -62,3 +62,35 @@ def test_unit_rows_of_the_largest_values(dtype):
     want = torch.sign(q.double()) / 128 ** 0.5
     tol = ref.HALF[dtype] + (terms(128)) * 2.0 ** -24
     assert ((y.double() - want).abs() <= tol * want.abs()).all(), y[0, :, 0, 0]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("case", [(128, 128, False, "l2"), (64, 64, True, "rms"), (32, 0, False, "l2"),
+                                  (128, 38, False, "rms"), (64, 6, True, "l2")])
+def test_infinities_and_nan_stay_in_their_rows(case, dtype):
+    """Every other row keeps its bits, also beside rows that are taken times a power of two; the
+    weights' gradients of the other tensor too."""
+    need_gpu()
+    import linear_attention_recurrence_05_amd as kda
+    d, rot, il, norm = case
+    x = make(2, 9, 5, 3, d, rot, dtype, True, seed=d)
+    kw = dict(w_q=x["w_q"], w_k=x["w_k"], norm=norm, eps=1e-6, interleaved=il)
+
+    def both():
+        y = kda.qk_norm_rope(x["q"], x["k"], x["positions"], x["inv_freq"], **kw)
+        g = kda.qk_norm_rope_backward(x["q"], x["k"], x["positions"], x["inv_freq"], x["dy_q"], x["dy_k"], **kw)
+        torch.cuda.synchronize()
+        return y[0], g["dq"], y[1], g["dk"], g["dw_k"]
+
+    clean = both()
+    bad = [(0, 0, 0, "nan"), (0, 3, 2, "inf"), (1, 5, 4, "-inf"), (1, 8, 1, "1e38")]
+    for b, t, h, value in bad:
+        x["q"][b, t, h, (7 * t + h) % d] = float(value)
+    got = both()
+    for b, t, h, value in bad[:3]:
+        assert not torch.isfinite(got[0][b, t, h].float()).all()
+    for b, t, h, value in bad:
+        for i in (0, 1):
+            got[i][b, t, h] = clean[i][b, t, h]
+    for a, c in zip(got, clean):
+        assert torch.equal(a, c)
