@@ -572,6 +572,155 @@ kda_status kda_qk_norm_rope_backward(const void *q, const void *k, const float *
                                      int H, int H_k, int d, kda_dtype dt, void *workspace,
                                      size_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The gated delta rule with a decay and a write strength for each token and
+ * head, both given:
+ *
+ *   a_t = exp(g_t)                            one number per token and head
+ *   e_t = v_t - (a_t S_{t-1})^T k_t
+ *   S_t = a_t S_{t-1} + beta_t k_t e_t^T      = a_t (I - beta_t k_t k_t^T) S_{t-1} + beta_t k_t v_t^T
+ *   o_t = scale S_t^T q_t
+ *
+ * Conventions: those of linear attention above (shared heads of q and k, head
+ * sizes, states and pools, lens, scale, finite inputs, padding, precision, what
+ * may differ between calls), and beyond them:
+ * - g, beta [B, T, H] fp32 (decode: [B, H]), 4-byte aligned.  g <= 0 is
+ *   expected; values below -10000 (also -infinity: a token that starts from a
+ *   zero state) are taken as -10000, for which a is exactly 0.  beta may be any
+ *   finite number ((0, 1) is usual; keys of length 1 keep the recurrence stable
+ *   up to 2).
+ * - B * H <= 2^19.
+ * - With bf16, an output's o, dq and dk take the state, the pairs' weights and
+ *   what each token writes as one bf16 term on their way into the output; the
+ *   states, dg, dbeta and dS0, and dv before its own rounding, are fp32
+ *   throughout. */
+
+/* Bytes of device workspace kda_delta_prefill and kda_delta_prefill_paged need
+ * for these sizes (0: none; also 0 for arguments they would reject). */
+size_t kda_delta_prefill_workspace_bytes(int B, int T, int H, int H_k, int d_k, int d_v,
+                                         kda_dtype dt);
+
+/* o for every token and, if S_T != NULL, the final state, from S0 (NULL:
+ * zero).  S_T may alias S0 exactly; no other overlap of an output or the
+ * workspace with another argument is allowed. */
+kda_status kda_delta_prefill(const void *q, const void *k, const void *v, const float *g,
+                             const float *beta, float scale, const float *S0, const int *lens,
+                             void *o, float *S_T, int B, int T, int H, int H_k, int d_k,
+                             int d_v, kda_dtype dt, void *workspace, size_t workspace_bytes,
+                             void *stream);
+
+/* kda_delta_prefill from pool row slots_in[b] (NULL: zero states) into pool
+ * row slots_out[b] (NULL: no state written). */
+kda_status kda_delta_prefill_paged(const void *q, const void *k, const void *v, const float *g,
+                                   const float *beta, float scale, float *pool, int n_slots,
+                                   const int *slots_in, const int *slots_out, const int *lens,
+                                   void *o, int B, int T, int H, int H_k, int d_k, int d_v,
+                                   kda_dtype dt, void *workspace, size_t workspace_bytes,
+                                   void *stream);
+
+/* Bytes of device workspace kda_delta_backward needs for these sizes (0: none;
+ * also 0 for arguments it would reject). */
+size_t kda_delta_backward_workspace_bytes(int B, int T, int H, int H_k, int d_k, int d_v,
+                                          kda_dtype dt);
+
+/* Gradients of kda_delta_prefill for L = sum(dO * o) + sum(dS_T * S_T): with
+ * Y_n = dS_T (NULL: zero) after the n tokens of a sequence,
+ *   R_t = scale q_t dO_t^T + Y_{t+1},  z_t = R_t^T k_t,  dv_t = beta_t z_t,
+ *   dbeta_t = z_t . e_t,  dq_t = scale S_t dO_t,
+ *   dk_t = beta_t R_t e_t - a_t S_{t-1} dv_t,
+ *   Y_t = a_t (R_t - k_t dv_t^T),  dg_t = sum(Y_t * S_{t-1}),  dS0 = Y_0.
+ * dq, dk [B, T, H_k, d_k] (summed over the heads that share them) and dv
+ * [B, T, H, d_v] have element type dt, dg and dbeta [B, T, H] and dS0
+ * [B, H, d_k, d_v] are fp32 (dS0 NULL: not written; dS_T itself for a length of
+ * 0).  The states are recomputed from the forward call's inputs.  No output may
+ * overlap another argument. */
+kda_status kda_delta_backward(const void *q, const void *k, const void *v, const float *g,
+                              const float *beta, float scale, const float *S0, const int *lens,
+                              const void *dO, const float *dS_T, void *dq, void *dk, void *dv,
+                              float *dg, float *dbeta, float *dS0, int B, int T, int H, int H_k,
+                              int d_k, int d_v, kda_dtype dt, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/* One token of every sequence: q, k [B, H_k, d_k], v, o [B, H, d_v], g, beta
+ * [B, H]; the state S is read once and overwritten in place.  o must not overlap
+ * another argument, nor S the inputs. */
+kda_status kda_delta_decode_step(const void *q, const void *k, const void *v, const float *g,
+                                 const float *beta, float scale, float *S, void *o, int B, int H,
+                                 int H_k, int d_k, int d_v, kda_dtype dt, void *stream);
+
+/* kda_delta_decode_step on pool row slots[b], in place. */
+kda_status kda_delta_decode_step_paged(const void *q, const void *k, const void *v,
+                                       const float *g, const float *beta, float scale,
+                                       float *pool, int n_slots, const int *slots, void *o,
+                                       int B, int H, int H_k, int d_k, int d_v, kda_dtype dt,
+                                       void *stream);
+
+/* ------------------------------------------------------------------------
+ * The norm of a recurrence's output under its gate.  For each of `rows` rows x,
+ * z of d elements (a head's; d in {32, 64, 128}), element type dt:
+ *   n = x (sum(x^2) / d + eps)^{-1/2},   y = act(z) w n
+ * act(z) = Sigmoid(z) (KDA_GATE_SIGMOID) or z Sigmoid(z) (KDA_GATE_SILU);
+ * w fp32 [d] (NULL: 1); eps > 0 and finite.  Rows of x may hold any finite
+ * values, also ones whose squares fp32 does not hold; an infinity or NaN reaches
+ * its own row and the weight's gradient only.  rows d <= 2^40. */
+enum { KDA_GATE_SIGMOID = 0, KDA_GATE_SILU = 1 };
+
+/* y may be x itself (in place); no other overlap of an output with another
+ * argument is allowed. */
+kda_status kda_gated_norm(const void *x, const void *z, const float *w, int act, float eps,
+                          void *y, long long rows, int d, kda_dtype dt, void *stream);
+
+/* Bytes of device workspace kda_gated_norm_backward needs for these sizes when
+ * the weight's gradient is asked for (0 for arguments it would reject). */
+size_t kda_gated_norm_backward_workspace_bytes(long long rows, int d, kda_dtype dt);
+
+/* Gradients of kda_gated_norm from dy (shape and type of y): dx, dz of element
+ * type dt, and dw [d] fp32, summed over all rows in a fixed order (NULL: not
+ * wanted; it needs w).  dx may be dy; no other overlap is allowed.  workspace:
+ * at least the queried bytes if dw is wanted, else it may be NULL. */
+kda_status kda_gated_norm_backward(const void *x, const void *z, const float *w, int act,
+                                   float eps, const void *dy, void *dx, void *dz, float *dw,
+                                   long long rows, int d, kda_dtype dt, void *workspace,
+                                   size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Between two blocks: the output y of one, normed after it (norm_y 1) or not,
+ * weighted, gated and scaled, added to the residual stream r, and the norm
+ * before the next.  For each of `rows` rows of D elements (the model's width; a
+ * multiple of 8 up to KDA_MAX_NORM_WIDTH), element type dt:
+ *   m = y (sum(y^2) / D + eps)^{-1/2} (norm_y 1) or y (0)
+ *   h = r + scale Sigmoid(z) w_y m
+ *   n = w_n h (sum(h^2) / D + eps)^{-1/2}
+ * z NULL: no gate; w_y, w_n fp32 [D], 16-byte aligned (NULL: 1); eps > 0 and
+ * scale finite.  n is formed of h before h is rounded.  y NULL (the first block
+ * of a stack): only n, of h = r; z, w_y and h are NULL then and norm_y 0.  Rows
+ * of y and h may hold any finite values; an infinity or NaN reaches its own row
+ * and the weights' gradients only.  rows D <= 2^40. */
+#define KDA_MAX_NORM_WIDTH 16384
+
+/* h may be r itself, and n may be y itself (without y: r); no other overlap of
+ * an output with another argument is allowed. */
+kda_status kda_block_norm(const void *y, const void *z, const float *w_y, const void *r,
+                          const float *w_n, int norm_y, float scale, float eps, void *h, void *n,
+                          long long rows, int D, kda_dtype dt, void *stream);
+
+/* Bytes of device workspace kda_block_norm_backward needs for these sizes when a
+ * weight's gradient is asked for (0 for arguments it would reject). */
+size_t kda_block_norm_backward_workspace_bytes(long long rows, int D, kda_dtype dt);
+
+/* Gradients of kda_block_norm from dn and dh (NULL: zero), those of its two
+ * outputs, at h as the forward call stored it (without y: r): dr (all that
+ * reaches the residual stream), dy, dz (NULL without z) of element type dt, and
+ * dw_y, dw_n [D] fp32, summed over all rows in a fixed order (NULL: not wanted;
+ * they need w_y, w_n).  Without y: dr and dw_n only.  dr may be dh; no other
+ * overlap is allowed.  workspace: at least the queried bytes if dw_y or dw_n is
+ * wanted, else it may be NULL. */
+kda_status kda_block_norm_backward(const void *y, const void *z, const float *w_y, const void *h,
+                                   const float *w_n, int norm_y, float scale, float eps,
+                                   const void *dn, const void *dh, void *dr, void *dy, void *dz,
+                                   float *dw_y, float *dw_n, long long rows, int D, kda_dtype dt,
+                                   void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

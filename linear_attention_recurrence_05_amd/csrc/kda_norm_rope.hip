@@ -16,8 +16,8 @@
 // rot / 2 elements away (halves of whole lanes), or through LDS (any other rot).
 #include <algorithm>
 
-#include "kda_device.hpp"
 #include "kda_linear.hpp"
+#include "kda_norm.hpp"
 
 namespace kda {
 
@@ -26,12 +26,6 @@ namespace kda {
 // with 4096; 2002 tokens of H 32 + 8 backward, each workgroup leaving a partial
 // weight gradient: 22 us with 512 to 768, 25 with 1024, 28 with 256).
 constexpr int kNormGroups = 1024, kNormBwdGroups = 768;
-
-// Outside these means of squares (eps included) fp32 has lost squares to
-// infinity, or some that count to its lower end, and the row is taken times
-// 2^-80 or 2^80.  The sum of its squares is then within 2^103 or 2^67, and the
-// mean at least 2^-32 or (eps being at least 2^-149) 2^11.
-constexpr float kLeastMean = 0x1p-100f, kMostMean = 0x1.fffffep127f, kDown = 0x1p-80f;
 
 // cos and sin of pos * f.  The product is formed and reduced to a turn in
 // 64 bits: at position 10^6 a product in fp32 would be off by 0.03 radians.
@@ -43,23 +37,6 @@ __device__ __forceinline__ void angle(int pos, float f, float& c, float& s) {
 
 // How a lane gets the other elements of its pairs.
 enum class Pairs { kNone, kLane, kLaneAny, kShuffle, kLds };
-
-template <typename E, int VE>
-__device__ __forceinline__ void unpack(u32x4 v, float (&x)[VE]) {
-    E e[VE];
-    *reinterpret_cast<u32x4*>(e) = v;
-#pragma unroll
-    for (int i = 0; i < VE; ++i) x[i] = to_f32(e[i]);
-}
-template <typename E, int VE>
-__device__ __forceinline__ void store_row(E* p, const float (&x)[VE]) {
-    u32x4 v;
-    if constexpr (sizeof(E) == 2)
-        v = __builtin_bit_cast(u32x4, pack8(f32x4{x[0], x[1], x[2], x[3]}, f32x4{x[4], x[5], x[6], x[7]}));
-    else
-        v = __builtin_bit_cast(u32x4, f32x4{x[0], x[1], x[2], x[3]});
-    __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
-}
 
 // N consecutive floats of LDS (N of 2, 4 or 8, aligned to min(N, 4) of them).
 template <int N>

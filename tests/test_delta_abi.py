@@ -1,0 +1,265 @@
+"""Refusals of the delta-rule, gated-norm and block-norm entry points on the CPU: the C library
+rejects bad arguments on the host before any HIP call, the binding tensors that do not fit.  No
+call here reaches a kernel launch."""
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+import linear_attention_recurrence_05_amd as kda
+from linear_attention_recurrence_05_amd import _lib
+
+HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "kda.h")
+E = {n: i for i, n in enumerate(_lib._STATUS)}
+
+
+def at(i, off=0):
+    """A fake device address, never dereferenced: every call below is refused."""
+    return ctypes.c_void_p((1 << 40) + i * (1 << 36) + off)
+
+
+INF, NAN = float("inf"), float("nan")
+SIZES = dict(B=2, T=64, H=4, H_k=2, d_k=64, d_v=128, dt=kda.KDA_BF16)
+ONE = dict(B=2, H=4, H_k=2, d_k=64, d_v=128, dt=kda.KDA_BF16, stream=None)
+WS = dict(workspace=at(30), workspace_bytes=1 << 34, stream=None)
+ROW = dict(q=at(0), k=at(1), v=at(2), g=at(3), beta=at(4), scale=1.0)
+CALLS = {
+    "kda_delta_prefill": dict(**ROW, S0=at(5), lens=at(6), o=at(7), S_T=at(8), **SIZES, **WS),
+    "kda_delta_prefill_paged": dict(**ROW, pool=at(5), n_slots=3, slots_in=at(6), slots_out=at(7), lens=at(8), o=at(9),
+                                    **SIZES, **WS),
+    "kda_delta_backward": dict(**ROW, S0=at(5), lens=at(6), dO=at(7), dS_T=at(8), dq=at(9), dk=at(10), dv=at(11),
+                               dg=at(12), dbeta=at(13), dS0=at(14), **SIZES, **WS),
+    "kda_delta_decode_step": dict(**ROW, S=at(5), o=at(6), **ONE),
+    "kda_delta_decode_step_paged": dict(**ROW, pool=at(5), n_slots=3, slots=at(6), o=at(7), **ONE),
+    "kda_gated_norm": dict(x=at(0), z=at(1), w=at(2), act=1, eps=1e-6, y=at(3), rows=64, d=128, dt=kda.KDA_BF16,
+                           stream=None),
+    "kda_gated_norm_backward": dict(x=at(0), z=at(1), w=at(2), act=1, eps=1e-6, dy=at(3), dx=at(4), dz=at(5), dw=at(6),
+                                    rows=64, d=128, dt=kda.KDA_BF16, **WS),
+    "kda_block_norm": dict(y=at(0), z=at(1), w_y=at(2), r=at(3), w_n=at(4), norm_y=1, scale=1.0, eps=1e-6, h=at(5),
+                           n=at(6), rows=64, D=2048, dt=kda.KDA_BF16, stream=None),
+    "kda_block_norm_backward": dict(y=at(0), z=at(1), w_y=at(2), h=at(3), w_n=at(4), norm_y=1, scale=1.0, eps=1e-6,
+                                    dn=at(5), dh=at(6), dr=at(7), dy=at(8), dz=at(9), dw_y=at(10), dw_n=at(11), rows=64,
+                                    D=2048, dt=kda.KDA_BF16, **WS),
+}
+DELTA = [n for n in CALLS if "delta" in n]
+GATED = [n for n in CALLS if "gated" in n]
+BLOCK = [n for n in CALLS if "block" in n]
+
+
+def refuse(name, code, **over):
+    args = dict(CALLS[name])
+    assert set(over) <= set(args), (name, over)
+    args.update(over)
+    L = kda.lib()
+    st = getattr(L, name)(*args.values())
+    assert st == E[code] and L.kda_last_error().decode(), (name, over, st, L.kda_last_error())
+
+
+def past(name, arg, off):
+    return ctypes.c_void_p(CALLS[name][arg].value + off)
+
+
+def test_the_argument_lists_are_the_headers():
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    for name, args in CALLS.items():
+        decl = re.search(r"\b%s\s*\(([^)]*)\)" % name, text).group(1)
+        assert [a.split()[-1].lstrip("*") for a in decl.split(",")] == list(args), name
+
+
+@pytest.mark.parametrize("name", DELTA)
+def test_delta_calls_refuse(name):
+    has = CALLS[name]
+    for over, code in [
+        (dict(B=0), "KDA_ERR_INVALID_SHAPE"), (dict(H=0), "KDA_ERR_INVALID_SHAPE"), (dict(B=-1), "KDA_ERR_INVALID_SHAPE"),
+        (dict(H_k=3), "KDA_ERR_INVALID_SHAPE"), (dict(H_k=0), "KDA_ERR_INVALID_SHAPE"),
+        (dict(H_k=8), "KDA_ERR_INVALID_SHAPE"), (dict(T=0), "KDA_ERR_INVALID_SHAPE"),
+        (dict(T=(1 << 30) + 1), "KDA_ERR_INVALID_SHAPE"),
+        (dict(B=(1 << 17) + 1), "KDA_ERR_INVALID_SHAPE"), (dict(H=1 << 18, H_k=1 << 18), "KDA_ERR_INVALID_SHAPE"),
+        (dict(d_k=48), "KDA_ERR_UNSUPPORTED"), (dict(d_v=256), "KDA_ERR_UNSUPPORTED"), (dict(d_k=0), "KDA_ERR_UNSUPPORTED"),
+        (dict(dt=2), "KDA_ERR_UNSUPPORTED"), (dict(scale=INF), "KDA_ERR_INVALID_VALUE"),
+        (dict(scale=NAN), "KDA_ERR_INVALID_VALUE"), (dict(n_slots=0), "KDA_ERR_INVALID_SHAPE"),
+        (dict(n_slots=1 << 25), "KDA_ERR_INVALID_SHAPE"),
+    ]:
+        if set(over) <= set(has):
+            refuse(name, code, **over)
+    for p in ("q", "k", "v", "g", "beta", "o", "S", "pool", "dO", "dq", "dk", "dv", "dg", "dbeta", "slots"):
+        if p in has:
+            refuse(name, "KDA_ERR_NULL_POINTER", **{p: None})
+            refuse(name, "KDA_ERR_MISALIGNED", **{p: past(name, p, 2)})
+    for p in ("S0", "S_T", "dS_T", "dS0"):
+        if p in has:
+            refuse(name, "KDA_ERR_MISALIGNED", **{p: past(name, p, 4)})
+    for out in ("o", "S_T", "S", "pool", "dq", "dk", "dv", "dg", "dbeta", "dS0"):
+        for p in ("q", "k", "v", "g", "beta", "lens", "dO"):
+            if out in has and p in has:
+                refuse(name, "KDA_ERR_ALIASING", **{out: has[p]})
+    if "S0" in has and "S_T" in has:                      # in place is fine, a partial overlap is not
+        refuse(name, "KDA_ERR_ALIASING", S_T=past(name, "S0", 16))
+    if "pool" in has:
+        refuse(name, "KDA_ERR_ALIASING", o=past(name, "pool", 64))
+    if "dq" in has:
+        for a, b in (("dq", "dk"), ("dg", "dbeta"), ("dS0", "dS_T"), ("dS0", "S0"), ("dv", "v"), ("dv", "dO")):
+            refuse(name, "KDA_ERR_ALIASING", **{a: has[b]})
+
+
+@pytest.mark.parametrize("name", [n for n in CALLS if "workspace" in CALLS[n]])
+def test_workspaces_are_checked(name):
+    need = dict(kda_delta_prefill=lambda: kda.kda_delta_prefill_workspace_bytes(2, 64, 4, 2, 64, 128, kda.KDA_BF16),
+                kda_delta_prefill_paged=lambda: kda.kda_delta_prefill_workspace_bytes(2, 64, 4, 2, 64, 128, kda.KDA_BF16),
+                kda_delta_backward=lambda: kda.kda_delta_backward_workspace_bytes(2, 64, 4, 2, 64, 128, kda.KDA_BF16),
+                kda_gated_norm_backward=lambda: kda.kda_gated_norm_backward_workspace_bytes(64, 128, kda.KDA_BF16),
+                kda_block_norm_backward=lambda: kda.kda_block_norm_backward_workspace_bytes(64, 2048, kda.KDA_BF16))[name]()
+    if need:
+        refuse(name, "KDA_ERR_NULL_POINTER", workspace=None)
+        refuse(name, "KDA_ERR_MISALIGNED", workspace=at(30, 8))
+        refuse(name, "KDA_ERR_WORKSPACE_TOO_SMALL", workspace_bytes=need - 1)
+        first = next(iter(CALLS[name]))
+        refuse(name, "KDA_ERR_ALIASING", workspace=CALLS[name][first])
+
+
+@pytest.mark.parametrize("name", GATED + BLOCK)
+def test_norm_calls_refuse(name):
+    has = CALLS[name]
+    for over, code in [
+        (dict(rows=0), "KDA_ERR_INVALID_SHAPE"), (dict(rows=-5), "KDA_ERR_INVALID_SHAPE"),
+        (dict(rows=1 << 40), "KDA_ERR_INVALID_SHAPE"), (dict(rows=(1 << 63) - 1), "KDA_ERR_INVALID_SHAPE"),
+        (dict(d=96), "KDA_ERR_UNSUPPORTED"), (dict(d=256), "KDA_ERR_UNSUPPORTED"), (dict(D=0), "KDA_ERR_UNSUPPORTED"),
+        (dict(D=2044), "KDA_ERR_UNSUPPORTED"), (dict(D=16392), "KDA_ERR_UNSUPPORTED"), (dict(D=-8), "KDA_ERR_UNSUPPORTED"),
+        (dict(dt=-1), "KDA_ERR_UNSUPPORTED"), (dict(act=2), "KDA_ERR_INVALID_VALUE"), (dict(act=-1), "KDA_ERR_INVALID_VALUE"),
+        (dict(eps=0.0), "KDA_ERR_INVALID_VALUE"), (dict(eps=-1.0), "KDA_ERR_INVALID_VALUE"),
+        (dict(eps=INF), "KDA_ERR_INVALID_VALUE"), (dict(eps=NAN), "KDA_ERR_INVALID_VALUE"),
+        (dict(norm_y=2), "KDA_ERR_INVALID_VALUE"), (dict(scale=NAN), "KDA_ERR_INVALID_VALUE"),
+        (dict(scale=INF), "KDA_ERR_INVALID_VALUE"),
+    ]:
+        if set(over) <= set(has):
+            refuse(name, code, **over)
+    inputs = [p for p in ("x", "z", "w", "dy", "y", "r", "h", "dn", "dh", "w_y", "w_n") if p in has]
+    outputs = dict(kda_gated_norm=["y"], kda_gated_norm_backward=["dx", "dz", "dw"], kda_block_norm=["h", "n"],
+                   kda_block_norm_backward=["dr", "dy", "dz", "dw_y", "dw_n"])[name]
+    inplace = dict(kda_gated_norm={"y": "x"}, kda_gated_norm_backward={"dx": "dy"}, kda_block_norm={"h": "r", "n": "y"},
+                   kda_block_norm_backward={"dr": "dh"})[name]
+    for p in ("x", "r", "dn", "n", "dx", "dr") + (("dy", "dz", "h") if "backward" in name else ("y", "h")):
+        if p in has and not (name == "kda_block_norm" and p == "y"):
+            refuse(name, "KDA_ERR_NULL_POINTER", **{p: None})
+    for p in set(inputs + outputs):
+        refuse(name, "KDA_ERR_MISALIGNED", **{p: past(name, p, 2)})
+    for out in outputs:
+        for p in inputs:
+            if p == out:
+                continue
+            if inplace.get(out) == p:
+                refuse(name, "KDA_ERR_ALIASING", **{out: past(name, p, 16)})
+            else:
+                refuse(name, "KDA_ERR_ALIASING", **{out: has[p]})
+        for other in outputs:
+            if other != out:
+                refuse(name, "KDA_ERR_ALIASING", **{out: has[other]})
+    # an input that shares the address of the one an output replaces would be lost
+    if name == "kda_block_norm":
+        refuse(name, "KDA_ERR_ALIASING", z=at(3), h=at(3))
+    if name == "kda_gated_norm":
+        refuse(name, "KDA_ERR_ALIASING", z=at(0), y=at(0))
+
+
+def test_block_norm_refuses_parts_of_an_absent_block():
+    alone = dict(y=None, z=None, w_y=None, h=None, norm_y=0)
+    for over in (dict(z=at(1)), dict(w_y=at(2)), dict(h=at(5)), dict(norm_y=1)):
+        refuse("kda_block_norm", "KDA_ERR_INVALID_VALUE", **{**alone, **over})
+    alone = dict(y=None, z=None, w_y=None, norm_y=0, dy=None, dz=None, dw_y=None)
+    for over in (dict(z=at(1)), dict(w_y=at(2)), dict(dy=at(8)), dict(dz=at(9)), dict(dw_y=at(10)), dict(norm_y=1)):
+        refuse("kda_block_norm_backward", "KDA_ERR_INVALID_VALUE", **{**alone, **over})
+    refuse("kda_block_norm_backward", "KDA_ERR_INVALID_VALUE", z=None)                     # dz without z
+    refuse("kda_block_norm_backward", "KDA_ERR_NULL_POINTER", w_y=None)                    # dw_y without w_y
+    refuse("kda_block_norm_backward", "KDA_ERR_NULL_POINTER", w_n=None)
+    refuse("kda_gated_norm_backward", "KDA_ERR_NULL_POINTER", w=None)
+
+
+def test_workspace_queries_of_refused_sizes_are_zero():
+    for f in (kda.kda_delta_prefill_workspace_bytes, kda.kda_delta_backward_workspace_bytes):
+        assert f(0, 64, 4, 2, 64, 64, kda.KDA_BF16) == 0
+        assert f(1, 64, 4, 3, 64, 64, kda.KDA_BF16) == 0
+        assert f(1, 64, 4, 2, 96, 64, kda.KDA_BF16) == 0
+        assert f((1 << 19) + 1, 64, 1, 1, 64, 64, kda.KDA_BF16) == 0
+        assert f(1, 64, 4, 2, 64, 64, 5) == 0
+    assert kda.kda_delta_backward_workspace_bytes(2, 64, 4, 2, 64, 64, torch.bfloat16) > 0
+    for f, d in ((kda.kda_gated_norm_backward_workspace_bytes, 64), (kda.kda_block_norm_backward_workspace_bytes, 4096)):
+        assert f(0, d, kda.KDA_BF16) == 0 and f(64, 44, kda.KDA_BF16) == 0 and f(64, d, 7) == 0
+        assert f(64, d, torch.float32) > 0
+
+
+# ----------------------------------------------------------------- the binding
+
+def tensors(dtype=torch.bfloat16):
+    B, T, H, Hk, dk, dv = 2, 6, 4, 2, 32, 64
+    z = torch.zeros
+    return dict(q=z(B, T, Hk, dk, dtype=dtype), k=z(B, T, Hk, dk, dtype=dtype), v=z(B, T, H, dv, dtype=dtype),
+                g=z(B, T, H), beta=z(B, T, H), S=z(B, H, dk, dv), o=z(B, T, H, dv, dtype=dtype),
+                lens=z(B, dtype=torch.int32), w=z(dv), pool=z(3, H, dk, dv), slots=z(B, dtype=torch.int32))
+
+
+def calls(x):
+    yield lambda: kda.delta_prefill(x["q"], x["k"], x["v"], x["g"], x["beta"], 1.0, x["S"], x["lens"], o=x["o"])
+    yield lambda: kda.delta_backward(x["q"], x["k"], x["v"], x["g"], x["beta"], x["o"], 1.0, x["S"], x["S"], x["lens"])
+    yield lambda: kda.kda_delta_prefill_paged(x["q"], x["k"], x["v"], x["g"], x["beta"], 1.0, x["pool"], x["slots"],
+                                              None, x["o"], x["lens"])
+
+
+def norm_calls(x):
+    yield lambda: kda.gated_norm(x["v"], x["o"], x["w"])
+    yield lambda: kda.gated_norm_backward(x["v"], x["o"], x["w"], x["v"])
+    yield lambda: kda.block_norm(x["v"], x["o"], z=x["v"], w_y=x["w"], w_n=x["w"])
+    yield lambda: kda.block_norm_backward(x["v"], x["o"], x["v"], x["v"], z=x["v"], w_y=x["w"], w_n=x["w"])
+
+
+def test_the_binding_refuses_host_tensors():
+    x = tensors()
+    for call in (*calls(x), *norm_calls(x)):
+        with pytest.raises(ValueError, match="CUDA device"):
+            call()
+
+
+@pytest.mark.parametrize("name,bad,error", [
+    ("k", lambda t: t.float(), ValueError), ("k", lambda t: t[:, :, :1], ValueError),
+    ("k", lambda t: t.transpose(0, 1).contiguous().transpose(0, 1), ValueError),
+    ("v", lambda t: t[:, :5], ValueError), ("v", lambda t: t[0], ValueError), ("v", lambda t: None, (TypeError, ValueError)),
+    ("g", lambda t: t.double(), ValueError), ("g", lambda t: t[:, :, 0], ValueError), ("g", lambda t: t[:, :3], ValueError),
+    ("beta", lambda t: t.bfloat16(), ValueError), ("beta", lambda t: None, ValueError), ("beta", lambda t: t[..., :1], ValueError),
+    ("lens", lambda t: t.long(), ValueError), ("k", lambda t: "k", (TypeError, ValueError)),
+])
+def test_the_binding_refuses_tensors_that_do_not_fit(monkeypatch, name, bad, error):
+    monkeypatch.setattr(_lib, "_DEVICE_TYPE", "cpu")
+    x = tensors()
+    x[name] = bad(x[name])
+    for call in calls(x):
+        with pytest.raises(error):
+            call()
+
+
+def test_the_binding_refuses_states_pools_rows_and_gates(monkeypatch):
+    monkeypatch.setattr(_lib, "_DEVICE_TYPE", "cpu")
+    x = tensors()
+    for bad in (x["S"].bfloat16(), x["S"].transpose(2, 3), x["S"][:1]):
+        y = {**x, "S": bad}
+        for call in list(calls(y))[:2]:
+            with pytest.raises(ValueError, match="S0|dS_T"):
+                call()
+    for key, bad in (("pool", x["pool"][0]), ("pool", x["pool"].double()), ("slots", x["slots"].long())):
+        with pytest.raises(ValueError, match=key):
+            list(calls({**x, key: bad}))[2]()
+    y = {n: t.half() if t.dtype == torch.bfloat16 else t for n, t in x.items()}
+    for call in (*calls(y), *norm_calls(y)):
+        with pytest.raises(ValueError, match="bfloat16 or float32"):
+            call()
+    for key, bad in (("o", x["o"][:, :5]), ("o", x["o"].float()), ("w", x["w"][:9]), ("w", x["w"].bfloat16()),
+                     ("o", x["o"].transpose(0, 1))):
+        for call in norm_calls({**x, key: bad}):
+            with pytest.raises(ValueError):
+                call()
+    with pytest.raises(ValueError, match="act must be"):
+        kda.gated_norm(x["v"], x["o"], act="relu")
+    with pytest.raises(TypeError):
+        kda.gated_norm(None, x["o"])
+    with pytest.raises(ValueError, match="dimension"):
+        kda.gated_norm(torch.zeros((), dtype=torch.bfloat16), x["o"])
