@@ -1,231 +1,280 @@
-// kda_delta.hip -- the gated delta rule over a sequence and its gradients, token
-// by token.  One workgroup of 256 threads per (b, h): thread tid holds column
-// tid % DV of DK / (256 / DV) rows of the state.
+// kda_delta.hip -- the gated delta rule over a sequence in chunk form
+// (kda_delta_chunk.hpp): the chain of states over the chunks.
 #include <algorithm>
 
-#include "kda_delta.hpp"
-#include "kda_device.hpp"
+#include "kda_delta_chain.hpp"
 
 namespace kda {
 
-template <typename E, int DK, int DV>
-struct Tok {
-    static constexpr int NT = 256, RG = NT / DV, R = DK / RG;   // row groups, rows of a thread
-    float S[R];
+// One workgroup per (b, h, 16 value columns), one wave for each 32 key channels:
+// the wave holds their part of the state [DK, 16] as two accumulator tiles, whose
+// rows are mapped to channels so that a lane's rows of both are eight consecutive
+// channels: the tiles are then an operand of K S and of Q S without a move.  The
+// waves' parts of K S (and of Q S, for o) are summed through LDS, in order, the one
+// barrier of a chunk; E and its scaled form are made by every wave, whose own
+// channels of the state they then update.
+template <typename E, int DK>
+__global__ __launch_bounds__(DK * 2, 2) void delta_chain_kernel(DeltaChain p) {
+    constexpr int C = kDeltaChunk, KM = DK / 32, NT = DK * 2;
+    constexpr int NE = sizeof(E) == 2 ? 1 : 3, NP = NE, ES = sizeof(E);
+    using Blk = DeltaBlock<NP, false>;
+    constexpr int LK = 40, LV = 24;                          // padded rows of the K slice and of v in LDS
+    constexpr int PB = Blk::bytes / 16, RB = (PB + NT - 1) / NT;   // pieces of a block, a thread's
+    constexpr int PV = C * 16 * ES / 16, RV = (PV + NT - 1) / NT;  // pieces of v's tile
+    __shared__ __align__(16) bf16 s_k[KM][NE][C * LK];
+    __shared__ __align__(16) bf16 s_v[2][NE][C * LV];
+    __shared__ __align__(16) char s_blk[2][Blk::bytes];
+    __shared__ f32x4 s_part[KM > 1 ? 2 : 1][KM > 1 ? KM : 1][4][kWave];
 
-    static __device__ int col() { return threadIdx.x % DV; }
-    static __device__ int row0() { return (int)(threadIdx.x / DV) * R; }
-    __device__ void load(const float* p) {
-        for (int i = 0; i < R; ++i) S[i] = p ? p[(row0() + i) * DV + col()] : 0.f;
-    }
-    __device__ void store(float* p) const {
-        for (int i = 0; i < R; ++i) p[(row0() + i) * DV + col()] = S[i];
-    }
-    // sum over the rows of x[row] S[row][col], in every thread of the column
-    __device__ float down(const float* x, float* s_red) const {
-        float t = 0.f;
-        for (int i = 0; i < R; ++i) t += x[row0() + i] * S[i];
-        s_red[threadIdx.x] = t;
-        __syncthreads();
-        t = 0.f;
-        for (int i = 0; i < RG; ++i) t += s_red[i * DV + col()];
-        __syncthreads();
-        return t;
-    }
-    // sum over the columns of S[row][col] y (y this column's), into out[row]
-    __device__ void across(float y, float* out, float* s_part) const {   // s_part [4][DK]
-        constexpr int W = DV < 64 ? DV : 64;
-        const int wave = threadIdx.x / 64;
-        for (int i = 0; i < R; ++i) {
-            float t = S[i] * y;
-            for (int o = 1; o < W; o <<= 1) t += __shfl_xor(t, o);
-            if (threadIdx.x % W == 0) s_part[(DV > 64 ? wave % 2 : 0) * DK + row0() + i] = t;
-        }
-        __syncthreads();
-        for (int i = threadIdx.x; i < DK; i += NT) out[i] = s_part[i] + (DV > 64 ? s_part[DK + i] : 0.f);
-        __syncthreads();
-    }
-    // sum of x over the columns (x the same in all row groups), in every thread
-    static __device__ float all(float x, float* s_red) {
-        s_red[threadIdx.x] = x;
-        __syncthreads();
-        float t = 0.f;
-        for (int i = 0; i < DV; ++i) t += s_red[i];
-        __syncthreads();
-        return t;
-    }
-};
-
-template <typename E, int DK, int DV>
-__global__ __launch_bounds__(256) void delta_prefill_kernel(DeltaPrefill p) {
-    using K = Tok<E, DK, DV>;
-    __shared__ float s_q[DK], s_k[DK], s_red[256];
-    const int b = blockIdx.x / p.H, h = blockIdx.x % p.H, hk = h / (p.H / p.Hk);
+    const int tiles = p.dv / 16, units = p.B * p.H;
+    int unit, tile;
+    unit_tile(blockIdx.x, units, tiles, unit, tile);
+    const int b = unit / p.H, h = unit % p.H, hk = h / (p.H / p.Hk);
     if (p.S.skip(b)) return;
-    const int n = p.lens ? min(max(p.lens[b], 0), p.T) : p.T;
-    K st;
-    st.load(p.S.in ? p.S.in + ((size_t)(p.S.in_slot ? p.S.in_slot[b] : b) * p.H + h) * (DK * DV) : nullptr);
-    for (int t = 0; t < n; ++t) {
-        const size_t tok = (size_t)b * p.T + t, qk = (tok * p.Hk + hk) * DK, vo = (tok * p.H + h) * DV;
-        for (int i = threadIdx.x; i < DK; i += 256) {
-            s_q[i] = to_f32(((const E*)p.q)[qk + i]);
-            s_k[i] = to_f32(((const E*)p.k)[qk + i]);
-        }
-        __syncthreads();
-        const float a = expf(log_decay(p.g[tok * p.H + h])), beta = p.beta[tok * p.H + h];
-        for (int i = 0; i < K::R; ++i) st.S[i] *= a;
-        const float e = to_f32(((const E*)p.v)[vo + K::col()]) - st.down(s_k, s_red);
-        for (int i = 0; i < K::R; ++i) st.S[i] += s_k[K::row0() + i] * (beta * e);
-        const float o = p.scale * st.down(s_q, s_red);
-        if (K::row0() == 0) ((E*)p.o)[vo + K::col()] = from_f32<E>(o);
+    const int n = seq_len(p.lens, b, p.T), c_end = min(p.c1, (n + C - 1) / C);
+    const int tid = threadIdx.x, kw = wave_id(), lane = lane_id(), j = lane & 15, g = lane >> 4;
+
+    // ---- the state's rows: tile t, channel 32 kw + 8 g + 4 t + i, column j
+    const size_t state = (size_t)DK * p.dv;
+    f32x4 M[2];
+    {
+        const float* in = p.S.in ? p.S.in + ((size_t)(p.S.in_slot ? p.S.in_slot[b] : b) * p.H + h) * state : nullptr;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) M[t][i] = in ? in[(size_t)(32 * kw + 8 * g + 4 * t + i) * p.dv + 16 * tile + j] : 0.f;
     }
-    if (p.S.out) st.store(p.S.out + ((size_t)(p.S.out_slot ? p.S.out_slot[b] : b) * p.H + h) * (DK * DV));
+
+    // ---- rows of chunk c: K and Q as operands (row 16 q + j, this wave's
+    // channels), v's tile and the block for all waves
+    const int ldk = p.Hk * DK * ES, ldv = p.H * p.dv * ES;
+    struct Own {
+        Raw<E> k[2], q[2];
+    };
+    struct Common {
+        u32x4 v[RV], blk[RB];
+    };
+    // Chunks past the end load nothing: every offset is past the buffer.
+    auto load_own = [&](int c, Own& x) {
+        const int rows = c < c_end ? min(C, n - c * C) : 0;
+        const size_t base = (((size_t)b * p.T + (size_t)c * C) * p.Hk + hk) * DK + 32 * kw;
+        const uint32_t bytes = rows > 0 ? (uint32_t)((rows - 1) * ldk + 32 * ES) : 0;
+        const Rsrc rk = make_rsrc((const E*)p.k + base, bytes), rq = make_rsrc((const E*)p.q + base, bytes);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int off = 16 * q + j < rows ? (16 * q + j) * ldk + 8 * g * ES : kOffPast;
+            x.k[q] = raw_load<E>(rk, off);
+            x.q[q] = raw_load<E>(rq, off);
+        }
+    };
+    const char* blocks = p.blocks + (size_t)unit * (p.c1 - p.c0) * Blk::bytes;
+    auto load_common = [&](int c, Common& x) {
+        const int rows = c < c_end ? min(C, n - c * C) : 0;
+        const size_t base = (((size_t)b * p.T + (size_t)c * C) * p.H + h) * p.dv + 16 * tile;
+        const Rsrc rv = make_rsrc((const E*)p.v + base, rows > 0 ? (uint32_t)((rows - 1) * ldv + 16 * ES) : 0);
+        const Rsrc rb = make_rsrc(blocks + (size_t)(c - p.c0) * Blk::bytes, rows > 0 ? Blk::bytes : 0);
+        constexpr int PR = ES;                               // 16-byte pieces of a row of 16 elements
+#pragma unroll
+        for (int i = 0; i < RV; ++i) {
+            const int at = tid + i * NT, row = at / PR;
+            x.v[i] = buf_load<u32x4>(rv, at < PV && row < rows ? row * ldv + at % PR * 16 : kOffPast);
+        }
+#pragma unroll
+        for (int i = 0; i < RB; ++i) x.blk[i] = buf_load<u32x4>(rb, tid + i * NT < PB ? (tid + i * NT) * 16 : kOffPast);
+    };
+    auto stage_common = [&](int buf, const Common& x) {
+        constexpr int PR = ES;
+#pragma unroll
+        for (int i = 0; i < RV; ++i) {
+            const int at = tid + i * NT, row = at / PR;
+            if (PV % NT == 0 || at < PV) {
+                if constexpr (NE == 1) {
+                    *reinterpret_cast<u32x4*>(&s_v[buf][0][row * LV + at % PR * 8]) = x.v[i];
+                } else {
+                    f32x4 f = __builtin_bit_cast(f32x4, x.v[i]);
+#pragma unroll
+                    for (int s = 0; s < NE; ++s) {
+                        const bf16x4 t = pack4(f);
+                        *reinterpret_cast<bf16x4*>(&s_v[buf][s][row * LV + at % PR * 4]) = t;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) f[e] -= (float)t[e];
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+            if (PB % NT == 0 || tid + i * NT < PB) reinterpret_cast<u32x4*>(s_blk[buf])[tid + i * NT] = x.blk[i];
+    };
+
+    ChunkDecay decay;
+    Own own[2];
+    Common common;
+    auto chunk = [&](auto set, int c) {
+        constexpr int s = decltype(set)::value;
+        Terms<NE> kt[2], qt[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            kt[q] = raw_terms(own[s].k[q]);
+            qt[q] = raw_terms(own[s].q[q]);
+#pragma unroll
+            for (int i = 0; i < NE; ++i) *reinterpret_cast<bf16x8*>(&s_k[kw][i][(16 * q + j) * LK + 8 * g]) = kt[q].t[i];
+        }
+        load_own(c + 2, own[s]);
+        // K S (rows: tokens) and (Q S)^T (columns: tokens) of this wave's channels
+        const Terms<3> sf = to_terms<3>(M[0], M[1]);
+        f32x4 ks[2], qs[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            ks[q] = mma(kt[q], sf, zero4());
+            qs[q] = mma(first_terms<NP>(sf), qt[q], zero4());
+        }
+        if constexpr (KM > 1) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                s_part[s][kw][q][lane] = ks[q];
+                s_part[s][kw][2 + q][lane] = qs[q];
+            }
+        }
+        __syncthreads();                                     // the parts are there, and this chunk's block and v
+        if constexpr (KM > 1) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                ks[q] = s_part[s][0][q][lane];
+#pragma unroll
+                for (int w = 1; w < KM; ++w) ks[q] += s_part[s][w][q][lane];
+            }
+        }
+        const char* blk = s_blk[s];
+        const float* row = reinterpret_cast<const float*>(blk + Blk::row);
+        // R = V - e^G K S, E = inv R
+        const Terms<NE> vt = col_terms<NE>(&s_v[s][0][0], C * LV, LV, 0, 4, j, g);
+        f32x4 R[2], e[2];
+        to_f32(vt, R[0], R[1]);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const f32x4 eg = *reinterpret_cast<const f32x4*>(row + 16 * q + 4 * g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) R[q][i] -= eg[i] * ks[q][i];
+        }
+        const Terms<3> rt = to_terms<3>(R[0], R[1]);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) e[q] = mma(frag_terms<3>(blk + Blk::inv + q * kFragBytes, 2 * kFragBytes), rt, zero4());
+        stage_common(1 - s, common);
+        load_common(c + 2, common);
+        // S' = e^{G_C} S + K^T (e^{G_C - G} beta E)
+        f32x4 u[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const f32x4 w = *reinterpret_cast<const f32x4*>(row + C + 16 * q + 4 * g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u[q][i] = w[i] * e[q][i];
+        }
+        const Terms<3> ut = to_terms<3>(u[0], u[1]);
+        const float f = decay(row[2 * C], row[2 * C + 1]);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+            M[t] = mma(col_terms<NE>(&s_k[kw][0][0], C * LK, LK, 4 * t, 8, j, g), ut, f * M[t]);
+        // o: the waves' first two (the only one's both) columns of tokens
+        const Terms<NP> et = to_terms<NP>(e[0], e[1]);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            if (KM > 1 && kw != q) continue;
+            f32x4 o = qs[q];
+            if constexpr (KM > 1) {
+                o = s_part[s][0][2 + q][lane];
+#pragma unroll
+                for (int w = 1; w < KM; ++w) o += s_part[s][w][2 + q][lane];
+            }
+            o = mma(et, frag_terms<NP>(blk + Blk::pair + q * kFragBytes, 2 * kFragBytes), (p.scale * row[16 * q + j]) * o);
+            const int t = c * C + 16 * q + j;
+            if (t < n) {
+                E* dst = (E*)p.o + (((size_t)b * p.T + t) * p.H + h) * p.dv + 16 * tile + 4 * g;
+                if constexpr (ES == 2)
+                    *reinterpret_cast<bf16x4*>(dst) = pack4(o);
+                else
+                    *reinterpret_cast<f32x4*>(dst) = o;
+            }
+        }
+    };
+
+    if (p.c0 < c_end) {
+        constexpr std::integral_constant<int, 0> set0{};
+        constexpr std::integral_constant<int, 1> set1{};
+        load_common(p.c0, common);
+        load_own(p.c0, own[0]);
+        load_own(p.c0 + 1, own[1]);
+        stage_common(0, common);
+        load_common(p.c0 + 1, common);
+        for (int c = p.c0;; c += 2) {
+            chunk(set0, c);
+            if (c + 1 >= c_end) break;
+            chunk(set1, c + 1);
+            if (c + 2 >= c_end) break;
+        }
+    }
+    if (p.S.out) {
+        float* out = p.S.out + ((size_t)(p.S.out_slot ? p.S.out_slot[b] : b) * p.H + h) * state;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) out[(size_t)(32 * kw + 8 * g + 4 * t + i) * p.dv + 16 * tile + j] = M[t][i];
+    }
 }
 
-// Three passes over the sequence: forward (E, the token sums of dO . o, dq and
-// what the old state gives dk once dv is known needs a third), reverse (dv,
-// dbeta, dg, dk's first part), forward again (dk's second part).
-// ws: E [B, T, H, DV], then dq and dk of every head [B, T, H, DK], all fp32.
-template <typename E, int DK, int DV>
-__global__ __launch_bounds__(256) void delta_backward_kernel(DeltaBackward p, float* ws) {
-    using K = Tok<E, DK, DV>;
-    __shared__ float s_q[DK], s_k[DK], s_red[256], s_part[4 * DK], s_out[DK];
-    const int b = blockIdx.x / p.H, h = blockIdx.x % p.H, hk = h / (p.H / p.Hk);
-    const int n = p.lens ? min(max(p.lens[b], 0), p.T) : p.T;
-    const size_t toks = (size_t)p.B * p.T * p.H;
-    float *we = ws, *wq = ws + toks * DV, *wk = wq + toks * DK;
-    const float* S0 = p.S0 ? p.S0 + (size_t)blockIdx.x * DK * DV : nullptr;
-    auto at = [&](int t) { return ((size_t)b * p.T + t) * p.H + h; };
-    auto rows = [&](int t) {
-        const size_t qk = (((size_t)b * p.T + t) * p.Hk + hk) * DK;
-        for (int i = threadIdx.x; i < DK; i += 256) {
-            s_q[i] = to_f32(((const E*)p.q)[qk + i]);
-            s_k[i] = to_f32(((const E*)p.k)[qk + i]);
-        }
-        __syncthreads();
-    };
-    K st;
-    st.load(S0);
-    for (int t = 0; t < n; ++t) {
-        rows(t);
-        const float a = expf(log_decay(p.g[at(t)])), beta = p.beta[at(t)];
-        for (int i = 0; i < K::R; ++i) st.S[i] *= a;
-        const float e = to_f32(((const E*)p.v)[at(t) * DV + K::col()]) - st.down(s_k, s_red);
-        if (K::row0() == 0) we[at(t) * DV + K::col()] = e;
-        for (int i = 0; i < K::R; ++i) st.S[i] += s_k[K::row0() + i] * (beta * e);
-        const float dO = p.scale * to_f32(((const E*)p.dO)[at(t) * DV + K::col()]);
-        const float dot = K::all(dO * st.down(s_q, s_red), s_red);
-        if (threadIdx.x == 0) p.dg[at(t)] = dot;
-        st.across(dO, s_out, s_part);
-        for (int i = threadIdx.x; i < DK; i += 256) wq[at(t) * DK + i] = s_out[i];
-        __syncthreads();
-    }
-    K Y;
-    Y.load(p.dST ? p.dST + (size_t)blockIdx.x * DK * DV : nullptr);
-    float end = 0.f;
-    for (int i = 0; i < K::R; ++i) end += st.S[i] * Y.S[i];
-    s_red[threadIdx.x] = end;
-    __syncthreads();
-    double run = 0;
-    for (int i = 0; i < 256; ++i) run += s_red[i];
-    __syncthreads();
-    for (int t = n - 1; t >= 0; --t) {
-        rows(t);
-        const float a = expf(log_decay(p.g[at(t)])), beta = p.beta[at(t)];
-        const float e = we[at(t) * DV + K::col()], dO = p.scale * to_f32(((const E*)p.dO)[at(t) * DV + K::col()]);
-        for (int i = 0; i < K::R; ++i) Y.S[i] += s_q[K::row0() + i] * dO;
-        const float z = Y.down(s_k, s_red), dv = beta * z;
-        const float db = K::all(z * e, s_red), vdot = K::all(dv * to_f32(((const E*)p.v)[at(t) * DV + K::col()]), s_red);
-        Y.across(beta * e, s_out, s_part);
-        for (int i = threadIdx.x; i < DK; i += 256) wk[at(t) * DK + i] = s_out[i];
-        run += (double)p.dg[at(t)] - vdot;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            p.dg[at(t)] = (float)run;
-            p.dbeta[at(t)] = db;
-        }
-        if (K::row0() == 0) {
-            ((E*)p.dv)[at(t) * DV + K::col()] = from_f32<E>(dv);
-            we[at(t) * DV + K::col()] = dv;
-        }
-        for (int i = 0; i < K::R; ++i) Y.S[i] = a * (Y.S[i] - s_k[K::row0() + i] * dv);
-        __syncthreads();
-    }
-    if (p.dS0) Y.store(p.dS0 + (size_t)blockIdx.x * DK * DV);
-    __syncthreads();
-    st.load(S0);
-    for (int t = 0; t < n; ++t) {
-        rows(t);
-        const float a = expf(log_decay(p.g[at(t)])), beta = p.beta[at(t)];
-        for (int i = 0; i < K::R; ++i) st.S[i] *= a;
-        st.across(we[at(t) * DV + K::col()], s_out, s_part);
-        for (int i = threadIdx.x; i < DK; i += 256) wk[at(t) * DK + i] -= s_out[i];
-        const float e = to_f32(((const E*)p.v)[at(t) * DV + K::col()]) - st.down(s_k, s_red);
-        for (int i = 0; i < K::R; ++i) st.S[i] += s_k[K::row0() + i] * (beta * e);
-        __syncthreads();
-    }
+// Chunks whose blocks the workspace holds at a time: longer sequences run window
+// by window, the state carried in the workspace.
+constexpr size_t kDeltaWindowBytes = (size_t)192 << 20;
+
+struct DeltaWindows {
+    int chunks, len, n;      // chunks of a sequence, of a window, windows
+    size_t blocks, carry;    // bytes
+};
+static DeltaWindows windows(int B, int T, int H, int dk, int dv, bool is_bf16) {
+    const size_t units = (size_t)B * H, blk = delta_block_bytes(is_bf16, false);
+    DeltaWindows w;
+    w.chunks = (T + kDeltaChunk - 1) / kDeltaChunk;
+    w.len = (int)std::min<size_t>(w.chunks, std::max<size_t>(8, kDeltaWindowBytes / (units * blk)));
+    w.n = (w.chunks + w.len - 1) / w.len;
+    w.len = (w.chunks + w.n - 1) / w.n;
+    w.blocks = (units * w.len * blk + 255) / 256 * 256;
+    w.carry = w.n > 1 ? units * dk * dv * sizeof(float) : 0;
+    return w;
+}
+
+size_t delta_prefill_ws_bytes(int B, int T, int H, int dk, int dv, bool is_bf16) {
+    const DeltaWindows w = windows(B, T, H, dk, dv, is_bf16);
+    return w.blocks + w.carry;
 }
 
 template <typename E>
-__global__ __launch_bounds__(256) void delta_share_kernel(const float* __restrict__ src, E* __restrict__ dq,
-                                                          E* __restrict__ dk, const int* __restrict__ lens, int T,
-                                                          int Hk, int G, int d, size_t count) {
-    for (size_t at = (size_t)blockIdx.x * 256 + threadIdx.x; at < 2 * count; at += (size_t)gridDim.x * 256) {
-        const size_t i = at < count ? at : at - count;
-        const size_t tok = i / ((size_t)Hk * d), rest = i % ((size_t)Hk * d);
-        if (lens && (int)(tok % T) >= lens[tok / T]) continue;
-        const int hk = (int)(rest / d), e = (int)(rest % d);
-        const float* from = src + (at < count ? 0 : count * G) + (tok * Hk * G + (size_t)hk * G) * d + e;
-        float s = 0.f;
-        for (int j = 0; j < G; ++j) s += from[j * d];
-        (at < count ? dq : dk)[i] = from_f32<E>(s);
+static hipError_t launch_chain(const DeltaChain& a, hipStream_t stream) {
+    const dim3 grid((unsigned)(a.B * a.H * (a.dv / 16)));
+    switch (a.dk) {
+        case 32: hipLaunchKernelGGL((delta_chain_kernel<E, 32>), grid, dim3(64), 0, stream, a); break;
+        case 64: hipLaunchKernelGGL((delta_chain_kernel<E, 64>), grid, dim3(128), 0, stream, a); break;
+        default: hipLaunchKernelGGL((delta_chain_kernel<E, 128>), grid, dim3(256), 0, stream, a); break;
     }
-}
-
-#define KDA_BY_SIZE(E, K, V, CALL)                                             \
-    switch (K * 256 + V) {                                                     \
-        case 32 * 256 + 32: CALL(E, 32, 32); break;                            \
-        case 32 * 256 + 64: CALL(E, 32, 64); break;                            \
-        case 32 * 256 + 128: CALL(E, 32, 128); break;                          \
-        case 64 * 256 + 32: CALL(E, 64, 32); break;                            \
-        case 64 * 256 + 64: CALL(E, 64, 64); break;                            \
-        case 64 * 256 + 128: CALL(E, 64, 128); break;                          \
-        case 128 * 256 + 32: CALL(E, 128, 32); break;                          \
-        case 128 * 256 + 64: CALL(E, 128, 64); break;                          \
-        default: CALL(E, 128, 128); break;                                     \
-    }
-
-size_t delta_prefill_ws_bytes(int, int, int, int, int, bool) { return 0; }
-
-hipError_t launch_delta_prefill(const DeltaPrefill& a, void*, hipStream_t stream) {
-    const dim3 grid((unsigned)(a.B * a.H)), block(256);
-#define CALL(E, K, V) hipLaunchKernelGGL((delta_prefill_kernel<E, K, V>), grid, block, 0, stream, a)
-    if (a.is_bf16) KDA_BY_SIZE(bf16, a.dk, a.dv, CALL) else KDA_BY_SIZE(float, a.dk, a.dv, CALL)
-#undef CALL
     return hipGetLastError();
 }
 
-size_t delta_backward_ws_bytes(int B, int T, int H, int, int dk, int dv, bool) {
-    return (size_t)B * T * H * (dv + 2 * dk) * sizeof(float);
-}
-
-hipError_t launch_delta_backward(const DeltaBackward& a, void* ws, hipStream_t stream) {
-    const dim3 grid((unsigned)(a.B * a.H)), block(256);
-#define CALL(E, K, V) hipLaunchKernelGGL((delta_backward_kernel<E, K, V>), grid, block, 0, stream, a, (float*)ws)
-    if (a.is_bf16) KDA_BY_SIZE(bf16, a.dk_, a.dv_, CALL) else KDA_BY_SIZE(float, a.dk_, a.dv_, CALL)
-#undef CALL
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    const size_t count = (size_t)a.B * a.T * a.Hk * a.dk_;
-    const float* part = (const float*)ws + (size_t)a.B * a.T * a.H * a.dv_;
-    const dim3 sgrid((unsigned)std::min<size_t>((2 * count + 255) / 256, 1 << 14));
-    if (a.is_bf16)
-        hipLaunchKernelGGL((delta_share_kernel<bf16>), sgrid, dim3(256), 0, stream, part, (bf16*)a.dq, (bf16*)a.dk,
-                           a.lens, a.T, a.Hk, a.H / a.Hk, a.dk_, count);
-    else
-        hipLaunchKernelGGL((delta_share_kernel<float>), sgrid, dim3(256), 0, stream, part, (float*)a.dq, (float*)a.dk,
-                           a.lens, a.T, a.Hk, a.H / a.Hk, a.dk_, count);
-    return hipGetLastError();
+hipError_t launch_delta_prefill(const DeltaPrefill& a, void* ws, hipStream_t stream) {
+    const DeltaWindows w = windows(a.B, a.T, a.H, a.dk, a.dv, a.is_bf16);
+    char* blocks = (char*)ws;
+    float* carry = w.n > 1 ? (float*)(blocks + w.blocks) : nullptr;
+    for (int i = 0; i < w.n; ++i) {
+        const int c0 = i * w.len, c1 = std::min(w.chunks, c0 + w.len);
+        StateIO S = a.S;
+        if (i > 0) S.in = carry, S.in_slot = nullptr;
+        if (i + 1 < w.n) S.out = carry, S.out_slot = nullptr;
+        hipError_t e = launch_delta_pairs({a.q, a.k, a.g, a.beta, a.scale, S, a.lens, blocks, a.B, a.T, a.H, a.Hk, a.dk, c0, c1,
+                                           a.is_bf16}, false, stream);
+        if (e != hipSuccess) return e;
+        const DeltaChain c{a.q, a.k, a.v, a.scale, S, a.lens, blocks, a.o, a.B, a.T, a.H, a.Hk, a.dk, a.dv, c0, c1, a.is_bf16};
+        e = a.is_bf16 ? launch_chain<bf16>(c, stream) : launch_chain<float>(c, stream);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace kda

@@ -1,0 +1,113 @@
+// kda_delta_chunk.hpp -- the chunk form of the gated delta rule, shared by the
+// prefill and the gradients.  With C = 32 tokens of a chunk, S the state before
+// them, G_i the sum of the chunk's log-decays up to token i, D_ij = exp(G_i - G_j)
+// for i >= j and N = (K K^T) * D below the diagonal:
+//   E  = (I + N diag(beta))^{-1} (V - e^G K S)        e_t of every token
+//   O  = scale (e^G Q S + ((Q K^T) * D) diag(beta) E)
+//   S' = e^{G_C} S + K^T diag(e^{G_C - G} beta) E
+// Every exponent is <= 0 for g <= 0; G is summed, and its differences taken, in
+// 64 bits, so that a decay behind a far smaller one keeps its digits.
+//
+// What does not depend on the state, the inverse and the pairs' weights, is made
+// first for all chunks at once (delta_pairs_kernel) and left in the workspace as
+// the matrix operands that the state's chain reads, 16 bytes a lane.
+#pragma once
+
+#include "kda_delta.hpp"
+#include "kda_device.hpp"
+#include "kda_linear_frag.hpp"
+
+namespace kda {
+
+constexpr int kDeltaChunk = 32;
+
+// A chunk's block in the workspace.  An operand of one 16x16x32 MFMA is 64 lanes
+// of 16 bytes; lane (j, g) holds row (or column) j, and along the contraction
+// tokens 4 g .. 4 g + 3 and 16 + 4 g .. 16 + 4 g + 3 of the chunk.
+//   inv  [3 terms][2]       rows 16 q + j of (I + N diag(beta))^{-1}
+//   pair [NP terms][2]      columns (queries) 16 q + j of scale ((Q K^T) * D diag(beta))^T
+//   row  [32] e^{G_i}, [32] e^{G_C - G_j} beta_j, then e^{G_C} as a factor and
+//        what its rounding left out, relative to it
+// and, for the gradients (BACK),
+//   invt [3][2]             rows of ((I + diag(beta) N)^{-1})^T
+//   pairt [3][2]            rows (keys) 16 q + j of scale ((Q K^T) * D)^T
+//   more [32] e^{G_C - G_j}, [32] beta_j
+constexpr int kFragBytes = 1024;
+template <int NP, bool BACK>
+struct DeltaBlock {
+    static constexpr int inv = 0, pair = inv + 6 * kFragBytes, row = pair + 2 * NP * kFragBytes;
+    static constexpr int more = row + 66 * 4 + 8, invt = row + 1024, pairt = invt + 6 * kFragBytes;
+    static constexpr int bytes = BACK ? pairt + 6 * kFragBytes : row + 512;
+};
+
+// Chunks c0 .. c1 - 1 of every sequence, block ((b H + h) (c1 - c0) + c - c0).
+struct DeltaPairs {
+    const void *q, *k;
+    const float *g, *beta;
+    float scale;
+    StateIO S;          // its check tables
+    const int* lens;
+    char* blocks;
+    int B, T, H, Hk, dk, c0, c1;
+    bool is_bf16;
+};
+size_t delta_block_bytes(bool is_bf16, bool back);
+hipError_t launch_delta_pairs(const DeltaPairs& a, bool back, hipStream_t stream);
+
+__device__ __forceinline__ int seq_len(const int* lens, int b, int T) { return lens ? min(max(lens[b], 0), T) : T; }
+
+// The factor e^{G_C} of a chunk, given as the block's pair: what each rounding
+// leaves out goes into the next factor, so the factors' product stays the
+// product however many chunks there are.
+struct ChunkDecay {
+    float left = 0.f;
+    __device__ float operator()(float f, float rest) {
+        const float d = f * (rest + left), got = f + d;
+        left = got > 1e-30f ? (d - (got - f)) / got : 0.f;
+        return got;
+    }
+};
+
+// Workgroup x of units x tiles: a unit's tiles follow each other on one XCD
+// (workgroups go round the eight), whose L2 then serves what they read in common.
+__device__ __forceinline__ void unit_tile(int x, int units, int tiles, int& unit, int& tile) {
+    const int whole = units / 8 * 8, rest = x - whole * tiles;
+    unit = rest < 0 ? x / 8 / tiles * 8 + x % 8 : whole + rest / tiles;
+    tile = rest < 0 ? x / 8 % tiles : rest % tiles;
+}
+
+// Eight consecutive elements of a row as loaded, 16 bytes of bf16 or 32 of fp32.
+template <typename E> struct Raw;
+template <> struct Raw<bf16> { u32x4 v; };
+template <> struct Raw<float> { u32x4 v, w; };
+template <typename E> __device__ __forceinline__ Raw<E> raw_load(Rsrc r, int off);
+template <> __device__ __forceinline__ Raw<bf16> raw_load<bf16>(Rsrc r, int off) { return {buf_load<u32x4>(r, off)}; }
+template <> __device__ __forceinline__ Raw<float> raw_load<float>(Rsrc r, int off) {
+    return {buf_load<u32x4>(r, off), buf_load<u32x4>(r, off + 16)};
+}
+__device__ __forceinline__ Terms<1> raw_terms(const Raw<bf16>& r) { return {{__builtin_bit_cast(bf16x8, r.v)}}; }
+__device__ __forceinline__ Terms<3> raw_terms(const Raw<float>& r) {
+    return to_terms<3>(__builtin_bit_cast(f32x4, r.v), __builtin_bit_cast(f32x4, r.w));
+}
+
+// An offset past any buffer's end, also 16 bytes further: such loads give zeros
+// and such stores are dropped.
+constexpr int kOffPast = -48;
+
+template <int N, int M>
+__device__ __forceinline__ Terms<N> first_terms(const Terms<M>& a) {
+    Terms<N> out;
+#pragma unroll
+    for (int i = 0; i < N; ++i) out.t[i] = a.t[i];
+    return out;
+}
+// Operands kept in LDS or in the workspace as N fragments `step` bytes apart.
+template <int N>
+__device__ __forceinline__ Terms<N> frag_terms(const char* p, int step) {
+    Terms<N> out;
+#pragma unroll
+    for (int i = 0; i < N; ++i) out.t[i] = *reinterpret_cast<const bf16x8*>(p + i * step + lane_id() * 16);
+    return out;
+}
+
+}  // namespace kda

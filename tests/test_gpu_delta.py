@@ -421,3 +421,27 @@ def test_the_same_call_gives_the_same_bits(dtype):
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+# ----------------------------------------------------------------- long sequences
+
+def test_long_slow_decays_keep_their_factor():
+    """20,000 tokens at decays near 1, keys of length 1 that write little: the state's error stays
+    that of fp32 sums.  Each of 625 chunks rounds the state by at most 2^-24 of itself, at random:
+    about sqrt(625) 2^-25 = 7.5e-7 of its norm, to which the weights add a few 2^-24; 4e-6 leaves
+    a factor of four.  Chunk factors rounded once would add up to 625 2^-25 = 1.9e-5."""
+    need_gpu()
+    import linear_attention_recurrence_05_amd as kda
+    x, _ = make(1, 20000, 4, 4, 32, 32, F32, seed=18)
+    x["g"] = torch.tensor([-1e-6, -3.1e-5, -1.7e-4, 0.0], device="cuda").expand(1, 20000, 4).contiguous()
+    x["beta"] *= 1e-3
+    _, S_T = kda.delta_prefill(*(x[n] for n in ARGS), x["S0"])
+    torch.cuda.synchronize()
+    a = torch.exp(x["g"][0, 0].double())[:, None, None]
+    S = x["S0"][0].double()
+    for t in range(20000):
+        k = x["k"][0, t].double()[:, :, None]
+        S = a * S
+        S = S + k * (x["beta"][0, t].double()[:, None] * (x["v"][0, t].double() - (k * S).sum(1)))[:, None]
+    err = torch.linalg.vector_norm(S_T[0].double() - S, dim=(1, 2)) / torch.linalg.vector_norm(S, dim=(1, 2))
+    assert (err < 4e-6).all(), err
