@@ -13,17 +13,20 @@ namespace kda {
 // waves' parts of K S (and of Q S, for o) are summed through LDS, in order, the one
 // barrier of a chunk; E and its scaled form are made by every wave, whose own
 // channels of the state they then update.
-template <typename E, int DK>
+// BACK: the gradients' forward sweep, which leaves e, the states and the parts of
+// dO . o, whose sum over the sequence needs o with fp32's accuracy (three terms).
+template <typename E, int DK, bool BACK>
 __global__ __launch_bounds__(DK * 2, 2) void delta_chain_kernel(DeltaChain p) {
     constexpr int C = kDeltaChunk, KM = DK / 32, NT = DK * 2;
-    constexpr int NE = sizeof(E) == 2 ? 1 : 3, NP = NE, ES = sizeof(E);
-    using Blk = DeltaBlock<NP, false>;
+    constexpr int NE = sizeof(E) == 2 ? 1 : 3, NP = BACK ? 3 : NE, ES = sizeof(E);
+    using Blk = DeltaBlock<NP, BACK>;
     constexpr int LK = 40, LV = 24;                          // padded rows of the K slice and of v in LDS
-    constexpr int PB = Blk::bytes / 16, RB = (PB + NT - 1) / NT;   // pieces of a block, a thread's
+    constexpr int kStage = BACK ? Blk::row + 512 : Blk::bytes;     // the block's part that is read here
+    constexpr int PB = kStage / 16, RB = (PB + NT - 1) / NT;   // pieces of a block, a thread's
     constexpr int PV = C * 16 * ES / 16, RV = (PV + NT - 1) / NT;  // pieces of v's tile
     __shared__ __align__(16) bf16 s_k[KM][NE][C * LK];
     __shared__ __align__(16) bf16 s_v[2][NE][C * LV];
-    __shared__ __align__(16) char s_blk[2][Blk::bytes];
+    __shared__ __align__(16) char s_blk[2][kStage];
     __shared__ f32x4 s_part[KM > 1 ? 2 : 1][KM > 1 ? KM : 1][4][kWave];
 
     const int tiles = p.dv / 16, units = p.B * p.H;
@@ -72,7 +75,7 @@ __global__ __launch_bounds__(DK * 2, 2) void delta_chain_kernel(DeltaChain p) {
         const int rows = c < c_end ? min(C, n - c * C) : 0;
         const size_t base = (((size_t)b * p.T + (size_t)c * C) * p.H + h) * p.dv + 16 * tile;
         const Rsrc rv = make_rsrc((const E*)p.v + base, rows > 0 ? (uint32_t)((rows - 1) * ldv + 16 * ES) : 0);
-        const Rsrc rb = make_rsrc(blocks + (size_t)(c - p.c0) * Blk::bytes, rows > 0 ? Blk::bytes : 0);
+        const Rsrc rb = make_rsrc(blocks + (size_t)(c - p.c0) * Blk::bytes, rows > 0 ? kStage : 0);
         constexpr int PR = ES;                               // 16-byte pieces of a row of 16 elements
 #pragma unroll
         for (int i = 0; i < RV; ++i) {
@@ -87,20 +90,7 @@ __global__ __launch_bounds__(DK * 2, 2) void delta_chain_kernel(DeltaChain p) {
 #pragma unroll
         for (int i = 0; i < RV; ++i) {
             const int at = tid + i * NT, row = at / PR;
-            if (PV % NT == 0 || at < PV) {
-                if constexpr (NE == 1) {
-                    *reinterpret_cast<u32x4*>(&s_v[buf][0][row * LV + at % PR * 8]) = x.v[i];
-                } else {
-                    f32x4 f = __builtin_bit_cast(f32x4, x.v[i]);
-#pragma unroll
-                    for (int s = 0; s < NE; ++s) {
-                        const bf16x4 t = pack4(f);
-                        *reinterpret_cast<bf16x4*>(&s_v[buf][s][row * LV + at % PR * 4]) = t;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) f[e] -= (float)t[e];
-                    }
-                }
-            }
+            if (PV % NT == 0 || at < PV) put_piece<E>(&s_v[buf][0][row * LV + at % PR * (16 / ES)], C * LV, x.v[i]);
         }
 #pragma unroll
         for (int i = 0; i < RB; ++i)
@@ -121,6 +111,21 @@ __global__ __launch_bounds__(DK * 2, 2) void delta_chain_kernel(DeltaChain p) {
             for (int i = 0; i < NE; ++i) *reinterpret_cast<bf16x8*>(&s_k[kw][i][(16 * q + j) * LK + 8 * g]) = kt[q].t[i];
         }
         load_own(c + 2, own[s]);
+        const DeltaSweep& sw = p.sweep;
+        if (BACK && c % kSuperChunks == 0) {
+            E* dst = (E*)sw.S + (((size_t)unit * sw.NS + c / kSuperChunks) * p.dv + 16 * tile + j) * DK + 32 * kw + 8 * g;
+            store8(dst, M[0], M[1]);
+        }
+        f32x4 dO[2];                                         // set out for early
+        if constexpr (BACK) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int t = c * C + 16 * q + j;
+                dO[q] = zero4();
+                if ((KM == 1 || kw == q) && t < n)
+                    load4((const E*)sw.dO + (((size_t)b * p.T + t) * p.H + h) * p.dv + 16 * tile + 4 * g, dO[q]);
+            }
+        }
         // K S (rows: tokens) and (Q S)^T (columns: tokens) of this wave's channels
         const Terms<3> sf = to_terms<3>(M[0], M[1]);
         f32x4 ks[2], qs[2];
@@ -175,6 +180,19 @@ __global__ __launch_bounds__(DK * 2, 2) void delta_chain_kernel(DeltaChain p) {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
             M[t] = mma(col_terms<NE>(&s_k[kw][0][0], C * LK, LK, 4 * t, 8, j, g), ut, f * M[t]);
+        if constexpr (BACK) {
+            if (kw == KM - 1) {                              // every wave has E
+                f32x4* dst = reinterpret_cast<f32x4*>(sw.e + (((size_t)unit * sw.NC + c) * p.dv + 16 * tile + j) * C) + g;
+                dst[0] = e[0];
+                dst[4] = e[1];
+            }
+            if (c % kAnchorChunks == kAnchorChunks - 1 || c == c_end - 1) {
+                f32x4* dst = reinterpret_cast<f32x4*>(sw.end) +
+                             ((((size_t)unit * sw.NA + c / kAnchorChunks) * tiles + tile) * KM + kw) * 2 * kWave + lane;
+                dst[0] = M[0];
+                dst[kWave] = M[1];
+            }
+        }
         // o: the waves' first two (the only one's both) columns of tokens
         const Terms<NP> et = to_terms<NP>(e[0], e[1]);
 #pragma unroll
@@ -188,7 +206,14 @@ __global__ __launch_bounds__(DK * 2, 2) void delta_chain_kernel(DeltaChain p) {
             }
             o = mma(et, frag_terms<NP>(blk + Blk::pair + q * kFragBytes, 2 * kFragBytes), (p.scale * row[16 * q + j]) * o);
             const int t = c * C + 16 * q + j;
-            if (t < n) {
+            if constexpr (BACK) {
+                float d = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d += dO[q][i] * o[i];
+                d += __shfl_xor(d, 16);
+                d += __shfl_xor(d, 32);
+                if (g == 0) sw.dot[((size_t)tile * units + unit) * sw.NC * C + t] = d;
+            } else if (t < n) {
                 E* dst = (E*)p.o + (((size_t)b * p.T + t) * p.H + h) * p.dv + 16 * tile + 4 * g;
                 if constexpr (ES == 2)
                     *reinterpret_cast<bf16x4*>(dst) = pack4(o);
@@ -247,15 +272,19 @@ size_t delta_prefill_ws_bytes(int B, int T, int H, int dk, int dv, bool is_bf16)
     return w.blocks + w.carry;
 }
 
-template <typename E>
+template <typename E, bool BACK>
 static hipError_t launch_chain(const DeltaChain& a, hipStream_t stream) {
     const dim3 grid((unsigned)(a.B * a.H * (a.dv / 16)));
     switch (a.dk) {
-        case 32: hipLaunchKernelGGL((delta_chain_kernel<E, 32>), grid, dim3(64), 0, stream, a); break;
-        case 64: hipLaunchKernelGGL((delta_chain_kernel<E, 64>), grid, dim3(128), 0, stream, a); break;
-        default: hipLaunchKernelGGL((delta_chain_kernel<E, 128>), grid, dim3(256), 0, stream, a); break;
+        case 32: hipLaunchKernelGGL((delta_chain_kernel<E, 32, BACK>), grid, dim3(64), 0, stream, a); break;
+        case 64: hipLaunchKernelGGL((delta_chain_kernel<E, 64, BACK>), grid, dim3(128), 0, stream, a); break;
+        default: hipLaunchKernelGGL((delta_chain_kernel<E, 128, BACK>), grid, dim3(256), 0, stream, a); break;
     }
     return hipGetLastError();
+}
+
+hipError_t launch_delta_sweep(const DeltaChain& a, hipStream_t stream) {
+    return a.is_bf16 ? launch_chain<bf16, true>(a, stream) : launch_chain<float, true>(a, stream);
 }
 
 hipError_t launch_delta_prefill(const DeltaPrefill& a, void* ws, hipStream_t stream) {
@@ -270,8 +299,8 @@ hipError_t launch_delta_prefill(const DeltaPrefill& a, void* ws, hipStream_t str
         hipError_t e = launch_delta_pairs({a.q, a.k, a.g, a.beta, a.scale, S, a.lens, blocks, a.B, a.T, a.H, a.Hk, a.dk, c0, c1,
                                            a.is_bf16}, false, stream);
         if (e != hipSuccess) return e;
-        const DeltaChain c{a.q, a.k, a.v, a.scale, S, a.lens, blocks, a.o, a.B, a.T, a.H, a.Hk, a.dk, a.dv, c0, c1, a.is_bf16};
-        e = a.is_bf16 ? launch_chain<bf16>(c, stream) : launch_chain<float>(c, stream);
+        const DeltaChain c{a.q, a.k, a.v, a.scale, S, a.lens, blocks, a.o, a.B, a.T, a.H, a.Hk, a.dk, a.dv, c0, c1, a.is_bf16, {}};
+        e = a.is_bf16 ? launch_chain<bf16, false>(c, stream) : launch_chain<float, false>(c, stream);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;

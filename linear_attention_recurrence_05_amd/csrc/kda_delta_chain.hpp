@@ -7,6 +7,26 @@
 
 namespace kda {
 
+// Chunks whose end has an anchor <S, Y> of dg (kda_delta_backward.hip), and those
+// that share one state in the gradients of q and k.
+constexpr int kAnchorChunks = 8, kSuperChunks = 2;
+
+// What the gradients' sweeps leave in the workspace, for unit u = b H + h, chunk
+// c of NC, superchunk s of NS, anchor a of NA, column tile t of `tiles`:
+//   e     [u][c][dv][32] fp32        e_t of every token
+//   S, Y  [u][s][dv][dk] of E        the state before a superchunk, and the
+//                                    gradient of the one after it, transposed
+//   end   [u][a][t] state tiles      the state at an anchor, as the chain holds it
+//   anchor[u][a][t][DK / 32] fp32    parts of <S, Y>
+//   dot   [2][t][u][32 NC] fp32      parts of dO . o - dv . v, and of dbeta
+struct DeltaSweep {
+    const void* dO;
+    float* e;
+    void *S, *Y;
+    float *end, *anchor, *dot;
+    int NC, NS, NA;
+};
+
 // Chunks c0 .. c1 - 1 from the state S.in to S.out.
 struct DeltaChain {
     const void *q, *k, *v;
@@ -17,6 +37,8 @@ struct DeltaChain {
     void* o;
     int B, T, H, Hk, dk, dv, c0, c1;
     bool is_bf16;
+    DeltaSweep sweep;       // of the gradients' forward sweep, which leaves no o
 };
+hipError_t launch_delta_sweep(const DeltaChain& a, hipStream_t stream);
 
 }  // namespace kda

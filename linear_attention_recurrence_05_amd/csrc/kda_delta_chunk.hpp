@@ -90,6 +90,37 @@ __device__ __forceinline__ Terms<3> raw_terms(const Raw<float>& r) {
     return to_terms<3>(__builtin_bit_cast(f32x4, r.v), __builtin_bit_cast(f32x4, r.w));
 }
 
+// A 16-byte piece of a row to LDS: bf16 as it is, four fp32 values as their three
+// terms, `plane` elements apart.
+template <typename E>
+__device__ __forceinline__ void put_piece(bf16* dst, int plane, u32x4 v) {
+    if constexpr (sizeof(E) == 2) {
+        *reinterpret_cast<u32x4*>(dst) = v;
+    } else {
+        f32x4 x = __builtin_bit_cast(f32x4, v);
+#pragma unroll
+        for (int s = 0; s < 3; ++s) {
+            const bf16x4 h = pack4(x);
+            *reinterpret_cast<bf16x4*>(dst + s * plane) = h;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] -= (float)h[i];
+        }
+    }
+}
+
+// Four elements from memory, and eight to it.
+__device__ __forceinline__ void load4(const bf16* p, f32x4& x) {
+    const bf16x4 v = *reinterpret_cast<const bf16x4*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = (float)v[i];
+}
+__device__ __forceinline__ void load4(const float* p, f32x4& x) { x = *reinterpret_cast<const f32x4*>(p); }
+__device__ __forceinline__ void store8(bf16* p, f32x4 lo, f32x4 hi) { *reinterpret_cast<bf16x8*>(p) = pack8(lo, hi); }
+__device__ __forceinline__ void store8(float* p, f32x4 lo, f32x4 hi) {
+    reinterpret_cast<f32x4*>(p)[0] = lo;
+    reinterpret_cast<f32x4*>(p)[1] = hi;
+}
+
 // An offset past any buffer's end, also 16 bytes further: such loads give zeros
 // and such stores are dropped.
 constexpr int kOffPast = -48;
