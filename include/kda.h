@@ -589,7 +589,7 @@ kda_status kda_qk_norm_rope_backward(const void *q, const void *k, const float *
  *   zero state) are taken as -10000, for which a is exactly 0.  beta may be any
  *   finite number ((0, 1) is usual; keys of length 1 keep the recurrence stable
  *   up to 2).
- * - B * H <= 2^19.
+ * - B * H <= 2^19, and H times the larger head size <= 2^22.
  * - With bf16, an output's o, dq and dk take the state, the pairs' weights and
  *   what each token writes as one bf16 term on their way into the output; the
  *   states, dg, dbeta and dS0, and dv before its own rounding, are fp32

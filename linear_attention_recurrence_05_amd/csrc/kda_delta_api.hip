@@ -13,6 +13,9 @@ kda_status check_delta(int B, int T, int H, int H_k, int d_k, int d_v, kda_dtype
     if (s != KDA_OK) return s;
     if ((long long)B * H > kda::kDeltaMaxUnits)
         return fail(KDA_ERR_INVALID_SHAPE, "B*H = %lld is too large (limit 2^19)", (long long)B * H);
+    // 64 tokens of a head lie within 2^30 bytes
+    if ((long long)H * (d_k > d_v ? d_k : d_v) > (1LL << 22))
+        return fail(KDA_ERR_INVALID_SHAPE, "H*d = %lld is too large (limit 2^22)", (long long)H * (d_k > d_v ? d_k : d_v));
     return KDA_OK;
 }
 

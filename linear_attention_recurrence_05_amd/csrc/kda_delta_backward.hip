@@ -34,239 +34,205 @@ struct DeltaReverse {
     int B, T, H, Hk, dk, dv;
 };
 
-// The chain from the last chunk to the first; as delta_chain_kernel: one workgroup
-// per (b, h, 16 value columns), one wave for each 32 key channels of Y.
+// The chain from the last chunk to the first, as delta_chain_kernel: one workgroup of
+// four waves per (b, h, 16 value columns), wave w with Y's rows of key channels
+// 32 w .. and the chunk's 16 tokens of tile w, three barriers a chunk:
+//   K Y of the wave's channels for all tokens                                    |
+//   dU of the wave's tokens, e^G dO                                              |
+//   Z = the inverse's transpose times dU of the wave's tokens, -e^G beta Z; and Z
+//   with a token a lane for what leaves the kernel                               |
+//   Y's update from all tokens
 template <typename E, int DK>
-__global__ __launch_bounds__(DK * 2, 2) void delta_reverse_kernel(DeltaReverse p) {
-    constexpr int C = kDeltaChunk, KM = DK / 32, NT = DK * 2;
-    constexpr int NE = sizeof(E) == 2 ? 1 : 3, ES = sizeof(E);
+__global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_reverse_kernel(DeltaReverse p) {
+    constexpr int C = kDeltaChunk, KM = DK / 32, ES = sizeof(E), NE = ES == 2 ? 1 : 3;
     using Blk = DeltaBlock<3, true>;
-    constexpr int kFrom = Blk::row, kStage = Blk::bytes - kFrom;             // the block's part that is read here
-    constexpr int LK = 40, LV = 24;
-    constexpr int PB = kStage / 16, RB = (PB + NT - 1) / NT;
-    constexpr int PR = ES, PV = C * PR, RV = (PV + NT - 1) / NT;             // pieces of 16 bytes of dO's rows, of its tile
-    __shared__ __align__(16) bf16 s_k[KM][NE][C * LK], s_q[KM][NE][C * LK];
-    __shared__ __align__(16) bf16 s_v[2][NE][C * LV];
-    __shared__ __align__(16) char s_blk[2][kStage];
-    __shared__ f32x4 s_part[KM > 1 ? 2 : 1][KM > 1 ? KM : 1][2][kWave];
+    constexpr int LK = NE == 1 ? 40 : 32, LV = 24;           // padded rows in LDS
+    __shared__ __align__(16) bf16 s_k[KM][NE][C * LK], s_q[KM][NE][C * LK];   // a wave's own channels
+    __shared__ __align__(16) bf16 s_o[NE][C * LV];           // dO's tile
+    __shared__ f32x4 s_part[KM][kDeltaTiles][kWave];
+    __shared__ __align__(16) char s_d[2][3 * kFragBytes], s_gq[2][3 * kFragBytes], s_gr[2][3 * kFragBytes];
 
     const int tiles = p.dv / 16, units = p.B * p.H;
     int unit, tile;
     unit_tile(blockIdx.x, units, tiles, unit, tile);
     const int b = unit / p.H, h = unit % p.H, hk = h / (p.H / p.Hk);
     const int n = seq_len(p.lens, b, p.T), c_end = (n + C - 1) / C;
-    const int tid = threadIdx.x, kw = wave_id(), lane = lane_id(), j = lane & 15, g = lane >> 4;
+    const int w = wave_id(), lane = lane_id(), j = lane & 15, g = lane >> 4;
+    const bool holds = KM == 4 || w < KM;                    // this wave has channels
     const DeltaSweep& sw = p.sweep;
 
-    const size_t state = (size_t)DK * p.dv;
-    f32x4 Y[2];
-    {
-        const float* in = p.dST ? p.dST + (size_t)unit * state : nullptr;
+    const size_t state = (size_t)DK * p.dv, at_state = (size_t)unit * state + (size_t)(32 * w + 8 * g) * p.dv + 16 * tile + j;
+    f32x4 Y[2] = {zero4(), zero4()};
+    if (holds && p.dST) {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) Y[t][i] = in ? in[(size_t)(32 * kw + 8 * g + 4 * t + i) * p.dv + 16 * tile + j] : 0.f;
+            for (int i = 0; i < 4; ++i) Y[t][i] = p.dST[at_state + (size_t)(4 * t + i) * p.dv];
     }
 
+    // ---- what a chunk reads.  Rows past the sequence's end, and chunks before the
+    // first, give zeros.
     const int ldk = p.Hk * DK * ES, ldv = p.H * p.dv * ES;
-    struct Own {
-        Raw<E> k[2], q[2];
+    const size_t at_k = (((size_t)b * p.T) * p.Hk + hk) * DK * ES;
+    const size_t at_v = (((size_t)b * p.T) * p.H + h) * p.dv * ES + (size_t)16 * tile * ES;
+    const char* pb = p.blocks + (size_t)unit * sw.NC * Blk::bytes;
+    auto rows_of = [&](int c) { return c >= 0 ? min(C, n - c * C) : 0; };
+    auto rows_rsrc = [&](const void* base, size_t at, int c, int rows, int ld, int width) {
+        return make_rsrc((const char*)base + at + (int64_t)max(c, 0) * C * ld, rows > 0 ? (uint32_t)((rows - 1) * ld + width) : 0);
     };
-    struct Common {
-        u32x4 v[RV], blk[RB];
-    };
-    auto load_own = [&](int c, Own& x) {                     // chunks before the first load nothing
-        const int rows = c >= 0 ? min(C, n - c * C) : 0;
-        const size_t base = (((size_t)b * p.T + (size_t)max(c, 0) * C) * p.Hk + hk) * DK + 32 * kw;
-        const uint32_t bytes = rows > 0 ? (uint32_t)((rows - 1) * ldk + 32 * ES) : 0;
-        const Rsrc rk = make_rsrc((const E*)p.k + base, bytes), rq = make_rsrc((const E*)p.q + base, bytes);
+    auto blk_rsrc = [&](int c) { return make_rsrc(pb + (int64_t)max(c, 0) * Blk::bytes, c >= 0 ? Blk::bytes : 0); };
+    Raw<E> rk[kDeltaTiles], rq[kDeltaTiles];
+    u32x4 ro;
+    f32x4 v, e, grow, end, beta, S[2];
+    Terms<3> rt[2], rp[2];
+    float beta_j, decay_f, decay_rest, dot;
+    auto load_rows = [&](int c) {                            // K, Q and dO
+        const int rows = rows_of(c);
+        const Rsrc k = rows_rsrc(p.k, at_k, c, holds ? rows : 0, ldk, DK * ES), q = rows_rsrc(p.q, at_k, c, holds ? rows : 0, ldk, DK * ES);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int off = 16 * q + j < rows ? (16 * q + j) * ldk + 8 * g * ES : kOffPast;
-            x.k[q] = raw_load<E>(rk, off);
-            x.q[q] = raw_load<E>(rq, off);
+        for (int a = 0; a < kDeltaTiles; ++a) {
+            const int off = 16 * a + j < rows ? (16 * a + j) * ldk + (32 * w + 8 * g) * ES : kOffPast;
+            rk[a] = raw_load<E>(k, off);
+            rq[a] = raw_load<E>(q, off);
         }
+        const int row = 16 * w + lane / ES;
+        ro = buf_load<u32x4>(rows_rsrc(sw.dO, at_v, c, rows, ldv, 16 * ES),
+                             lane < 16 * ES && row < rows ? row * ldv + lane % ES * 16 : kOffPast);
     };
-    const char* blocks = p.blocks + (size_t)unit * sw.NC * Blk::bytes + kFrom;
-    auto load_common = [&](int c, Common& x) {
-        const int rows = c >= 0 ? min(C, n - c * C) : 0;
-        const size_t base = (((size_t)b * p.T + (size_t)max(c, 0) * C) * p.H + h) * p.dv + 16 * tile;
-        const Rsrc rv = make_rsrc((const E*)sw.dO + base, rows > 0 ? (uint32_t)((rows - 1) * ldv + 16 * ES) : 0);
-        const Rsrc rb = make_rsrc(blocks + (size_t)max(c, 0) * Blk::bytes, rows > 0 ? kStage : 0);
+    auto is_anchor = [&](int c) { return holds && c >= 0 && (c % kAnchorChunks == kAnchorChunks - 1 || c == c_end - 1); };
+    auto anchor_at = [&](int c) { return (((size_t)unit * sw.NA + max(c, 0) / kAnchorChunks) * tiles + tile) * KM + (holds ? w : 0); };
+    auto load_pair = [&](int c) {
+        const Rsrc r = blk_rsrc(c);
 #pragma unroll
-        for (int i = 0; i < RV; ++i) {
-            const int at = tid + i * NT, row = at / PR;
-            x.v[i] = buf_load<u32x4>(rv, at < PV && row < rows ? row * ldv + at % PR * 16 : kOffPast);
-        }
+        for (int x = 0; x < 2; ++x) rp[x] = load_terms<3>(r, x >= w / 2 ? Blk::pairt + upper(w, x) * 3 * kFragBytes : kOffPast);
+        grow = __builtin_bit_cast(f32x4, buf_load<u32x4>(r, Blk::row + (kRowGrow + 16 * w + 4 * g) * 4));
+        end = __builtin_bit_cast(f32x4, buf_load<u32x4>(r, Blk::row + (kRowEnd + 16 * w + 4 * g) * 4));
+        const f32x4 d = __builtin_bit_cast(f32x4, buf_load<u32x4>(r, Blk::row + kRowDecay * 4));
+        decay_f = d[0];
+        decay_rest = d[1];
+        const Rsrc m = make_rsrc((const f32x4*)sw.end + anchor_at(c) * 2 * kWave, 2 * kWave * 16);
 #pragma unroll
-        for (int i = 0; i < RB; ++i) x.blk[i] = buf_load<u32x4>(rb, tid + i * NT < PB ? (tid + i * NT) * 16 : kOffPast);
+        for (int t = 0; t < 2; ++t)
+            S[t] = __builtin_bit_cast(f32x4, buf_load<u32x4>(m, is_anchor(c) ? (t * kWave + lane) * 16 : kOffPast));
     };
-    auto stage_common = [&](int buf, const Common& x) {
+    auto load_inv = [&](int c) {                             // and what the outputs take: v, e and dO . o of token 16 w + j
+        const int rows = rows_of(c);
+        const Rsrc r = blk_rsrc(c);
 #pragma unroll
-        for (int i = 0; i < RV; ++i) {
-            const int at = tid + i * NT, row = at / PR;
-            if (PV % NT == 0 || at < PV) put_piece<E>(&s_v[buf][0][row * LV + at % PR * (16 / ES)], C * LV, x.v[i]);
-        }
+        for (int x = 0; x < 2; ++x) rt[x] = load_terms<3>(r, x >= w / 2 ? Blk::invt + upper(w, x) * 3 * kFragBytes : kOffPast);
+        beta = __builtin_bit_cast(f32x4, buf_load<u32x4>(r, Blk::row + (kRowBeta + 16 * w + 4 * g) * 4));
+        beta_j = __builtin_bit_cast(float, buf_load<uint32_t>(r, Blk::row + (kRowBeta + 16 * w + j) * 4));
+        v = buf_load4<E>(rows_rsrc(p.v, at_v, c, rows, ldv, 16 * ES), 16 * w + j < rows ? (16 * w + j) * ldv + 4 * g * ES : kOffPast);
+        const Rsrc re = make_rsrc(sw.e + (((size_t)unit * sw.NC + max(c, 0)) * p.dv + 16 * tile) * C, c >= 0 ? 16 * C * 4 : 0);
 #pragma unroll
-        for (int i = 0; i < RB; ++i)
-            if (PB % NT == 0 || tid + i * NT < PB) reinterpret_cast<u32x4*>(s_blk[buf])[tid + i * NT] = x.blk[i];
+        for (int i = 0; i < 4; ++i) e[i] = __builtin_bit_cast(float, buf_load<uint32_t>(re, ((4 * g + i) * C + 16 * w + j) * 4));
+        const Rsrc rd = make_rsrc(sw.dot + (((size_t)tile * units + unit) * sw.NC + max(c, 0)) * C, c >= 0 ? C * 4 : 0);
+        dot = __builtin_bit_cast(float, buf_load<uint32_t>(rd, (16 * w + j) * 4));
     };
 
     ChunkDecay decay;
-    Own own[2];
-    Common common;
-    auto chunk = [&](auto set, int c) {
-        constexpr int s = decltype(set)::value;
-        Terms<NE> kt[2];
+    if (c_end > 0) {
+        load_rows(c_end - 1);
+        load_pair(c_end - 1);
+        load_inv(c_end - 1);
+    }
+    for (int c = c_end - 1; c >= 0; --c) {
+        const int rows = min(C, n - c * C);
+        // ---- K Y of the wave's channels; Y itself, for dk, and at an anchor <S, Y>
+        buf_store8<E>(make_rsrc((E*)sw.Y + (((size_t)unit * sw.NC + c) * p.dv + 16 * tile) * DK, 16 * DK * ES),
+                      holds ? (j * DK + 32 * w + 8 * g) * ES : kOffPast, Y[0], Y[1]);
+        float a = 0.f;
+        if (is_anchor(c)) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            kt[q] = raw_terms(own[s].k[q]);
-            const Terms<NE> qt = raw_terms(own[s].q[q]);
+            for (int i = 0; i < 4; ++i) a += S[0][i] * Y[0][i] + S[1][i] * Y[1][i];
 #pragma unroll
-            for (int i = 0; i < NE; ++i) {
-                *reinterpret_cast<bf16x8*>(&s_k[kw][i][(16 * q + j) * LK + 8 * g]) = kt[q].t[i];
-                *reinterpret_cast<bf16x8*>(&s_q[kw][i][(16 * q + j) * LK + 8 * g]) = qt.t[i];
+            for (int o = 1; o < kWave; o <<= 1) a += __shfl_xor(a, o);
+        }
+        buf_store_u32(make_rsrc(sw.anchor + anchor_at(c), 4), is_anchor(c) && lane == 0 ? 0 : kOffPast, __builtin_bit_cast(uint32_t, a));
+        if (holds) {
+            const Terms<3> yf = to_terms<3>(Y[0], Y[1]);
+#pragma unroll
+            for (int x = 0; x < kDeltaTiles; ++x) {
+                const Terms<NE> kt = raw_terms(rk[x]), qt = raw_terms(rq[x]);
+#pragma unroll
+                for (int i = 0; i < NE; ++i) {
+                    *reinterpret_cast<bf16x8*>(&s_k[w][i][(16 * x + j) * LK + 8 * g]) = kt.t[i];
+                    *reinterpret_cast<bf16x8*>(&s_q[w][i][(16 * x + j) * LK + 8 * g]) = qt.t[i];
+                }
+                s_part[w][x][lane] = mma(kt, yf, zero4());
             }
         }
-        load_own(c - 2, own[s]);
-        // what the outputs need, set out for early: v and e of token 16 q + j
-        f32x4 v[2], e[2];
+        put_piece<E>(&s_o[0][(16 * w + min(lane / ES, 15)) * LV + lane % ES * (16 / ES)], C * LV, ro, lane < 16 * ES);
+        load_rows(c - 1);
+        __syncthreads();
+        // ---- dU of the wave's tokens; e^G dO
+        f32x4 u = s_part[0][w][lane];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int t = c * C + 16 * q + j;
-            v[q] = e[q] = zero4();
-            if ((KM > 1 && kw != q) || t >= n) continue;
-            load4((const E*)p.v + (((size_t)b * p.T + t) * p.H + h) * p.dv + 16 * tile + 4 * g, v[q]);
-            const float* from = sw.e + (((size_t)unit * sw.NC + c) * p.dv + 16 * tile + 4 * g) * C + 16 * q + j;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) e[q][i] = from[i * C];
+        for (int m = 1; m < KM; ++m) u += s_part[m][w][lane];
+        u *= end;
+        if (w < 2) u = mma(rp[0], col_terms<NE>(&s_o[0][0], C * LV, LV, 0, 4, j, g), u);
+        u = mma(rp[1], col_terms<NE>(&s_o[0][32 * LV], C * LV, LV, 0, 4, j, g), u);
+        put_half<3>(s_d[w >> 1], w & 1, u);
+        put_half<3>(s_gq[w >> 1], w & 1, p.scale * grow * col4<NE>(&s_o[0][16 * w * LV], C * LV, LV, j, g));
+        const f32x4 eg = grow;
+        const float f = decay(decay_f, decay_rest);
+        load_pair(c - 1);
+        __syncthreads();
+        // ---- Z of the wave's tokens, a column a lane and (zt) a token a lane
+        const Terms<3> d1 = frag_terms<3>(s_d[1]);
+        f32x4 z = mma(rt[1], d1, zero4()), zt = mma(d1, rt[1], zero4());
+        if (w < 2) {
+            const Terms<3> d0 = frag_terms<3>(s_d[0]);
+            z = mma(rt[0], d0, z);
+            zt = mma(d0, rt[0], zt);
         }
-        if (c % kSuperChunks == kSuperChunks - 1 || c == c_end - 1) {
-            E* dst = (E*)sw.Y + (((size_t)unit * sw.NS + c / kSuperChunks) * p.dv + 16 * tile + j) * DK + 32 * kw + 8 * g;
-            store8(dst, Y[0], Y[1]);
-        }
-        if (c % kAnchorChunks == kAnchorChunks - 1 || c == c_end - 1) {
-            const size_t at = (((size_t)unit * sw.NA + c / kAnchorChunks) * tiles + tile) * KM + kw;
-            const f32x4* S = reinterpret_cast<const f32x4*>(sw.end) + at * 2 * kWave + lane;
-            float d = 0.f;
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) d += S[t * kWave][i] * Y[t][i];
-#pragma unroll
-            for (int o = 1; o < kWave; o <<= 1) d += __shfl_xor(d, o);
-            if (lane == 0) sw.anchor[at] = d;
-        }
-        // K Y of this wave's channels
-        const Terms<3> yf = to_terms<3>(Y[0], Y[1]);
-        f32x4 x[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            x[q] = mma(kt[q], yf, zero4());
-            if constexpr (KM > 1) s_part[s][kw][q][lane] = x[q];
-        }
-        __syncthreads();                                     // the parts are there, and this chunk's block and dO
-        if constexpr (KM > 1) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                x[q] = s_part[s][0][q][lane];
-#pragma unroll
-                for (int w = 1; w < KM; ++w) x[q] += s_part[s][w][q][lane];
-            }
-        }
-        const char* blk = s_blk[s] - kFrom;
-        const float *row = reinterpret_cast<const float*>(blk + Blk::row), *more = reinterpret_cast<const float*>(blk + Blk::more);
-        // dU, Z
-        const Terms<NE> dOt = col_terms<NE>(&s_v[s][0][0], C * LV, LV, 0, 4, j, g);
-        f32x4 u[2], z[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const f32x4 end = *reinterpret_cast<const f32x4*>(more + 16 * q + 4 * g);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) u[q][i] = end[i] * x[q][i];
-            u[q] = mma(frag_terms<3>(blk + Blk::pairt + q * kFragBytes, 2 * kFragBytes), dOt, u[q]);
-        }
-        const Terms<3> ut = to_terms<3>(u[0], u[1]);
-#pragma unroll
-        for (int q = 0; q < 2; ++q) z[q] = mma(frag_terms<3>(blk + Blk::invt + q * kFragBytes, 2 * kFragBytes), ut, zero4());
-        stage_common(1 - s, common);
-        load_common(c - 2, common);
-        // Y' = e^{G_C} Y + Q^T (e^G dO) - K^T (e^G beta Z)
-        f32x4 dO[2], gq[2], gr[2];
-        to_f32(dOt, dO[0], dO[1]);
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const f32x4 eg = *reinterpret_cast<const f32x4*>(row + 16 * q + 4 * g);
-            const f32x4 beta = *reinterpret_cast<const f32x4*>(more + C + 16 * q + 4 * g);
+        put_half<3>(s_gr[w >> 1], w & 1, -eg * (beta * z));
+        // ---- out: dv = beta Z; dO . o - dv . v, and dbeta = Z . E
+        {
+            const f32x4 r = beta_j * zt;
+            float x = 0.f, db = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                gq[q][i] = p.scale * eg[i] * dO[q][i];
-                gr[q][i] = -eg[i] * (beta[i] * z[q][i]);
+                x += r[i] * v[i];
+                db += zt[i] * e[i];
             }
-        }
-        const Terms<3> gqt = to_terms<3>(gq[0], gq[1]), grt = to_terms<3>(gr[0], gr[1]);
-        const float f = decay(row[2 * C], row[2 * C + 1]);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            Y[t] = mma(col_terms<NE>(&s_q[kw][0][0], C * LK, LK, 4 * t, 8, j, g), gqt, f * Y[t]);
-            Y[t] = mma(col_terms<NE>(&s_k[kw][0][0], C * LK, LK, 4 * t, 8, j, g), grt, Y[t]);
-        }
-        // out: Z once more with a token a lane, of the first two waves (the only
-        // one's both) columns of tokens
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            if (KM > 1 && kw != q) continue;
-            const f32x4 zt = mma(ut, frag_terms<3>(blk + Blk::invt + q * kFragBytes, 2 * kFragBytes), zero4());
-            const float beta = more[C + 16 * q + j];
-            const int t = c * C + 16 * q + j;
-            f32x4 r;
-            float d = 0.f, db = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                r[i] = beta * zt[i];
-                d += r[i] * v[q][i];
-                db += zt[i] * e[q][i];
-            }
-            d += __shfl_xor(d, 16);
-            d += __shfl_xor(d, 32);
+            x += __shfl_xor(x, 16);
+            x += __shfl_xor(x, 32);
             db += __shfl_xor(db, 16);
             db += __shfl_xor(db, 32);
-            if (g == 0) {
-                float* dot = sw.dot + ((size_t)tile * units + unit) * sw.NC * C + t;
-                *dot -= d;
-                dot[(size_t)tiles * units * sw.NC * C] = db;
-            }
-            if (t < n) {
-                E* dst = (E*)p.dv_out + (((size_t)b * p.T + t) * p.H + h) * p.dv + 16 * tile + 4 * g;
-                if constexpr (ES == 2)
-                    *reinterpret_cast<bf16x4*>(dst) = pack4(r);
-                else
-                    *reinterpret_cast<f32x4*>(dst) = r;
-            }
+            const int at = g == 0 ? (16 * w + j) * 4 : kOffPast;
+            buf_store_u32(make_rsrc(sw.dot + (((size_t)tile * units + unit) * sw.NC + c) * C, C * 4), at, __builtin_bit_cast(uint32_t, dot - x));
+            buf_store_u32(make_rsrc(sw.dot + (((size_t)(tiles + tile) * units + unit) * sw.NC + c) * C, C * 4), at,
+                          __builtin_bit_cast(uint32_t, db));
+            const Rsrc to = rows_rsrc(p.dv_out, at_v, c, rows, ldv, 16 * ES);
+            const int off = 16 * w + j < rows ? (16 * w + j) * ldv + 4 * g * ES : kOffPast;
+            if constexpr (ES == 2)
+                buf_store_u32x2(to, off, __builtin_bit_cast(u32x2, pack4(r)));
+            else
+                buf_store_u32x4(to, off, __builtin_bit_cast(u32x4, r));
         }
-    };
-
-    if (c_end > 0) {
-        constexpr std::integral_constant<int, 0> set0{};
-        constexpr std::integral_constant<int, 1> set1{};
-        load_common(c_end - 1, common);
-        load_own(c_end - 1, own[0]);
-        load_own(c_end - 2, own[1]);
-        stage_common(0, common);
-        load_common(c_end - 2, common);
-        for (int c = c_end - 1;; c -= 2) {
-            chunk(set0, c);
-            if (c < 1) break;
-            chunk(set1, c - 1);
-            if (c < 2) break;
+        load_inv(c - 1);
+        __syncthreads();
+        // ---- Y' = e^{G_C} Y + Q^T (e^G dO) - K^T (e^G beta Z)
+        if (holds) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) Y[t] *= f;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const Terms<3> gq = frag_terms<3>(s_gq[x]), gr = frag_terms<3>(s_gr[x]);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    Y[t] = mma(col_terms<NE>(&s_q[w][0][32 * x * LK], C * LK, LK, 4 * t, 8, j, g), gq, Y[t]);
+                    Y[t] = mma(col_terms<NE>(&s_k[w][0][32 * x * LK], C * LK, LK, 4 * t, 8, j, g), gr, Y[t]);
+                }
+            }
         }
     }
-    if (p.dS0) {
-        float* out = p.dS0 + (size_t)unit * state;
+    if (holds && p.dS0) {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) out[(size_t)(32 * kw + 8 * g + 4 * t + i) * p.dv + 16 * tile + j] = Y[t][i];
+            for (int i = 0; i < 4; ++i) p.dS0[at_state + (size_t)(4 * t + i) * p.dv] = Y[t][i];
     }
 }
 
@@ -282,7 +248,7 @@ struct DeltaQK {
     int B, T, H, Hk, dk_, dv_;
 };
 
-// One workgroup of four waves per superchunk of a head of q and k, over the heads
+// One workgroup of four waves per chunk of a head of q and k, over the heads
 // that share it.  Over 32 value columns at a time, in LDS: S^T and Y^T [32][DK], dO
 // and dv [64][32], U^T [32][64].  Wave m makes the products with S and Y of
 // channels 32 m .. (transposed: a token a lane), and wave w the pairs of its 16
@@ -291,7 +257,7 @@ struct DeltaQK {
 // part of the sum, beside the result's own rounding.
 template <typename E, int DK>
 __global__ __launch_bounds__(256) void delta_qk_kernel(DeltaQK p) {
-    constexpr int NE = sizeof(E) == 2 ? 1 : 3, ES = sizeof(E), PE = 16 / ES, L = kSuperChunks * kDeltaChunk;
+    constexpr int NE = sizeof(E) == 2 ? 1 : 3, ES = sizeof(E), PE = 16 / ES, L = kDeltaChunk;
     constexpr int LS = DK + 8, LT = 32 + 8, LU = L + 8;      // padded rows
     constexpr int QS = 32 * LS, QT = L * LT, QU = 32 * LU, QK = L * LS;      // elements of a plane
     constexpr int kFrags = 3 * 4 * 2 * NE * kFragBytes;      // bytes of the pairs' operands
@@ -303,12 +269,11 @@ __global__ __launch_bounds__(256) void delta_qk_kernel(DeltaQK p) {
     char* s_frag = s_mem;                                    // then, in the same place, the pairs and K or Q
     bf16* s_K = reinterpret_cast<bf16*>(s_mem + kFrags);
     const DeltaSweep& sw = p.sweep;
-    const int sc = blockIdx.x / p.Hk % sw.NS, hk = blockIdx.x % p.Hk, b = blockIdx.x / p.Hk / sw.NS;
-    const int n = seq_len(p.lens, b, p.T), t0 = sc * L, rows = min(L, n - t0);
+    const int c = blockIdx.x / p.Hk % sw.NC, hk = blockIdx.x % p.Hk, b = blockIdx.x / p.Hk / sw.NC;
+    const int n = seq_len(p.lens, b, p.T), t0 = c * L, rows = min(L, n - t0);
     if (rows <= 0) return;
     const int tid = threadIdx.x, wave = wave_id(), lane = lane_id(), j = lane & 15, g = lane >> 4, G = p.H / p.Hk;
     const bool mine = wave < DK / 32;                        // this wave has channels
-    const int chunks = (rows + kDeltaChunk - 1) / kDeltaChunk;
     f32x4 dq[2][4], dk[2][4];
 #pragma unroll
     for (int t = 0; t < 2; ++t)
@@ -333,10 +298,10 @@ __global__ __launch_bounds__(256) void delta_qk_kernel(DeltaQK p) {
             s_beta[lane] = lane < rows ? p.beta[at] : 0.f;
         }
         __syncthreads();
-        const E* gS = (const E*)sw.S + ((size_t)unit * sw.NS + sc) * p.dv_ * DK;
-        const E* gY = (const E*)sw.Y + ((size_t)unit * sw.NS + sc) * p.dv_ * DK;
+        const E* gS = (const E*)sw.S + ((size_t)unit * sw.NC + c) * p.dv_ * DK;
+        const E* gY = (const E*)sw.Y + ((size_t)unit * sw.NC + c) * p.dv_ * DK;
         const size_t tok = (((size_t)b * p.T + t0) * p.H + h) * p.dv_;
-        const float* gE = sw.e + ((size_t)unit * sw.NC + kSuperChunks * sc) * p.dv_ * kDeltaChunk;
+        const float* gE = sw.e + ((size_t)unit * sw.NC + c) * p.dv_ * L;
         f32x4 aq[2][4], as[2][4], ay[2][4], pr[4], xr[4], pd = zero4(), xd = zero4();
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -347,33 +312,30 @@ __global__ __launch_bounds__(256) void delta_qk_kernel(DeltaQK p) {
         for (int c0 = 0; c0 < p.dv_; c0 += 32) {
             if (c0) __syncthreads();
             for (int i = tid; i < 32 * DK / PE; i += 256) {
-                const int c = i / (DK / PE), ch = i % (DK / PE) * PE;
-                put_piece<E>(s_S + c * LS + ch, QS, *reinterpret_cast<const u32x4*>(gS + (size_t)(c0 + c) * DK + ch));
-                put_piece<E>(s_Y + c * LS + ch, QS, *reinterpret_cast<const u32x4*>(gY + (size_t)(c0 + c) * DK + ch));
+                const int vc = i / (DK / PE), ch = i % (DK / PE) * PE;
+                put_piece<E>(s_S + vc * LS + ch, QS, *reinterpret_cast<const u32x4*>(gS + (size_t)(c0 + vc) * DK + ch));
+                put_piece<E>(s_Y + vc * LS + ch, QS, *reinterpret_cast<const u32x4*>(gY + (size_t)(c0 + vc) * DK + ch));
             }
             for (int i = tid; i < L * 32 / PE; i += 256) {
-                const int t = i / (32 / PE), c = i % (32 / PE) * PE;
+                const int t = i / (32 / PE), vc = i % (32 / PE) * PE;
                 u32x4 x{}, y{};
                 if (t < rows) {
-                    const size_t at = tok + (size_t)t * p.H * p.dv_ + c0 + c;
+                    const size_t at = tok + (size_t)t * p.H * p.dv_ + c0 + vc;
                     x = *reinterpret_cast<const u32x4*>((const E*)sw.dO + at);
                     y = *reinterpret_cast<const u32x4*>((const E*)p.dv + at);
                 }
-                put_piece<E>(s_O + t * LT + c, QT, x);
-                put_piece<E>(s_R + t * LT + c, QT, y);
+                put_piece<E>(s_O + t * LT + vc, QT, x);
+                put_piece<E>(s_R + t * LT + vc, QT, y);
             }
             for (int i = tid; i < 32 * L / 4; i += 256) {
-                const int c = i / (L / 4), t = i % (L / 4) * 4, cc = t / kDeltaChunk;
-                f32x4 u = zero4();
-                if (cc < chunks) {
-                    u = *reinterpret_cast<const f32x4*>(gE + ((size_t)cc * p.dv_ + c0 + c) * kDeltaChunk + t % kDeltaChunk);
+                const int vc = i / (L / 4), t = i % (L / 4) * 4;
+                f32x4 u = *reinterpret_cast<const f32x4*>(gE + (size_t)(c0 + vc) * L + t);
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) u[x] *= s_beta[t + x];
-                }
+                for (int x = 0; x < 4; ++x) u[x] *= s_beta[t + x];
 #pragma unroll
                 for (int s = 0; s < NE; ++s) {
                     const bf16x4 hi = pack4(u);
-                    *reinterpret_cast<bf16x4*>(s_U + s * QU + c * LU + t) = hi;
+                    *reinterpret_cast<bf16x4*>(s_U + s * QU + vc * LU + t) = hi;
 #pragma unroll
                     for (int x = 0; x < 4; ++x) u[x] -= (float)hi[x];
                 }
@@ -475,7 +437,7 @@ __global__ __launch_bounds__(256) void delta_qk_kernel(DeltaQK p) {
             }
             __syncthreads();
             if (!mine) continue;
-            auto frag = [&](int kind, int r, int ks) { return frag_terms<NE>(s_frag + ((kind * 4 + r) * 2 + ks) * NE * kFragBytes, kFragBytes); };
+            auto frag = [&](int kind, int r, int ks) { return frag_terms<NE>(s_frag + ((kind * 4 + r) * 2 + ks) * NE * kFragBytes); };
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
@@ -555,12 +517,11 @@ __global__ __launch_bounds__(256) void delta_gates_kernel(DeltaSweep sw, const i
 // Byte offsets of the workspace's regions, each 256-byte aligned.
 struct DeltaBackLayout {
     size_t blocks, e, S, Y, end, anchor, dot, total;
-    int NC, NS, NA;
+    int NC, NA;
 };
 static DeltaBackLayout back_layout(int B, int T, int H, int dk, int dv, bool is_bf16) {
     DeltaBackLayout l;
     l.NC = (T + kDeltaChunk - 1) / kDeltaChunk;
-    l.NS = (l.NC + kSuperChunks - 1) / kSuperChunks;
     l.NA = (l.NC + kAnchorChunks - 1) / kAnchorChunks;
     const size_t units = (size_t)B * H, state = (size_t)dk * dv;
     size_t at = 0;
@@ -571,8 +532,8 @@ static DeltaBackLayout back_layout(int B, int T, int H, int dk, int dv, bool is_
     };
     l.blocks = take(units * l.NC * delta_block_bytes(is_bf16, true));
     l.e = take(units * l.NC * dv * kDeltaChunk * 4);
-    l.S = take(units * l.NS * state * (is_bf16 ? 2 : 4));
-    l.Y = take(units * l.NS * state * (is_bf16 ? 2 : 4));
+    l.S = take(units * l.NC * state * (is_bf16 ? 2 : 4));
+    l.Y = take(units * l.NC * state * (is_bf16 ? 2 : 4));
     l.end = take(units * l.NA * state * 4);
     l.anchor = take(units * l.NA * (dv / 16) * (dk / 32) * 4);
     l.dot = take(2 * (size_t)(dv / 16) * units * l.NC * kDeltaChunk * 4);
@@ -586,10 +547,10 @@ size_t delta_backward_ws_bytes(int B, int T, int H, int, int dk, int dv, bool is
 
 template <typename E, int DK>
 static hipError_t launch_k(const DeltaBackward& a, const DeltaReverse& r, const DeltaQK& x, hipStream_t stream) {
-    hipLaunchKernelGGL((delta_reverse_kernel<E, DK>), dim3((unsigned)(a.B * a.H * (a.dv_ / 16))), dim3(DK * 2), 0, stream, r);
+    hipLaunchKernelGGL((delta_reverse_kernel<E, DK>), dim3((unsigned)(a.B * a.H * (a.dv_ / 16))), dim3(256), 0, stream, r);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((delta_qk_kernel<E, DK>), dim3((unsigned)(a.B * a.Hk * r.sweep.NS)), dim3(256), 0, stream, x);
+    hipLaunchKernelGGL((delta_qk_kernel<E, DK>), dim3((unsigned)(a.B * a.Hk * r.sweep.NC)), dim3(256), 0, stream, x);
     return hipGetLastError();
 }
 
@@ -606,7 +567,7 @@ hipError_t launch_delta_backward(const DeltaBackward& a, void* ws, hipStream_t s
     const DeltaBackLayout l = back_layout(a.B, a.T, a.H, a.dk_, a.dv_, a.is_bf16);
     char* w = (char*)ws;
     const DeltaSweep sw{a.dO, (float*)(w + l.e), w + l.S, w + l.Y, (float*)(w + l.end), (float*)(w + l.anchor), (float*)(w + l.dot),
-                        l.NC, l.NS, l.NA};
+                        l.NC, l.NA};
     const StateIO S = dense_state(a.S0, nullptr);
     hipError_t e = launch_delta_pairs({a.q, a.k, a.g, a.beta, a.scale, S, a.lens, w + l.blocks, a.B, a.T, a.H, a.Hk, a.dk_, 0, l.NC,
                                        a.is_bf16}, true, stream);

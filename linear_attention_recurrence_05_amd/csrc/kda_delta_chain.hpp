@@ -7,24 +7,23 @@
 
 namespace kda {
 
-// Chunks whose end has an anchor <S, Y> of dg (kda_delta_backward.hip), and those
-// that share one state in the gradients of q and k.
-constexpr int kAnchorChunks = 8, kSuperChunks = 2;
+// Chunks from one anchor <S, Y> of dg (kda_delta_backward.hip) to the next.
+constexpr int kAnchorChunks = 4;
 
 // What the gradients' sweeps leave in the workspace, for unit u = b H + h, chunk
-// c of NC, superchunk s of NS, anchor a of NA, column tile t of `tiles`:
-//   e     [u][c][dv][32] fp32        e_t of every token
-//   S, Y  [u][s][dv][dk] of E        the state before a superchunk, and the
-//                                    gradient of the one after it, transposed
+// c of NC, anchor a of NA, column tile t of `tiles`:
+//   e     [u][c][dv][64] fp32        e_t of every token
+//   S, Y  [u][c][dv][dk] of E        the state before a chunk, and the gradient of
+//                                    the one behind it, transposed
 //   end   [u][a][t] state tiles      the state at an anchor, as the chain holds it
 //   anchor[u][a][t][DK / 32] fp32    parts of <S, Y>
-//   dot   [2][t][u][32 NC] fp32      parts of dO . o - dv . v, and of dbeta
+//   dot   [2][t][u][64 NC] fp32      parts of dO . o - dv . v, and of dbeta
 struct DeltaSweep {
     const void* dO;
     float* e;
     void *S, *Y;
     float *end, *anchor, *dot;
-    int NC, NS, NA;
+    int NC, NA;
 };
 
 // Chunks c0 .. c1 - 1 from the state S.in to S.out.

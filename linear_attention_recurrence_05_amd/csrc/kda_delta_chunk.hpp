@@ -1,12 +1,12 @@
 // kda_delta_chunk.hpp -- the chunk form of the gated delta rule, shared by the
-// prefill and the gradients.  With C = 32 tokens of a chunk, S the state before
+// prefill and the gradients.  With C = 64 tokens of a chunk, S the state before
 // them, G_i the sum of the chunk's log-decays up to token i, D_ij = exp(G_i - G_j)
 // for i >= j and N = (K K^T) * D below the diagonal:
 //   E  = (I + N diag(beta))^{-1} (V - e^G K S)        e_t of every token
 //   O  = scale (e^G Q S + ((Q K^T) * D) diag(beta) E)
 //   S' = e^{G_C} S + K^T diag(e^{G_C - G} beta) E
-// Every exponent is <= 0 for g <= 0; G is summed, and its differences taken, in
-// 64 bits, so that a decay behind a far smaller one keeps its digits.
+// Every exponent is <= 0 for g <= 0; G is summed in 64 bits and its differences are
+// taken of two fp32 parts, so that a decay behind a far smaller one keeps its digits.
 //
 // What does not depend on the state, the inverse and the pairs' weights, is made
 // first for all chunks at once (delta_pairs_kernel) and left in the workspace as
@@ -19,26 +19,30 @@
 
 namespace kda {
 
-constexpr int kDeltaChunk = 32;
+constexpr int kDeltaChunk = 64, kDeltaTiles = kDeltaChunk / 16;
 
 // A chunk's block in the workspace.  An operand of one 16x16x32 MFMA is 64 lanes
 // of 16 bytes; lane (j, g) holds row (or column) j, and along the contraction
-// tokens 4 g .. 4 g + 3 and 16 + 4 g .. 16 + 4 g + 3 of the chunk.
-//   inv  [3 terms][2]       rows 16 q + j of (I + N diag(beta))^{-1}
-//   pair [NP terms][2]      columns (queries) 16 q + j of scale ((Q K^T) * D diag(beta))^T
-//   row  [32] e^{G_i}, [32] e^{G_C - G_j} beta_j, then e^{G_C} as a factor and
-//        what its rounding left out, relative to it
+// tokens 4 g .. 4 g + 3 and 16 + 4 g .. 16 + 4 g + 3 of 32 tokens.  Of the lower
+// triangular matrices six operands of 16 rows x 32 are not zero (lower()), of
+// their transposes another six (upper()); each is N terms one after the other.
+//   inv   lower, 3 terms   rows of (I + N diag(beta))^{-1}
+//   pair  lower, NP terms  columns (queries) of scale ((Q K^T) * D diag(beta))^T
+//   row   [64] e^{G_i}, [64] e^{G_C - G_j} beta_j, [64] e^{G_C - G_j}, [64] beta_j,
+//         then e^{G_C} as a factor and what its rounding left out, relative to it
 // and, for the gradients (BACK),
-//   invt [3][2]             rows of ((I + diag(beta) N)^{-1})^T
-//   pairt [3][2]            rows (keys) 16 q + j of scale ((Q K^T) * D)^T
-//   more [32] e^{G_C - G_j}, [32] beta_j
+//   invt  upper, 3 terms   rows of ((I + diag(beta) N)^{-1})^T
+//   pairt upper, 3 terms   rows (keys) of scale ((Q K^T) * D)^T
 constexpr int kFragBytes = 1024;
+__host__ __device__ constexpr int lower(int tile, int half) { return tile < 2 ? tile : 2 * tile - 2 + half; }
+__host__ __device__ constexpr int upper(int tile, int half) { return tile < 2 ? 2 * tile + half : 2 + tile; }
 template <int NP, bool BACK>
 struct DeltaBlock {
-    static constexpr int inv = 0, pair = inv + 6 * kFragBytes, row = pair + 2 * NP * kFragBytes;
-    static constexpr int more = row + 66 * 4 + 8, invt = row + 1024, pairt = invt + 6 * kFragBytes;
-    static constexpr int bytes = BACK ? pairt + 6 * kFragBytes : row + 512;
+    static constexpr int inv = 0, pair = inv + 18 * kFragBytes, row = pair + 6 * NP * kFragBytes;
+    static constexpr int invt = row + 1088, pairt = invt + 18 * kFragBytes;
+    static constexpr int bytes = BACK ? pairt + 18 * kFragBytes : invt;
 };
+enum DeltaRow { kRowGrow = 0, kRowWrite = 64, kRowEnd = 128, kRowBeta = 192, kRowDecay = 256 };   // floats from `row`
 
 // Chunks c0 .. c1 - 1 of every sequence, block ((b H + h) (c1 - c0) + c - c0).
 struct DeltaPairs {
@@ -63,7 +67,7 @@ struct ChunkDecay {
     float left = 0.f;
     __device__ float operator()(float f, float rest) {
         const float d = f * (rest + left), got = f + d;
-        left = got > 1e-30f ? (d - (got - f)) / got : 0.f;
+        left = got > 1e-30f ? (d - (got - f)) * fast_rcp(got) : 0.f;
         return got;
     }
 };
@@ -93,9 +97,9 @@ __device__ __forceinline__ Terms<3> raw_terms(const Raw<float>& r) {
 // A 16-byte piece of a row to LDS: bf16 as it is, four fp32 values as their three
 // terms, `plane` elements apart.
 template <typename E>
-__device__ __forceinline__ void put_piece(bf16* dst, int plane, u32x4 v) {
+__device__ __forceinline__ void put_piece(bf16* dst, int plane, u32x4 v, bool on = true) {
     if constexpr (sizeof(E) == 2) {
-        *reinterpret_cast<u32x4*>(dst) = v;
+        if (on) *reinterpret_cast<u32x4*>(dst) = v;
     } else {
         f32x4 x = __builtin_bit_cast(f32x4, v);
 #pragma unroll
@@ -108,22 +112,34 @@ __device__ __forceinline__ void put_piece(bf16* dst, int plane, u32x4 v) {
     }
 }
 
-// Four elements from memory, and eight to it.
-__device__ __forceinline__ void load4(const bf16* p, f32x4& x) {
-    const bf16x4 v = *reinterpret_cast<const bf16x4*>(p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = (float)v[i];
+// Four elements from a buffer, and eight to it.
+template <typename E>
+__device__ __forceinline__ f32x4 buf_load4(Rsrc r, int off) {
+    if constexpr (sizeof(E) == 4) {
+        return __builtin_bit_cast(f32x4, buf_load<u32x4>(r, off));
+    } else {
+        const bf16x4 v = __builtin_bit_cast(bf16x4, buf_load<u32x2>(r, off));
+        return f32x4{(float)v[0], (float)v[1], (float)v[2], (float)v[3]};
+    }
 }
-__device__ __forceinline__ void load4(const float* p, f32x4& x) { x = *reinterpret_cast<const f32x4*>(p); }
+template <typename E>
+__device__ __forceinline__ void buf_store8(Rsrc r, int off, f32x4 lo, f32x4 hi) {
+    if constexpr (sizeof(E) == 2) {
+        buf_store_u32x4(r, off, __builtin_bit_cast(u32x4, pack8(lo, hi)));
+    } else {
+        buf_store_u32x4(r, off, __builtin_bit_cast(u32x4, lo));
+        buf_store_u32x4(r, off + 16, __builtin_bit_cast(u32x4, hi));
+    }
+}
 __device__ __forceinline__ void store8(bf16* p, f32x4 lo, f32x4 hi) { *reinterpret_cast<bf16x8*>(p) = pack8(lo, hi); }
 __device__ __forceinline__ void store8(float* p, f32x4 lo, f32x4 hi) {
     reinterpret_cast<f32x4*>(p)[0] = lo;
     reinterpret_cast<f32x4*>(p)[1] = hi;
 }
 
-// An offset past any buffer's end, also 16 bytes further: such loads give zeros
-// and such stores are dropped.
-constexpr int kOffPast = -48;
+// An offset past any buffer's end, also some KB further: such loads give zeros and
+// such stores are dropped.
+constexpr int kOffPast = -(1 << 16);
 
 template <int N, int M>
 __device__ __forceinline__ Terms<N> first_terms(const Terms<M>& a) {
@@ -132,13 +148,49 @@ __device__ __forceinline__ Terms<N> first_terms(const Terms<M>& a) {
     for (int i = 0; i < N; ++i) out.t[i] = a.t[i];
     return out;
 }
-// Operands kept in LDS or in the workspace as N fragments `step` bytes apart.
+// An operand kept in LDS as N fragments `step` bytes apart.
 template <int N>
-__device__ __forceinline__ Terms<N> frag_terms(const char* p, int step) {
+__device__ __forceinline__ Terms<N> frag_terms(const char* p, int step = kFragBytes) {
     Terms<N> out;
 #pragma unroll
     for (int i = 0; i < N; ++i) out.t[i] = *reinterpret_cast<const bf16x8*>(p + i * step + lane_id() * 16);
     return out;
+}
+// N fragments of a block in the workspace (off kOffPast: zeros).
+template <int N>
+__device__ __forceinline__ Terms<N> load_terms(Rsrc r, int off) {
+    Terms<N> out;
+#pragma unroll
+    for (int i = 0; i < N; ++i) out.t[i] = __builtin_bit_cast(bf16x8, buf_load<u32x4>(r, off + i * kFragBytes + lane_id() * 16));
+    return out;
+}
+// A tile of 16 x 16 (rows 4 g + i of column j, an accumulator's layout) as N terms
+// to its half of an operand in LDS: half 0 is tokens 4 g .., half 1 16 + 4 g ..
+template <int N>
+__device__ __forceinline__ void put_half(char* frag, int half, f32x4 x) {
+#pragma unroll
+    for (int s = 0; s < N; ++s) {
+        const bf16x4 h = pack4(x);
+        *reinterpret_cast<bf16x4*>(frag + s * kFragBytes + lane_id() * 16 + half * 8) = h;
+        if (s + 1 < N) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] -= (float)h[i];
+        }
+    }
+}
+// Column j of rows 4 g .. 4 g + 3 of a [16][ld] tile kept as N bf16 planes in LDS.
+template <int N>
+__device__ __forceinline__ f32x4 col4(const bf16* s, int plane, int ld, int j, int g) {
+    typedef __attribute__((address_space(3))) i16x4 lds4;
+    f32x4 x = zero4();
+#pragma unroll
+    for (int n = N - 1; n >= 0; --n) {
+        const bf16* p = s + n * plane + (4 * g + (j >> 2)) * ld + 4 * (j & 3);
+        const bf16x4 v = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)p));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] += (float)v[i];
+    }
+    return x;
 }
 
 }  // namespace kda

@@ -2,255 +2,278 @@
 // depend on the state (kda_delta_chunk.hpp): the inverse of the triangular system
 // and the weights of pairs of tokens, as matrix operands in the workspace.
 //
-// One wave per chunk and head.  K K^T and Q K^T by MFMA with the decays applied
-// in the accumulators.  The inverse: the two 16 x 16 blocks on the diagonal by
-// substitution, a column a lane (stable for any beta in [0, 2] and keys of length
-// 1, where a series in powers of N is not: repeated keys make its terms grow to
-// thousands before they cancel), and the block below as -T22 A21 T11 in fp32 MFMA.
+// One workgroup of four waves per chunk and head; wave w has the 16 tokens of tile
+// w.  K K^T and Q K^T by MFMA with the decays applied in the accumulators.  The
+// inverse: the four 16 x 16 blocks on the diagonal by substitution, a column a lane
+// (stable for any beta in [0, 2] and keys of length 1, where a series in powers of
+// N is not: repeated keys make its terms grow to thousands before they cancel),
+// then the blocks below as T_ll = -T_l A T_u in fp32 MFMA, first within 32 tokens,
+// then across.
 #include <algorithm>
 
 #include "kda_delta_chunk.hpp"
 
 namespace kda {
 
-constexpr int kPairWaves = 4;
-constexpr int kPairLd = 36;   // floats of a row of the 32 x 32 matrices in LDS
+constexpr int kPairLd = 68;                     // floats of a row of the 64 x 64 matrices in LDS
+constexpr long long kPairGroups = 1LL << 20;    // most workgroups of a launch: more chunks loop
 
-// Waves of a launch: more chunks loop.
-constexpr long long kPairUnits = 1LL << 22;
-
-// x of lane `from`, a double as two words
-__device__ __forceinline__ double shfl_up_d(double x, int by) {
-    const uint64_t u = __builtin_bit_cast(uint64_t, x);
-    const uint32_t lo = __shfl_up((uint32_t)u, by), hi = __shfl_up((uint32_t)(u >> 32), by);
-    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+// sum of x over the lanes up to this one
+__device__ __forceinline__ double wave_scan(double x) {
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+        const double up = __shfl_up(x, o);
+        if (lane_id() >= o) x += up;
+    }
+    return x;
 }
 
 template <typename E, int DK, int NP, bool BACK>
-__global__ __launch_bounds__(kPairWaves * 64) void delta_pairs_kernel(DeltaPairs p) {
+__global__ __launch_bounds__(256, 2) void delta_pairs_kernel(DeltaPairs p) {
     using Blk = DeltaBlock<NP, BACK>;
-    constexpr int C = kDeltaChunk, KM = DK / 32, NE = sizeof(E) == 2 ? 1 : 3, LD = kPairLd;
-    __shared__ __align__(16) float s_a[kPairWaves][C * LD];                    // A, later its inverse
-    __shared__ __align__(16) float s_b[kPairWaves][BACK ? C * LD : 4];        // the other system's
-    __shared__ double s_G[kPairWaves][C];
-    __shared__ float s_beta[kPairWaves][C];
-    const int wave = wave_id(), lane = lane_id(), j = lane & 15, g = lane >> 4, W = p.c1 - p.c0;
+    constexpr int C = kDeltaChunk, KM = DK / 32, NE = sizeof(E) == 2 ? 1 : 3, ES = sizeof(E), LD = kPairLd;
+    __shared__ __align__(16) float s_m[BACK ? 2 : 1][C * LD];   // N diag(beta), diag(beta) N; then their inverses
+    __shared__ __align__(16) float s_hi[C], s_lo[C], s_beta[C];
+    const int w = wave_id(), W = p.c1 - p.c0;
     const long long all = (long long)p.B * W * p.H;
-    for (long long at = (long long)blockIdx.x * kPairWaves + wave; at < all; at += (long long)gridDim.x * kPairWaves) {
+    for (long long at = blockIdx.x; at < all; at += gridDim.x) {
+        const int lane = fresh_lane_id(), j = lane & 15, g = lane >> 4;
         const int h = (int)(at % p.H), c = p.c0 + (int)(at / p.H % W), b = (int)(at / p.H / W);
         const int n = seq_len(p.lens, b, p.T), t0 = c * C, rows = min(C, n - t0);
-        if (rows <= 0 || p.S.skip(b)) continue;                                // uniform over the wave
+        if (rows <= 0 || p.S.skip(b)) continue;                // uniform over the workgroup
         char* blk = p.blocks + (((size_t)b * p.H + h) * W + (c - p.c0)) * Blk::bytes;
-        // ---- decays and strengths
-        const size_t gate = ((size_t)b * p.T + t0) * p.H + h;
-        const int t = lane & 31;
-        double G = 0;
-        float beta = 0.f;
-        if (t < rows) {
-            G = (double)log_decay(p.g[gate + (size_t)t * p.H]);
-            beta = p.beta[gate + (size_t)t * p.H];
-        }
-#pragma unroll
-        for (int o = 1; o < C; o <<= 1) {
-            const double up = shfl_up_d(G, o);
-            if (t >= o) G += up;
-        }
-        float* A = s_a[wave];
-        if (lane < C) {
-            s_G[wave][t] = G;
-            s_beta[wave][t] = beta;
-        }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        const double GC = s_G[wave][C - 1];
-        if (lane < C) {
-            float* row = reinterpret_cast<float*>(blk + Blk::row);
-            const float end = expf((float)(GC - G));
-            row[t] = expf((float)G);
-            row[C + t] = end * beta;
-            if (t == 0) {
-                const double f = exp(GC);
-                const float ff = (float)f;
-                row[2 * C] = ff;
-                row[2 * C + 1] = f > 1e-30 ? (float)((f - (double)ff) / f) : 0.f;
-            }
-            if constexpr (BACK) {
-                float* more = reinterpret_cast<float*>(blk + Blk::more);
-                more[t] = end;
-                more[C + t] = beta;
-            }
-        }
-        // ---- K K^T and (K Q^T): rows are keys, columns the later token
-        const int hk = h / (p.H / p.Hk), ld = p.Hk * DK * (int)sizeof(E);
+        // ---- rows: K and Q of tile w
+        const int hk = h / (p.H / p.Hk), ld = p.Hk * DK * ES;
         const size_t base = (((size_t)b * p.T + t0) * p.Hk + hk) * DK;
-        const uint32_t bytes = (uint32_t)((rows - 1) * ld + DK * (int)sizeof(E));
+        const uint32_t bytes = (uint32_t)((rows - 1) * ld + DK * ES);
         const Rsrc rk = make_rsrc((const E*)p.k + base, bytes), rq = make_rsrc((const E*)p.q + base, bytes);
-        f32x4 kk[3], kq[3], qk[3];                                            // tiles (0,0), (0,1), (1,1): key, later
-#pragma unroll
-        for (int i = 0; i < 3; ++i) kk[i] = kq[i] = qk[i] = zero4();
+        auto row = [&](Rsrc r, int a, int m) {
+            return raw_load<E>(r, 16 * a + j < rows ? (16 * a + j) * ld + (32 * m + 8 * g) * ES : kOffPast);
+        };
+        Raw<E> xw[KM], yw[KM];
 #pragma unroll
         for (int m = 0; m < KM; ++m) {
-            Terms<NE> x[2], y[2];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int off = 16 * q + j < rows ? (16 * q + j) * ld + (32 * m + 8 * g) * (int)sizeof(E) : kOffPast;
-                x[q] = raw_terms(raw_load<E>(rk, off));
-                y[q] = raw_terms(raw_load<E>(rq, off));
-            }
-            kk[0] = mma(x[0], x[0], kk[0]);
-            kk[1] = mma(x[0], x[1], kk[1]);
-            kk[2] = mma(x[1], x[1], kk[2]);
-            kq[0] = mma(x[0], y[0], kq[0]);
-            kq[1] = mma(x[0], y[1], kq[1]);
-            kq[2] = mma(x[1], y[1], kq[2]);
-            if constexpr (BACK) {
-                qk[0] = mma(y[0], x[0], qk[0]);                                // rows: queries, columns: keys
-                qk[1] = mma(y[1], x[0], qk[1]);
-                qk[2] = mma(y[1], x[1], qk[2]);
-            }
+            xw[m] = row(rk, w, m);
+            yw[m] = row(rq, w, m);
         }
-        // ---- decays: key 16 a + 4 g + i, later token 16 b + j
-        f32x4 bk[2];
-        double Gk[2][4], Gl[2];
-#pragma unroll
-        for (int a = 0; a < 2; ++a) {
-            Gl[a] = s_G[wave][16 * a + j];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                Gk[a][i] = s_G[wave][16 * a + 4 * g + i];
-                bk[a][i] = s_beta[wave][16 * a + 4 * g + i];
-            }
+        // ---- decays and strengths
+        double G = 0;
+        float beta = 0.f;
+        if (lane < rows) {
+            const size_t gate = ((size_t)b * p.T + t0 + lane) * p.H + h;
+            G = (double)log_decay(p.g[gate]);
+            beta = p.beta[gate];
         }
-        f32x4 P[3], Dt[3];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int d = j - 4 * g - i;                                       // later - key within a diagonal tile
-            const float d00 = expf((float)fmin(Gl[0] - Gk[0][i], 0.0)), d01 = expf((float)fmin(Gl[1] - Gk[0][i], 0.0)),
-                        d11 = expf((float)fmin(Gl[1] - Gk[1][i], 0.0));
-            P[0][i] = d >= 0 ? p.scale * d00 * bk[0][i] * kq[0][i] : 0.f;
-            P[1][i] = p.scale * d01 * bk[0][i] * kq[1][i];
-            P[2][i] = d >= 0 ? p.scale * d11 * bk[1][i] * kq[2][i] : 0.f;
-            Dt[0][i] = d > 0 ? d00 * kk[0][i] : 0.f;                           // N[later][key]
-            Dt[1][i] = d01 * kk[1][i];
-            Dt[2][i] = d > 0 ? d11 * kk[2][i] : 0.f;
-        }
-        const Terms<NP> w0 = to_terms<NP>(P[0], zero4()), w1 = to_terms<NP>(P[1], P[2]);
-#pragma unroll
-        for (int s = 0; s < NP; ++s) {
-            bf16x8* dst = reinterpret_cast<bf16x8*>(blk + Blk::pair + 2 * s * kFragBytes) + lane;
-            dst[0] = w0.t[s];
-            dst[kFragBytes / 16] = w1.t[s];
-        }
-        if constexpr (BACK) {                                                  // row: key j, contraction: queries
-            f32x4 X[3];
-            // query 16 a + 4 g + i, key 16 b + j: later is the row here
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int d = 4 * g + i - j;
-                X[0][i] = d >= 0 ? p.scale * expf((float)fmin(Gk[0][i] - Gl[0], 0.0)) * qk[0][i] : 0.f;
-                X[1][i] = p.scale * expf((float)fmin(Gk[1][i] - Gl[0], 0.0)) * qk[1][i];
-                X[2][i] = d >= 0 ? p.scale * expf((float)fmin(Gk[1][i] - Gl[1], 0.0)) * qk[2][i] : 0.f;
-            }
-            const Terms<3> t0f = to_terms<3>(X[0], X[1]), t1f = to_terms<3>(zero4(), X[2]);
-#pragma unroll
-            for (int s = 0; s < 3; ++s) {
-                bf16x8* dst = reinterpret_cast<bf16x8*>(blk + Blk::pairt + 2 * s * kFragBytes) + lane;
-                dst[0] = t0f.t[s];
-                dst[kFragBytes / 16] = t1f.t[s];
+        G = wave_scan(G);                                      // in every wave
+        const double GC = __shfl(G, C - 1);
+        __syncthreads();                                       // the last chunk is done with LDS
+        if (w == 0) {
+            s_hi[lane] = (float)G;
+            s_lo[lane] = (float)(G - (double)(float)G);
+            s_beta[lane] = beta;
+        } else if (w == 1) {
+            float* out = reinterpret_cast<float*>(blk + Blk::row);
+            const float end = expf((float)(GC - G));
+            out[kRowGrow + lane] = expf((float)G);
+            out[kRowWrite + lane] = end * beta;
+            out[kRowEnd + lane] = end;
+            out[kRowBeta + lane] = beta;
+            if (lane == 0) {
+                const double f = exp(GC);
+                const float ff = (float)f;
+                out[kRowDecay] = ff;
+                out[kRowDecay + 1] = f > 1e-30 ? (float)((f - (double)ff) / f) : 0.f;
             }
         }
-        // ---- A = N diag(beta) (and diag(beta) N) in LDS, row: the later token
-        auto put = [&](float* M, int row, int col, f32x4 v) { *reinterpret_cast<f32x4*>(M + row * LD + col) = v; };
-        put(A, j, 4 * g, Dt[0] * bk[0]);
-        put(A, 16 + j, 4 * g, Dt[1] * bk[0]);
-        put(A, 16 + j, 16 + 4 * g, Dt[2] * bk[1]);
-        if constexpr (BACK) {
-            float* Bm = s_b[wave];
-            const float b0 = s_beta[wave][j], b1 = s_beta[wave][16 + j];
-            put(Bm, j, 4 * g, Dt[0] * b0);
-            put(Bm, 16 + j, 4 * g, Dt[1] * b1);
-            put(Bm, 16 + j, 16 + 4 * g, Dt[2] * b1);
+        __syncthreads();
+        // ---- tiles (key a, later token w): K K^T and K Q^T; (BACK) (query a, key w)
+        f32x4 kk[kDeltaTiles], kq[kDeltaTiles], qk[kDeltaTiles];
+#pragma unroll
+        for (int a = 0; a < kDeltaTiles; ++a) {
+            kk[a] = kq[a] = qk[a] = zero4();
+            if (a < w) {
+                Raw<E> x[KM];
+#pragma unroll
+                for (int m = 0; m < KM; ++m) x[m] = row(rk, a, m);
+#pragma unroll
+                for (int m = 0; m < KM; ++m) {
+                    const Terms<NE> xa = raw_terms(x[m]);
+                    kk[a] = mma(xa, raw_terms(xw[m]), kk[a]);
+                    kq[a] = mma(xa, raw_terms(yw[m]), kq[a]);
+                }
+            } else if (a == w) {
+#pragma unroll
+                for (int m = 0; m < KM; ++m) {
+                    const Terms<NE> xa = raw_terms(xw[m]), ya = raw_terms(yw[m]);
+                    kk[a] = mma(xa, xa, kk[a]);
+                    kq[a] = mma(xa, ya, kq[a]);
+                    if constexpr (BACK) qk[a] = mma(ya, xa, qk[a]);
+                }
+            } else if (BACK) {
+                Raw<E> y[KM];
+#pragma unroll
+                for (int m = 0; m < KM; ++m) y[m] = row(rq, a, m);
+#pragma unroll
+                for (int m = 0; m < KM; ++m) qk[a] = mma(raw_terms(y[m]), raw_terms(xw[m]), qk[a]);
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        // ---- with their decays: to LDS (row: the later token), and the pairs' operands
+        const float hi = s_hi[16 * w + j], lo = s_lo[16 * w + j], bl = s_beta[16 * w + j];
+        f32x4 P[kDeltaTiles], X[kDeltaTiles];
+#pragma unroll
+        for (int a = 0; a < kDeltaTiles; ++a) {
+            P[a] = X[a] = zero4();
+            const f32x4 ghi = *reinterpret_cast<const f32x4*>(&s_hi[16 * a + 4 * g]),
+                        glo = *reinterpret_cast<const f32x4*>(&s_lo[16 * a + 4 * g]);
+            if (a <= w) {
+                const f32x4 bk = *reinterpret_cast<const f32x4*>(&s_beta[16 * a + 4 * g]);
+                f32x4 N0, N1;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int d = 16 * (w - a) + j - 4 * g - i;   // later - key
+                    const float D = d >= 0 ? __expf((hi - ghi[i]) + (lo - glo[i])) : 0.f;
+                    P[a][i] = p.scale * D * bk[i] * kq[a][i];
+                    const float N = d > 0 ? D * kk[a][i] : 0.f;
+                    N0[i] = N * bk[i];
+                    N1[i] = N * bl;
+                }
+                *reinterpret_cast<f32x4*>(&s_m[0][(16 * w + j) * LD + 16 * a + 4 * g]) = N0;
+                if constexpr (BACK) *reinterpret_cast<f32x4*>(&s_m[BACK][(16 * w + j) * LD + 16 * a + 4 * g]) = N1;
+            }
+            if (BACK && a >= w) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int d = 16 * (a - w) + 4 * g + i - j;   // query - key
+                    X[a][i] = d >= 0 ? p.scale * __expf((ghi[i] - hi) + (glo[i] - lo)) * qk[a][i] : 0.f;
+                }
+            }
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            if (half <= w / 2) {
+                const Terms<NP> f = to_terms<NP>(P[2 * half], P[2 * half + 1]);
+#pragma unroll
+                for (int s = 0; s < NP; ++s)
+                    reinterpret_cast<bf16x8*>(blk + Blk::pair + (lower(w, half) * NP + s) * kFragBytes)[lane] = f.t[s];
+            }
+            if (BACK && half >= w / 2) {
+                const Terms<3> f = to_terms<3>(X[2 * half], X[2 * half + 1]);
+#pragma unroll
+                for (int s = 0; s < 3; ++s)
+                    reinterpret_cast<bf16x8*>(blk + Blk::pairt + (upper(w, half) * 3 + s) * kFragBytes)[lane] = f.t[s];
+            }
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
-        // ---- the diagonal blocks' inverses: lanes 0..15 block 0, 16..31 block 1
-        // of A, 32..63 the same of the other system
+        __builtin_amdgcn_sched_barrier(0);
+        // ---- the inverse of this wave's block on the diagonal: a column a lane
+        // (lanes 16 .. 31 of the other system)
         {
-            const float* M = BACK && lane >= 32 ? s_b[wave] : A;
-            const int o = 16 * (g & 1);
+            float* M = &s_m[BACK ? g & 1 : 0][(16 * w) * LD + 16 * w];
             float x[16];
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 float acc = r == j ? 1.f : 0.f;
                 f32x4 a[4];
+                if (r % 4 == 0) __builtin_amdgcn_sched_barrier(0);   // else all rows are read first: 144 registers
 #pragma unroll
-                for (int q = 0; q < (r + 3) / 4; ++q) a[q] = *reinterpret_cast<const f32x4*>(M + (o + r) * LD + o + 4 * q);
+                for (int q = 0; q < (r + 3) / 4; ++q) a[q] = *reinterpret_cast<const f32x4*>(M + r * LD + 4 * q);
 #pragma unroll
                 for (int q = 0; q < r; ++q) acc -= a[q / 4][q % 4] * x[q];
                 x[r] = acc;
             }
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             __builtin_amdgcn_wave_barrier();
-            if (BACK || lane < 32) {
-                float* W_ = const_cast<float*>(M);
+            if (lane < (BACK ? 32 : 16)) {
 #pragma unroll
-                for (int r = 0; r < 16; ++r) W_[(o + r) * LD + o + j] = x[r];
+                for (int r = 0; r < 16; ++r) M[r * LD + j] = x[r];
             }
         }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        // ---- the block below, and out: rows of the inverse, or (t) its columns
-        auto finish = [&](float* M, int at_byte, bool transposed) {
-            f32x4 X = zero4(), Y = zero4();                                    // A21 T11, then T22 of it
+        __syncthreads();
+        // ---- the blocks below: first (1, 0) and (3, 2), then the four of the lower
+        // left quarter, a column of two to a wave.  An accumulator is the next
+        // product's operand as it is (rows 4 g + s for both).
+        auto tile = [&](const float* M, int r, int c, int s) { return M[(16 * r + j) * LD + 16 * c + 4 * g + s]; };
+        auto column = [&](const float* M, int r, int c, int s) { return M[(16 * r + 4 * g + s) * LD + 16 * c + j]; };
+        auto times = [&](const float* M, int r, int c, int c2, f32x4 acc) {   // block (r, c) times block (c, c2)
 #pragma unroll
-            for (int s = 0; s < 4; ++s) X = mma_f32_k4(M[(16 + j) * LD + 4 * g + s], M[(4 * g + s) * LD + j], X);
+            for (int s = 0; s < 4; ++s) acc = mma_f32_k4(tile(M, r, c, s), column(M, c, c2, s), acc);
+            __builtin_amdgcn_sched_barrier(0);
+            return acc;
+        };
+        auto applied = [&](const float* M, int r, int c, f32x4 X, f32x4 acc) {   // block (r, c) times X
 #pragma unroll
-            for (int s = 0; s < 4; ++s) Y = mma_f32_k4(M[(16 + j) * LD + 16 + 4 * g + s], X[s], Y);
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
+            for (int s = 0; s < 4; ++s) acc = mma_f32_k4(tile(M, r, c, s), X[s], acc);
+            __builtin_amdgcn_sched_barrier(0);
+            return acc;
+        };
+        auto put = [&](float* M, int r, int c, f32x4 X) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) M[(16 + 4 * g + i) * LD + j] = -Y[i];
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            f32x4 lo[2], hi[2];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (!transposed) {
-                    lo[0][i] = M[j * LD + 4 * g + i];
-                    hi[0][i] = 0.f;
-                    lo[1][i] = M[(16 + j) * LD + 4 * g + i];
-                    hi[1][i] = M[(16 + j) * LD + 16 + 4 * g + i];
-                } else {
-                    lo[0][i] = M[(4 * g + i) * LD + j];
-                    hi[0][i] = M[(16 + 4 * g + i) * LD + j];
-                    lo[1][i] = 0.f;
-                    hi[1][i] = M[(16 + 4 * g + i) * LD + 16 + j];
-                }
+            for (int i = 0; i < 4; ++i) M[(16 * r + 4 * g + i) * LD + 16 * c + j] = -X[i];
+        };
+        float* M = s_m[BACK ? w / 2 : 0];
+        const bool busy = BACK || w < 2;
+        const int e = w & 1;
+        f32x4 X1 = zero4();
+        if (busy) X1 = applied(M, 2 * e + 1, 2 * e + 1, times(M, 2 * e + 1, 2 * e, 2 * e, zero4()), zero4());
+        if (busy) put(M, 2 * e + 1, 2 * e, X1);                // read by this wave alone so far
+        __syncthreads();
+        f32x4 X2 = zero4(), X3 = zero4();
+        if (busy) {
+            f32x4 a2, a3;
+            if (e == 0) {
+                a2 = times(M, 2, 1, 0, times(M, 2, 0, 0, zero4()));
+                a3 = times(M, 3, 1, 0, times(M, 3, 0, 0, zero4()));
+            } else {
+                a2 = times(M, 2, 1, 1, zero4());
+                a3 = times(M, 3, 1, 1, zero4());
             }
+            X2 = applied(M, 2, 2, a2, zero4());
+            X3 = applied(M, 3, 2, a2, applied(M, 3, 3, a3, zero4()));
+        }
+        __syncthreads();
+        if (busy) {
+            put(M, 2, e, X2);
+            put(M, 3, e, X3);
+        }
+        __syncthreads();
+        // ---- out: rows of the inverse, columns of the other one
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const Terms<3> f = to_terms<3>(lo[q], hi[q]);
+        for (int half = 0; half < 2; ++half) {
+            if (half <= w / 2) {
+                const float* row = &s_m[0][(16 * w + j) * LD + 32 * half + 4 * g];
+                const f32x4 a = *reinterpret_cast<const f32x4*>(row);
+                const f32x4 z = *reinterpret_cast<const f32x4*>(row + 16);
+                const Terms<3> f = to_terms<3>(a, 2 * half + 1 <= w ? z : zero4());
 #pragma unroll
                 for (int s = 0; s < 3; ++s)
-                    reinterpret_cast<bf16x8*>(blk + at_byte + (2 * s + q) * kFragBytes)[lane] = f.t[s];
+                    reinterpret_cast<bf16x8*>(blk + Blk::inv + (lower(w, half) * 3 + s) * kFragBytes)[lane] = f.t[s];
             }
-        };
-        finish(A, Blk::inv, false);
-        if constexpr (BACK) finish(s_b[wave], Blk::invt, true);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
+            if (BACK && half >= w / 2) {
+                f32x4 a = zero4(), z;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (2 * half >= w) a[i] = s_m[BACK][(32 * half + 4 * g + i) * LD + 16 * w + j];
+                    z[i] = s_m[BACK][(32 * half + 16 + 4 * g + i) * LD + 16 * w + j];
+                }
+                const Terms<3> f = to_terms<3>(a, z);
+#pragma unroll
+                for (int s = 0; s < 3; ++s)
+                    reinterpret_cast<bf16x8*>(blk + Blk::invt + (upper(w, half) * 3 + s) * kFragBytes)[lane] = f.t[s];
+            }
+        }
     }
 }
 
 size_t delta_block_bytes(bool is_bf16, bool back) {
-    return is_bf16 ? (back ? DeltaBlock<3, true>::bytes : DeltaBlock<1, false>::bytes)
-                   : (back ? DeltaBlock<3, true>::bytes : DeltaBlock<3, false>::bytes);
+    return back ? DeltaBlock<3, true>::bytes : is_bf16 ? DeltaBlock<1, false>::bytes : DeltaBlock<3, false>::bytes;
 }
 
 template <typename E, int NP, bool BACK>
 static hipError_t launch_e(const DeltaPairs& a, hipStream_t stream) {
     const long long all = (long long)a.B * (a.c1 - a.c0) * a.H;
-    const dim3 grid((unsigned)((std::min(all, kPairUnits) + kPairWaves - 1) / kPairWaves)), block(kPairWaves * 64);
+    const dim3 grid((unsigned)std::min(all, kPairGroups)), block(256);
     switch (a.dk) {
         case 32: hipLaunchKernelGGL((delta_pairs_kernel<E, 32, NP, BACK>), grid, block, 0, stream, a); break;
         case 64: hipLaunchKernelGGL((delta_pairs_kernel<E, 64, NP, BACK>), grid, block, 0, stream, a); break;

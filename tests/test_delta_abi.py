@@ -77,6 +77,7 @@ def test_delta_calls_refuse(name):
         (dict(H_k=8), "KDA_ERR_INVALID_SHAPE"), (dict(T=0), "KDA_ERR_INVALID_SHAPE"),
         (dict(T=(1 << 30) + 1), "KDA_ERR_INVALID_SHAPE"),
         (dict(B=(1 << 17) + 1), "KDA_ERR_INVALID_SHAPE"), (dict(H=1 << 18, H_k=1 << 18), "KDA_ERR_INVALID_SHAPE"),
+        (dict(B=1, H=1 << 16, H_k=1 << 16), "KDA_ERR_INVALID_SHAPE"),
         (dict(d_k=48), "KDA_ERR_UNSUPPORTED"), (dict(d_v=256), "KDA_ERR_UNSUPPORTED"), (dict(d_k=0), "KDA_ERR_UNSUPPORTED"),
         (dict(dt=2), "KDA_ERR_UNSUPPORTED"), (dict(scale=INF), "KDA_ERR_INVALID_VALUE"),
         (dict(scale=NAN), "KDA_ERR_INVALID_VALUE"), (dict(n_slots=0), "KDA_ERR_INVALID_SHAPE"),
