@@ -114,12 +114,16 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_chain_kerne
     };
 
     ChunkDecay decay;
-    if (p.c0 < c_end) {
-        load_k(p.c0);
-        load_qv(p.c0);
-        load_inv(p.c0);
-        load_pair(p.c0);
-    }
+    // The first chunk's loads in the order of the loop's, or a wait there would be
+    // for as many as the worse of the two orders asks (all of them).
+    load_k(p.c0);
+    __builtin_amdgcn_sched_barrier(0);
+    load_qv(p.c0);
+    __builtin_amdgcn_sched_barrier(0);
+    load_inv(p.c0);
+    __builtin_amdgcn_sched_barrier(0);
+    load_pair(p.c0);
+    __builtin_amdgcn_sched_barrier(0);
     for (int c = p.c0; c < c_end; ++c) {
         const int rows = min(C, n - c * C);
         const DeltaSweep& sw = p.sweep;

@@ -131,11 +131,12 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_reverse_ker
     };
 
     ChunkDecay decay;
-    if (c_end > 0) {
-        load_rows(c_end - 1);
-        load_pair(c_end - 1);
-        load_inv(c_end - 1);
-    }
+    load_rows(c_end - 1);                                    // in the loop's order, as in delta_chain_kernel
+    __builtin_amdgcn_sched_barrier(0);
+    load_pair(c_end - 1);
+    __builtin_amdgcn_sched_barrier(0);
+    load_inv(c_end - 1);
+    __builtin_amdgcn_sched_barrier(0);
     for (int c = c_end - 1; c >= 0; --c) {
         const int rows = min(C, n - c * C);
         // ---- K Y of the wave's channels; Y itself, for dk, and at an anchor <S, Y>
@@ -248,23 +249,26 @@ struct DeltaQK {
     int B, T, H, Hk, dk_, dv_;
 };
 
-// One workgroup of four waves per chunk of a head of q and k, over the heads
-// that share it.  Over 32 value columns at a time, in LDS: S^T and Y^T [32][DK], dO
-// and dv [64][32], U^T [32][64].  Wave m makes the products with S and Y of
-// channels 32 m .. (transposed: a token a lane), and wave w the pairs of its 16
-// tokens with all others, which then go through LDS as operands.
+// One workgroup of eight waves per chunk of a head of q and k, over the heads that
+// share it.  Over 64 value columns at a time (fp32: 32), in LDS: S^T and Y^T [64][DK],
+// dO and dv [64][64], U^T [64][64], the next ones in flight.  Wave w makes the
+// products with S and Y of channels 32 (w % 4) .. for two of the four token tiles
+// (transposed: a token a lane), and of the tokens of tile w % 4 the pairs of dO
+// (w < 4) or of R with all others, which then go through LDS as operands.
 // With bf16 an operand is one bf16 term: what it leaves out is half a step on a
 // part of the sum, beside the result's own rounding.
 template <typename E, int DK>
-__global__ __launch_bounds__(256) void delta_qk_kernel(DeltaQK p) {
-    constexpr int NE = sizeof(E) == 2 ? 1 : 3, ES = sizeof(E), PE = 16 / ES, L = kDeltaChunk;
-    constexpr int LS = DK + 8, LT = 32 + 8, LU = L + 8;      // padded rows
-    constexpr int QS = 32 * LS, QT = L * LT, QU = 32 * LU, QK = L * LS;      // elements of a plane
+__global__ __launch_bounds__(512, 2) void delta_qk_kernel(DeltaQK p) {
+    constexpr int NE = sizeof(E) == 2 ? 1 : 3, ES = sizeof(E), PE = 16 / ES, L = kDeltaChunk, NT = 512;
+    constexpr int CS = NE == 1 ? 64 : 32;                    // value columns at a time
+    constexpr int LS = DK + 8, LT = CS + 8, LU = L + 8;      // padded rows
+    constexpr int QS = CS * LS, QT = L * LT, QU = CS * LU, QK = L * LS;      // elements of a plane
     constexpr int kFrags = 3 * 4 * 2 * NE * kFragBytes;      // bytes of the pairs' operands
     constexpr int kStage1 = NE * (2 * QS + 2 * QT + QU) * 2, kStage2 = kFrags + NE * QK * 2;
+    constexpr int RS = (CS * DK / PE + NT - 1) / NT, RT = (L * CS / PE + NT - 1) / NT, RU = (CS * L / 4 + NT - 1) / NT,
+                  RK = (L * DK / PE + NT - 1) / NT;          // pieces of a thread
     __shared__ __align__(16) char s_mem[kStage1 > kStage2 ? kStage1 : kStage2];
-    __shared__ double s_G[L];
-    __shared__ float s_eg[L], s_end[L], s_beta[L];
+    __shared__ __align__(16) float s_hi[L], s_lo[L], s_eg[L], s_end[L], s_beta[L];
     bf16 *s_S = reinterpret_cast<bf16*>(s_mem), *s_Y = s_S + NE * QS, *s_O = s_Y + NE * QS, *s_R = s_O + NE * QT, *s_U = s_R + NE * QT;
     char* s_frag = s_mem;                                    // then, in the same place, the pairs and K or Q
     bf16* s_K = reinterpret_cast<bf16*>(s_mem + kFrags);
@@ -273,16 +277,44 @@ __global__ __launch_bounds__(256) void delta_qk_kernel(DeltaQK p) {
     const int n = seq_len(p.lens, b, p.T), t0 = c * L, rows = min(L, n - t0);
     if (rows <= 0) return;
     const int tid = threadIdx.x, wave = wave_id(), lane = lane_id(), j = lane & 15, g = lane >> 4, G = p.H / p.Hk;
-    const bool mine = wave < DK / 32;                        // this wave has channels
-    f32x4 dq[2][4], dk[2][4];
+    const int m = wave & 3, half = wave >> 2;                // channels 32 m .., token tiles 2 half ..; tokens of tile m, dO or R
+    const bool mine = DK == 128 || m < DK / 32;              // this wave has channels
+    f32x4 dq[2][2], dk[2][2];
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) dq[t][r] = dk[t][r] = zero4();
+        for (int r = 0; r < 2; ++r) dq[t][r] = dk[t][r] = zero4();
 
     for (int hg = 0; hg < G; ++hg) {
         const int h = hk * G + hg, unit = b * p.H + h;
-        __syncthreads();                                     // the last head is done with LDS
+        const Rsrc rS = make_rsrc((const E*)sw.S + ((size_t)unit * sw.NC + c) * p.dv_ * DK, (uint32_t)(p.dv_ * DK * ES));
+        const Rsrc rY = make_rsrc((const E*)sw.Y + ((size_t)unit * sw.NC + c) * p.dv_ * DK, (uint32_t)(p.dv_ * DK * ES));
+        const Rsrc rE = make_rsrc(sw.e + ((size_t)unit * sw.NC + c) * p.dv_ * L, (uint32_t)(p.dv_ * L * 4));
+        const int ldv = p.H * p.dv_ * ES;
+        const size_t tok = (((size_t)b * p.T + t0) * p.H + h) * p.dv_;
+        const uint32_t tok_bytes = (uint32_t)((rows - 1) * ldv + p.dv_ * ES);
+        const Rsrc rO = make_rsrc((const E*)sw.dO + tok, tok_bytes), rR = make_rsrc((const E*)p.dv + tok, tok_bytes);
+        u32x4 xS[RS], xY[RS], xO[RT], xR[RT], xE[RU];
+        auto load = [&](int c0) {                            // columns past the last: zeros
+#pragma unroll
+            for (int i = 0; i < RS; ++i) {
+                const int at = (tid + i * NT) * 16 + c0 * DK * ES;
+                const bool in = RS * NT * PE == CS * DK || tid + i * NT < CS * DK / PE;
+                xS[i] = buf_load<u32x4>(rS, in ? at : kOffPast);
+                xY[i] = buf_load<u32x4>(rY, in ? at : kOffPast);
+            }
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                const int t = (tid + i * NT) / (CS / PE), vc = c0 + (tid + i * NT) % (CS / PE) * PE;
+                const int off = t < rows && vc < p.dv_ ? t * ldv + vc * ES : kOffPast;
+                xO[i] = buf_load<u32x4>(rO, off);
+                xR[i] = buf_load<u32x4>(rR, off);
+            }
+#pragma unroll
+            for (int i = 0; i < RU; ++i) xE[i] = buf_load<u32x4>(rE, (tid + i * NT) * 16 + c0 * L * 4);
+        };
+        load(0);
+        if (hg) __syncthreads();                             // the last head is done with LDS
         if (wave == 0) {
             const size_t at = ((size_t)b * p.T + t0 + lane) * p.H + h;
             double s = lane < rows ? (double)log_decay(p.g[at]) : 0.0;
@@ -292,46 +324,40 @@ __global__ __launch_bounds__(256) void delta_qk_kernel(DeltaQK p) {
                 if (lane >= o) s += up;
             }
             const double end = __shfl(s, L - 1);
-            s_G[lane] = s;
+            s_hi[lane] = (float)s;
+            s_lo[lane] = (float)(s - (double)(float)s);
             s_eg[lane] = expf((float)s);
             s_end[lane] = expf((float)(end - s));
             s_beta[lane] = lane < rows ? p.beta[at] : 0.f;
         }
         __syncthreads();
-        const E* gS = (const E*)sw.S + ((size_t)unit * sw.NC + c) * p.dv_ * DK;
-        const E* gY = (const E*)sw.Y + ((size_t)unit * sw.NC + c) * p.dv_ * DK;
-        const size_t tok = (((size_t)b * p.T + t0) * p.H + h) * p.dv_;
-        const float* gE = sw.e + ((size_t)unit * sw.NC + c) * p.dv_ * L;
-        f32x4 aq[2][4], as[2][4], ay[2][4], pr[4], xr[4], pd = zero4(), xd = zero4();
+        f32x4 aq[2][2], as[2][2], ay[2][2], pr[4], pd = zero4();
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            pr[r] = xr[r] = zero4();
+        for (int r = 0; r < 4; ++r) pr[r] = zero4();
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
             for (int t = 0; t < 2; ++t) aq[t][r] = as[t][r] = ay[t][r] = zero4();
-        }
-        for (int c0 = 0; c0 < p.dv_; c0 += 32) {
+        for (int c0 = 0; c0 < p.dv_; c0 += CS) {
             if (c0) __syncthreads();
-            for (int i = tid; i < 32 * DK / PE; i += 256) {
-                const int vc = i / (DK / PE), ch = i % (DK / PE) * PE;
-                put_piece<E>(s_S + vc * LS + ch, QS, *reinterpret_cast<const u32x4*>(gS + (size_t)(c0 + vc) * DK + ch));
-                put_piece<E>(s_Y + vc * LS + ch, QS, *reinterpret_cast<const u32x4*>(gY + (size_t)(c0 + vc) * DK + ch));
-            }
-            for (int i = tid; i < L * 32 / PE; i += 256) {
-                const int t = i / (32 / PE), vc = i % (32 / PE) * PE;
-                u32x4 x{}, y{};
-                if (t < rows) {
-                    const size_t at = tok + (size_t)t * p.H * p.dv_ + c0 + vc;
-                    x = *reinterpret_cast<const u32x4*>((const E*)sw.dO + at);
-                    y = *reinterpret_cast<const u32x4*>((const E*)p.dv + at);
-                }
-                put_piece<E>(s_O + t * LT + vc, QT, x);
-                put_piece<E>(s_R + t * LT + vc, QT, y);
-            }
-            for (int i = tid; i < 32 * L / 4; i += 256) {
-                const int vc = i / (L / 4), t = i % (L / 4) * 4;
-                f32x4 u = *reinterpret_cast<const f32x4*>(gE + (size_t)(c0 + vc) * L + t);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) u[x] *= s_beta[t + x];
+            for (int i = 0; i < RS; ++i) {
+                const int vc = (tid + i * NT) / (DK / PE), ch = (tid + i * NT) % (DK / PE) * PE;
+                if (RS * NT * PE == CS * DK || vc < CS) {
+                    put_piece<E>(s_S + vc * LS + ch, QS, xS[i]);
+                    put_piece<E>(s_Y + vc * LS + ch, QS, xY[i]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                const int t = (tid + i * NT) / (CS / PE), vc = (tid + i * NT) % (CS / PE) * PE;
+                put_piece<E>(s_O + t * LT + vc, QT, xO[i]);
+                put_piece<E>(s_R + t * LT + vc, QT, xR[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < RU; ++i) {
+                const int vc = (tid + i * NT) / (L / 4), t = (tid + i * NT) % (L / 4) * 4;
+                f32x4 u = __builtin_bit_cast(f32x4, xE[i]) * *reinterpret_cast<const f32x4*>(&s_beta[t]);
 #pragma unroll
                 for (int s = 0; s < NE; ++s) {
                     const bf16x4 hi = pack4(u);
@@ -341,81 +367,103 @@ __global__ __launch_bounds__(256) void delta_qk_kernel(DeltaQK p) {
                 }
             }
             __syncthreads();
-            // operands with a token a lane, value columns 4 g .. and 16 + 4 g ..
-            auto tokens = [&](const bf16* s, int r) {
+            load(c0 + CS);
+            // operands with a token a lane, value columns 32 k + 4 g .. and 32 k + 16 + 4 g ..
+            auto tokens = [&](const bf16* s, int r, int k) {
                 Terms<NE> f;
 #pragma unroll
                 for (int x = 0; x < NE; ++x) {
-                    const bf16* at = s + x * QT + (16 * r + j) * LT + 4 * g;
+                    const bf16* at = s + x * QT + (16 * r + j) * LT + 32 * k + 4 * g;
                     const bf16x4 lo = *reinterpret_cast<const bf16x4*>(at), hi = *reinterpret_cast<const bf16x4*>(at + 16);
                     f.t[x] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
                 }
                 return f;
             };
-            auto written = [&](int r) { return col_terms<NE>(s_U, QU, LU, 16 * r, 4, j, g); };
-            const Terms<NE> Ow = tokens(s_O, wave), Rw = tokens(s_R, wave), Uw = written(wave);
-            Terms<NE> Sf[2], Yf[2];
-            if (mine) {
+            auto written = [&](int r, int k) { return col_terms<NE>(s_U + 32 * k * LU, QU, LU, 16 * r, 4, j, g); };
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    Sf[t] = col_terms<NE>(s_S, QS, LS, 32 * wave + 4 * t, 8, j, g);
-                    Yf[t] = col_terms<NE>(s_Y, QS, LS, 32 * wave + 4 * t, 8, j, g);
-                }
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const Terms<NE> O = tokens(s_O, r), R = tokens(s_R, r), U = written(r);
+            for (int k = 0; k < CS / 32; ++k) {
+                if (c0 + 32 * k >= p.dv_) break;
                 if (mine) {
+                    Terms<NE> Sf[2], Yf[2];
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        aq[t][r] = mma(Sf[t], O, aq[t][r]);
-                        as[t][r] = mma(Sf[t], R, as[t][r]);
-                        ay[t][r] = mma(Yf[t], U, ay[t][r]);
+                        Sf[t] = col_terms<NE>(s_S + 32 * k * LS, QS, LS, 32 * m + 4 * t, 8, j, g);
+                        Yf[t] = col_terms<NE>(s_Y + 32 * k * LS, QS, LS, 32 * m + 4 * t, 8, j, g);
+                    }
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const Terms<NE> O = tokens(s_O, 2 * half + r, k), R = tokens(s_R, 2 * half + r, k), U = written(2 * half + r, k);
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            aq[t][r] = mma(Sf[t], O, aq[t][r]);
+                            as[t][r] = mma(Sf[t], R, as[t][r]);
+                            ay[t][r] = mma(Yf[t], U, ay[t][r]);
+                        }
                     }
                 }
-                if (r <= wave) {                             // rows: what token r wrote, lane: the later one
-                    pr[r] = mma(U, Ow, pr[r]);
-                    xr[r] = mma(U, Rw, xr[r]);
-                }
-                if (r >= wave) {                             // rows: the later token, lane: what this one wrote
-                    f32x4 &pp = r == wave ? pd : pr[r], &xx = r == wave ? xd : xr[r];
-                    pp = mma(O, Uw, pp);
-                    xx = mma(R, Uw, xx);
+                const bf16* s_x = half ? s_R : s_O;
+                const Terms<NE> Xw = tokens(s_x, m, k), Uw = written(m, k);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    if (r <= m) pr[r] = mma(written(r, k), Xw, pr[r]);     // rows: what token r wrote, lane: the later one
+                    if (r == m) pd = mma(Xw, Uw, pd);                      // rows: the later token, lane: what this one wrote
+                    if (r > m) pr[r] = mma(tokens(s_x, r, k), Uw, pr[r]);
                 }
             }
         }
         // ---- pairs with their decays, as operands with the output's token a lane:
         // (dO U^T)*D for dq, its transpose for dk, -(X + X^T) for dk
-        f32x4 wq[4], wk[4], wx[4];
-        const double Gw = s_G[16 * wave + j];
+        f32x4 wa[4], wb[4];
+        const float hi = s_hi[16 * m + j], lo = s_lo[16 * m + j];
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < 4; ++r) {
+            const f32x4 rh = *reinterpret_cast<const f32x4*>(&s_hi[16 * r + 4 * g]), rl = *reinterpret_cast<const f32x4*>(&s_lo[16 * r + 4 * g]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int d = 16 * (wave - r) + j - 4 * g - i;   // lane's token - row's token
-                const float D = expf((float)fmin(d >= 0 ? Gw - s_G[16 * r + 4 * g + i] : s_G[16 * r + 4 * g + i] - Gw, 0.0));
-                const float later = r == wave ? pd[i] : pr[r][i], xlater = r == wave ? xd[i] : xr[r][i];
-                wq[r][i] = d >= 0 ? p.scale * D * pr[r][i] : 0.f;
-                wk[r][i] = d <= 0 ? p.scale * D * later : 0.f;
-                wx[r][i] = d > 0 ? -D * xr[r][i] : d < 0 ? -D * xlater : 0.f;
+                const int d = 16 * (m - r) + j - 4 * g - i;  // lane's token - row's token
+                const float gap = (hi - rh[i]) + (lo - rl[i]), D = __expf(d >= 0 ? gap : -gap);
+                const float later = r == m ? pd[i] : pr[r][i];
+                if (half == 0) {
+                    wa[r][i] = d >= 0 ? p.scale * D * pr[r][i] : 0.f;
+                    wb[r][i] = d <= 0 ? p.scale * D * later : 0.f;
+                } else {
+                    wa[r][i] = d > 0 ? -D * pr[r][i] : d < 0 ? -D * later : 0.f;
+                }
             }
+        }
         auto put = [&](int kind, const f32x4 (&w)[4]) {
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
                 const Terms<NE> f = to_terms<NE>(w[2 * ks], w[2 * ks + 1]);
 #pragma unroll
                 for (int x = 0; x < NE; ++x)
-                    reinterpret_cast<bf16x8*>(s_frag + (((kind * 4 + wave) * 2 + ks) * NE + x) * kFragBytes)[lane] = f.t[x];
+                    reinterpret_cast<bf16x8*>(s_frag + (((kind * 4 + m) * 2 + ks) * NE + x) * kFragBytes)[lane] = f.t[x];
             }
         };
+        const int ldk = p.Hk * DK * ES;
+        const size_t row0 = (((size_t)b * p.T + t0) * p.Hk + hk) * DK;
+        const uint32_t k_bytes = (uint32_t)((rows - 1) * ldk + DK * ES);
+        const Rsrc rK = make_rsrc((const E*)p.k + row0, k_bytes), rQ = make_rsrc((const E*)p.q + row0, k_bytes);
+        u32x4 xK[RK], xQ[RK];
+#pragma unroll
+        for (int i = 0; i < RK; ++i) {
+            const int t = (tid + i * NT) / (DK / PE), ch = (tid + i * NT) % (DK / PE) * PE;
+            const int off = t < rows ? t * ldk + ch * ES : kOffPast;
+            xK[i] = buf_load<u32x4>(rK, off);
+            xQ[i] = buf_load<u32x4>(rQ, off);
+        }
         __syncthreads();                                     // every wave is done with the rows
-        put(0, wq);
-        put(1, wk);
-        put(2, wx);
+        if (half == 0) {
+            put(0, wa);
+            put(1, wb);
+        } else {
+            put(2, wa);
+        }
         if (mine) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float eg = s_eg[16 * r + j], end = s_end[16 * r + j], sq = p.scale * eg;
+            for (int r = 0; r < 2; ++r) {
+                const int t16 = 16 * (2 * half + r) + j;
+                const float eg = s_eg[t16], end = s_end[t16], sq = p.scale * eg;
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -427,29 +475,28 @@ __global__ __launch_bounds__(256) void delta_qk_kernel(DeltaQK p) {
         }
 #pragma unroll
         for (int pass = 0; pass < 2; ++pass) {               // K, then Q
-            __syncthreads();                                 // the pairs are there, K is used
-            const E* from = (const E*)(pass ? p.q : p.k) + (((size_t)b * p.T + t0) * p.Hk + hk) * DK;
-            for (int i = tid; i < L * DK / PE; i += 256) {
-                const int t = i / (DK / PE), ch = i % (DK / PE) * PE;
-                u32x4 x{};
-                if (t < rows) x = *reinterpret_cast<const u32x4*>(from + (size_t)t * p.Hk * DK + ch);
-                put_piece<E>(s_K + t * LS + ch, QK, x);
+            if (pass) __syncthreads();                       // K is used
+#pragma unroll
+            for (int i = 0; i < RK; ++i) {
+                const int t = (tid + i * NT) / (DK / PE), ch = (tid + i * NT) % (DK / PE) * PE;
+                if (RK * NT * PE == L * DK || t < L) put_piece<E>(s_K + t * LS + ch, QK, pass ? xQ[i] : xK[i]);
             }
-            __syncthreads();
+            __syncthreads();                                 // with the pairs
             if (!mine) continue;
             auto frag = [&](int kind, int r, int ks) { return frag_terms<NE>(s_frag + ((kind * 4 + r) * 2 + ks) * NE * kFragBytes); };
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    const Terms<NE> f = col_terms<NE>(s_K + 32 * ks * LS, QK, LS, 32 * wave + 4 * t, 8, j, g);
+                    const Terms<NE> f = col_terms<NE>(s_K + 32 * ks * LS, QK, LS, 32 * m + 4 * t, 8, j, g);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
+                    for (int x = 0; x < 2; ++x) {
+                        const int r = 2 * half + x;
                         if (pass == 0) {
-                            if (ks <= r / 2) dq[t][r] = mma(f, frag(0, r, ks), dq[t][r]);
-                            dk[t][r] = mma(f, frag(2, r, ks), dk[t][r]);
-                        } else if (ks >= r / 2) {
-                            dk[t][r] = mma(f, frag(1, r, ks), dk[t][r]);
+                            if (ks <= half) dq[t][x] = mma(f, frag(0, r, ks), dq[t][x]);
+                            dk[t][x] = mma(f, frag(2, r, ks), dk[t][x]);
+                        } else if (ks >= half) {
+                            dk[t][x] = mma(f, frag(1, r, ks), dk[t][x]);
                         }
                     }
                 }
@@ -457,10 +504,10 @@ __global__ __launch_bounds__(256) void delta_qk_kernel(DeltaQK p) {
     }
     if (!mine) return;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int t = 16 * r + j;
+    for (int r = 0; r < 2; ++r) {
+        const int t = 16 * (2 * half + r) + j;
         if (t >= rows) continue;
-        const size_t at = (((size_t)b * p.T + t0 + t) * p.Hk + hk) * DK + 32 * wave + 8 * g;
+        const size_t at = (((size_t)b * p.T + t0 + t) * p.Hk + hk) * DK + 32 * m + 8 * g;
         store8((E*)p.dq + at, dq[0][r], dq[1][r]);
         store8((E*)p.dk + at, dk[0][r], dk[1][r]);
     }
@@ -550,7 +597,7 @@ static hipError_t launch_k(const DeltaBackward& a, const DeltaReverse& r, const 
     hipLaunchKernelGGL((delta_reverse_kernel<E, DK>), dim3((unsigned)(a.B * a.H * (a.dv_ / 16))), dim3(256), 0, stream, r);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((delta_qk_kernel<E, DK>), dim3((unsigned)(a.B * a.Hk * r.sweep.NC)), dim3(256), 0, stream, x);
+    hipLaunchKernelGGL((delta_qk_kernel<E, DK>), dim3((unsigned)(a.B * a.Hk * r.sweep.NC)), dim3(512), 0, stream, x);
     return hipGetLastError();
 }
 
