@@ -14,7 +14,7 @@ CSRC = os.path.join(PKG, "csrc")
 SOURCES = ["kda_api.hip", "kda_decode.hip", "kda_tokens.hip", "kda_prefill.hip", "kda_pair.hip", "kda_ring.hip",
            "kda_backward.hip", "kda_bwd_chunk.hip", "kda_segscan.hip", "kda_linear_api.hip",
            "kda_linear.hip", "kda_linear_decode.hip", "kda_linear_tree.hip", "kda_norm_rope.hip",
-           "kda_delta_api.hip", "kda_delta.hip", "kda_delta_pairs.hip",
+           "kda_delta_api.hip", "kda_delta.hip", "kda_delta_wide.hip", "kda_delta_pairs.hip",
            "kda_delta_backward.hip", "kda_delta_decode.hip", "kda_gated_norm.hip", "kda_block_norm.hip"]
 # Machine scheduler per source.  The fused prefill passes and the single-token
 # decode step run 2.5-4% faster under the ILP-first strategy (measured at B1

@@ -133,7 +133,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_chain_kerne
             buf_store8<E>(to, holds ? (j * DK + 32 * w + 8 * g) * ES : kOffPast, M[0], M[1]);
         }
         if (holds) {
-            const Terms<3> sf = to_terms<3>(M[0], M[1]);
+            const Terms<3> sf = split_terms<3>(M[0], M[1]);
 #pragma unroll
             for (int s = 0; s < NS; ++s) reinterpret_cast<bf16x8*>(s_S[w] + s * kFragBytes)[lane] = sf.t[s];
 #pragma unroll
@@ -227,6 +227,9 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_chain_kerne
 // by window, the state carried in the workspace.
 constexpr size_t kDeltaWindowBytes = (size_t)192 << 20;
 
+// From so many heads on a workgroup takes a whole one (delta_wide_kernel).
+constexpr int kWideUnits = 64;
+
 struct DeltaWindows {
     int chunks, len, n;      // chunks of a sequence, of a window, windows
     size_t blocks, carry;    // bytes
@@ -265,6 +268,7 @@ hipError_t launch_delta_sweep(const DeltaChain& a, hipStream_t stream) {
 
 hipError_t launch_delta_prefill(const DeltaPrefill& a, void* ws, hipStream_t stream) {
     const DeltaWindows w = windows(a.B, a.T, a.H, a.dk, a.dv, a.is_bf16);
+    const bool wide = a.is_bf16 && a.dv == 128 && a.B * a.H >= kWideUnits;
     char* blocks = (char*)ws;
     float* carry = w.n > 1 ? (float*)(blocks + w.blocks) : nullptr;
     for (int i = 0; i < w.n; ++i) {
@@ -276,7 +280,7 @@ hipError_t launch_delta_prefill(const DeltaPrefill& a, void* ws, hipStream_t str
                                            a.is_bf16}, false, stream);
         if (e != hipSuccess) return e;
         const DeltaChain c{a.q, a.k, a.v, a.scale, S, a.lens, blocks, a.o, a.B, a.T, a.H, a.Hk, a.dk, a.dv, c0, c1, a.is_bf16, {}};
-        e = a.is_bf16 ? launch_chain<bf16, false>(c, stream) : launch_chain<float, false>(c, stream);
+        e = wide ? launch_delta_wide(c, stream) : a.is_bf16 ? launch_chain<bf16, false>(c, stream) : launch_chain<float, false>(c, stream);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;

@@ -151,7 +151,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_reverse_ker
         }
         buf_store_u32(make_rsrc(sw.anchor + anchor_at(c), 4), is_anchor(c) && lane == 0 ? 0 : kOffPast, __builtin_bit_cast(uint32_t, a));
         if (holds) {
-            const Terms<3> yf = to_terms<3>(Y[0], Y[1]);
+            const Terms<3> yf = split_terms<3>(Y[0], Y[1]);
 #pragma unroll
             for (int x = 0; x < kDeltaTiles; ++x) {
                 const Terms<NE> kt = raw_terms(rk[x]), qt = raw_terms(rq[x]);
@@ -434,7 +434,7 @@ __global__ __launch_bounds__(512, 2) void delta_qk_kernel(DeltaQK p) {
         auto put = [&](int kind, const f32x4 (&w)[4]) {
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
-                const Terms<NE> f = to_terms<NE>(w[2 * ks], w[2 * ks + 1]);
+                const Terms<NE> f = split_terms<NE>(w[2 * ks], w[2 * ks + 1]);
 #pragma unroll
                 for (int x = 0; x < NE; ++x)
                     reinterpret_cast<bf16x8*>(s_frag + (((kind * 4 + m) * 2 + ks) * NE + x) * kFragBytes)[lane] = f.t[x];

@@ -39,5 +39,7 @@ struct DeltaChain {
     DeltaSweep sweep;       // of the gradients' forward sweep, which leaves no o
 };
 hipError_t launch_delta_sweep(const DeltaChain& a, hipStream_t stream);
+// The prefill's chain by one workgroup per (b, h): bf16, dv = 128.
+hipError_t launch_delta_wide(const DeltaChain& a, hipStream_t stream);
 
 }  // namespace kda

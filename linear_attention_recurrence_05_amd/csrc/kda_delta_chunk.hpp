@@ -80,6 +80,36 @@ __device__ __forceinline__ void unit_tile(int x, int units, int tiles, int& unit
     tile = rest < 0 ? x / 8 % tiles : rest % tiles;
 }
 
+// Two fp32 values rounded to bf16 in one word, which then hold what that leaves:
+// the halves of the word are fp32 values as they stand.
+__device__ __forceinline__ uint32_t take_pair(float& a, float& b) {
+    const uint32_t w = __builtin_bit_cast(uint32_t, pack2(a, b));
+    a -= __builtin_bit_cast(float, w << 16);
+    b -= __builtin_bit_cast(float, w & 0xffff0000u);
+    return w;
+}
+// to_terms with both values of a word taken from it (44 instructions for three terms
+// of eight values, where a conversion of each value alone makes 60).
+template <int N>
+__device__ __forceinline__ Terms<N> split_terms(f32x4 lo, f32x4 hi) {
+    Terms<N> out;
+#pragma unroll
+    for (int s = 0; s < N; ++s) {
+        if (s + 1 < N) {
+            float a[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            u32x4 w;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = take_pair(a[2 * i], a[2 * i + 1]);
+            out.t[s] = __builtin_bit_cast(bf16x8, w);
+            lo = f32x4{a[0], a[1], a[2], a[3]};
+            hi = f32x4{a[4], a[5], a[6], a[7]};
+        } else {
+            out.t[s] = pack8(lo, hi);
+        }
+    }
+    return out;
+}
+
 // Eight consecutive elements of a row as loaded, 16 bytes of bf16 or 32 of fp32.
 template <typename E> struct Raw;
 template <> struct Raw<bf16> { u32x4 v; };
@@ -91,7 +121,7 @@ template <> __device__ __forceinline__ Raw<float> raw_load<float>(Rsrc r, int of
 }
 __device__ __forceinline__ Terms<1> raw_terms(const Raw<bf16>& r) { return {{__builtin_bit_cast(bf16x8, r.v)}}; }
 __device__ __forceinline__ Terms<3> raw_terms(const Raw<float>& r) {
-    return to_terms<3>(__builtin_bit_cast(f32x4, r.v), __builtin_bit_cast(f32x4, r.w));
+    return split_terms<3>(__builtin_bit_cast(f32x4, r.v), __builtin_bit_cast(f32x4, r.w));
 }
 
 // A 16-byte piece of a row to LDS: bf16 as it is, four fp32 values as their three
@@ -170,22 +200,23 @@ template <int N>
 __device__ __forceinline__ void put_half(char* frag, int half, f32x4 x) {
 #pragma unroll
     for (int s = 0; s < N; ++s) {
-        const bf16x4 h = pack4(x);
-        *reinterpret_cast<bf16x4*>(frag + s * kFragBytes + lane_id() * 16 + half * 8) = h;
-        if (s + 1 < N) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] -= (float)h[i];
-        }
+        float a[4] = {x[0], x[1], x[2], x[3]};
+        u32x2 w;
+        w[0] = take_pair(a[0], a[1]);
+        w[1] = take_pair(a[2], a[3]);
+        *reinterpret_cast<u32x2*>(frag + s * kFragBytes + lane_id() * 16 + half * 8) = w;
+        x = f32x4{a[0], a[1], a[2], a[3]};
     }
 }
-// Column j of rows 4 g .. 4 g + 3 of a [16][ld] tile kept as N bf16 planes in LDS.
+// Column step (j / 4) + j % 4 of rows 4 g .. 4 g + 3 of a [16][ld] tile kept as N
+// bf16 planes in LDS.
 template <int N>
-__device__ __forceinline__ f32x4 col4(const bf16* s, int plane, int ld, int j, int g) {
+__device__ __forceinline__ f32x4 col4(const bf16* s, int plane, int ld, int j, int g, int step = 4) {
     typedef __attribute__((address_space(3))) i16x4 lds4;
     f32x4 x = zero4();
 #pragma unroll
     for (int n = N - 1; n >= 0; --n) {
-        const bf16* p = s + n * plane + (4 * g + (j >> 2)) * ld + 4 * (j & 3);
+        const bf16* p = s + n * plane + (4 * g + (j >> 2)) * ld + step * (j & 3);
         const bf16x4 v = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)p));
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] += (float)v[i];
