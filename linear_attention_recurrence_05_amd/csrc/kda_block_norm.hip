@@ -10,7 +10,12 @@
 //
 // Bound by the one read and one write of the rows.  A row is held in registers,
 // as up to NV pieces of 16 bytes in each of TPR threads: one wave (four rows a
-// workgroup, no LDS), 256 or 1024 threads, which sum through LDS in fixed order.
+// workgroup, no LDS) or a workgroup, which sums through LDS in fixed order.  A
+// workgroup takes several rows, with the next one's pieces in flight and the
+// weights, twice a bf16 row's bytes each, in registers throughout: 4,096 bf16 rows
+// of 7,168 with norm, gate and weights take 54 us, 5.4 TB/s (85 us with one row of
+// a workgroup after the other and the weights read for each), the gradients of
+// 2,002 rows of 4,096 take 38.5 us (57.5 us).
 #include <algorithm>
 
 #include "kda_delta.hpp"
@@ -18,69 +23,84 @@
 
 namespace kda {
 
-// Most workgroups of a launch; more rows loop.  Each row slot of the gradients'
-// workgroups leaves partial weight gradients.
-constexpr int kBlockGroups = 4096, kBlockBwdGroups = 512;
+// Waves of a launch at most, about as many as a device holds: more rows loop.  Each
+// row slot of the gradients' workgroups leaves partial weight gradients.
+constexpr int kBlockWaves = 4096, kBlockBwdWaves = 2048;
 
 // Sums over a row's TPR threads, the same in all of them.  With more than one
 // wave, a call uses buffer `at` of LDS, which the call after the next may reuse.
 template <int TPR>
 struct RowSum {
     static constexpr int W = TPR / kWave;
-    float (*s)[W][2];   // [3][W][2]
+    float* s;   // [2][W]
     int at = 0;
-    __device__ void operator()(float& a, float& b) {
+    __device__ float operator()(float a) {
 #pragma unroll
-        for (int o = 1; o < kWave; o <<= 1) {
-            a += __shfl_xor(a, o);
-            b += __shfl_xor(b, o);
-        }
+        for (int o = 1; o < kWave; o <<= 1) a += __shfl_xor(a, o);
         if constexpr (W > 1) {
-            if (lane_id() == 0) {
-                s[at][threadIdx.x / kWave][0] = a;
-                s[at][threadIdx.x / kWave][1] = b;
-            }
+            if (lane_id() == 0) s[at * W + threadIdx.x / kWave] = a;
             __syncthreads();
-            a = b = 0.f;
+            a = 0.f;
 #pragma unroll
-            for (int i = 0; i < W; ++i) {
-                a += s[at][i][0];
-                b += s[at][i][1];
-            }
-            at = at == 2 ? 0 : at + 1;
+            for (int i = 0; i < W; ++i) a += s[at * W + i];
+            at ^= 1;
         }
+        return a;
     }
 };
 
 template <typename E, int TPR, int NV, bool BWD>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void block_norm_kernel(BlockNorm p, float* __restrict__ part) {
     constexpr int VE = 16 / sizeof(E), NT = TPR < 256 ? 256 : TPR, RPW = NT / TPR;
-    __shared__ float s_sum[3][TPR / kWave][2];
+    constexpr bool FAST = sizeof(E) == 2;
+    constexpr bool AHEAD = TPR < 1024;   // 1,024 threads have half the registers
+    __shared__ float s_sum[2 * TPR / kWave];
     RowSum<TPR> sum{s_sum};
     const int t = threadIdx.x % TPR, slot = TPR < 256 ? wave_id() : 0, pieces = p.D / VE;
     const float inv = 1.0f / (float)p.D;
-    auto load = [&](const void* base, size_t row, int v, float (&x)[VE]) {
-        unpack<E, VE>(__builtin_nontemporal_load(reinterpret_cast<const u32x4*>((const E*)base + row * p.D) + v * TPR + t), x);
-    };
-    auto store = [&](void* base, size_t row, int v, const float (&x)[VE]) {
-        store_row<E, VE>((E*)base + row * p.D + (size_t)(v * TPR + t) * VE, x);
-    };
-    auto weight = [&](const float* w, int v, float (&x)[VE]) {
-#pragma unroll
-        for (int i = 0; i < VE; i += 4)
-            *reinterpret_cast<f32x4*>(&x[i]) = *reinterpret_cast<const f32x4*>(w + (size_t)(v * TPR + t) * VE + i);
-    };
     auto has = [&](int v) { return v * TPR + t < pieces; };
+    float wy[NV][VE], wn[NV][VE];
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int i = 0; i < VE; i += 4) {
+            const size_t e = (size_t)(v * TPR + t) * VE + i;
+            const f32x4 one = {1.f, 1.f, 1.f, 1.f};
+            *reinterpret_cast<f32x4*>(&wy[v][i]) = p.w_y && has(v) ? *reinterpret_cast<const f32x4*>(p.w_y + e) : one;
+            *reinterpret_cast<f32x4*>(&wn[v][i]) = p.w_n && has(v) ? *reinterpret_cast<const f32x4*>(p.w_n + e) : one;
+        }
+    struct Row {
+        u32x4 y[NV], h[NV], z[NV], dn[BWD ? NV : 1], dh[BWD ? NV : 1];
+    };
+    auto fetch = [&](long long row, Row& x) {                // pieces that are absent: zeros
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const bool in = row < p.rows && has(v);
+            const size_t at = ((size_t)row * p.D) / VE + v * TPR + t;
+            auto get = [&](const void* base) {
+                return base && in ? __builtin_nontemporal_load((const u32x4*)base + at) : u32x4{0, 0, 0, 0};
+            };
+            x.y[v] = get(p.y);
+            x.h[v] = get(BWD ? p.h_in : p.r);
+            x.z[v] = get(p.z);
+            if constexpr (BWD) {
+                x.dn[v] = get(p.dn);
+                x.dh[v] = get(p.dh);
+            }
+        }
+    };
+    auto store = [&](void* base, long long row, int v, const float (&x)[VE]) {
+        store_row<E, VE>((E*)base + (size_t)row * p.D + (size_t)(v * TPR + t) * VE, x);
+    };
     // r of the row in x, which is taken times `scale` where its squares leave fp32
     auto norm = [&](float (&x)[NV][VE], float& scale) {
         auto mean = [&](float eps) {
-            float a = 0.f, b = 0.f;
+            float a = 0.f;
 #pragma unroll
             for (int v = 0; v < NV; ++v)
 #pragma unroll
                 for (int i = 0; i < VE; ++i) a += x[v][i] * x[v][i];
-            sum(a, b);
-            return a * inv + eps;
+            return sum(a) * inv + eps;
         };
         float m = mean(p.eps);
         scale = 1.0f;
@@ -99,117 +119,91 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void block_norm_kernel(Block
     for (int v = 0; v < (BWD ? NV : 1); ++v)
 #pragma unroll
         for (int i = 0; i < VE; ++i) dwy[v][i] = dwn[v][i] = 0.f;
-    for (long long row = (long long)blockIdx.x * RPW + slot; row < p.rows; row += (long long)gridDim.x * RPW) {
+    const long long step = (long long)gridDim.x * RPW;
+    long long row = (long long)blockIdx.x * RPW + slot;
+    Row next;
+    if constexpr (AHEAD) fetch(row, next);
+    for (; row < p.rows; row += step) {
+        if constexpr (!AHEAD) fetch(row, next);
+        const Row cur = next;
+        if constexpr (AHEAD) fetch(row + step, next);
         float y[NV][VE], h[NV][VE], scale;
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
-#pragma unroll
-            for (int i = 0; i < VE; ++i) y[v][i] = h[v][i] = 0.f;
-        if (p.y) {
-#pragma unroll
-            for (int v = 0; v < NV; ++v)
-                if (has(v)) load(p.y, row, v, y[v]);
+        for (int v = 0; v < NV; ++v) {
+            unpack<E, VE>(cur.y[v], y[v]);
+            unpack<E, VE>(cur.h[v], h[v]);
         }
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-            if (has(v)) load(BWD ? p.h_in : p.r, row, v, h[v]);
         float ry = 1.0f, yscale = 1.0f;
         if (p.norm_y) ry = norm(y, yscale);
         if constexpr (!BWD) {
             if (p.y) {
 #pragma unroll
                 for (int v = 0; v < NV; ++v) {
-                    if (!has(v)) continue;
-                    float w[VE], z[VE];
-                    if (p.w_y) weight(p.w_y, v, w);
-                    if (p.z) load(p.z, row, v, z);
+                    float z[VE];
+                    unpack<E, VE>(cur.z[v], z);
 #pragma unroll
                     for (int i = 0; i < VE; ++i) {
-                        float u = y[v][i] * ry, s, rest;
-                        if (p.w_y) u *= w[i];
-                        if (p.z) {
-                            sigmoids(z[i], s, rest);
-                            u *= s;
-                        }
+                        float u = y[v][i] * ry * wy[v][i];
+                        if (p.z) u *= sigmoid<FAST>(z[i]);
                         h[v][i] += p.scale * u;
                     }
-                    store(p.h, row, v, h[v]);
+                    if (has(v)) store(p.h, row, v, h[v]);
                 }
             }
             const float r = norm(h, scale);
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                if (!has(v)) continue;
-                float w[VE];
-                if (p.w_n) weight(p.w_n, v, w);
 #pragma unroll
-                for (int i = 0; i < VE; ++i) h[v][i] *= p.w_n ? r * w[i] : r;
-                store(p.n, row, v, h[v]);
+                for (int i = 0; i < VE; ++i) h[v][i] *= r * wn[v][i];
+                if (has(v)) store(p.n, row, v, h[v]);
             }
         } else {
             const float r = norm(h, scale);
-            float t1[NV][VE], dot = 0.f, none = 0.f;
+            float g[NV][VE], dot = 0.f, dot_y = 0.f;
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-#pragma unroll
-                for (int i = 0; i < VE; ++i) t1[v][i] = 0.f;
-                if (!has(v)) continue;
-                float w[VE];
-                load(p.dn, row, v, t1[v]);
-                if (p.w_n) weight(p.w_n, v, w);
+                unpack<E, VE>(cur.dn[v], g[v]);
 #pragma unroll
                 for (int i = 0; i < VE; ++i) {
                     h[v][i] *= r;
-                    dwn[v][i] += t1[v][i] * h[v][i];
-                    if (p.w_n) t1[v][i] *= w[i];
-                    dot += t1[v][i] * h[v][i];
+                    dwn[v][i] += g[v][i] * h[v][i];
+                    g[v][i] *= wn[v][i];
+                    dot += g[v][i] * h[v][i];
                 }
             }
-            sum(dot, none);
-            dot *= inv;
-            float dot_y = 0.f;
+            dot = sum(dot) * inv;
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                if (!has(v)) continue;
-                float x[VE], w[VE], z[VE], dz[VE];
-                if (p.dh) load(p.dh, row, v, x);
+                float x[VE], z[VE], dz[VE];
+                unpack<E, VE>(cur.dh[v], x);
 #pragma unroll
-                for (int i = 0; i < VE; ++i) {
-                    const float g = scale * (r * (t1[v][i] - dot * h[v][i]));
-                    t1[v][i] = p.dh ? x[i] + g : g;
-                }
-                store(p.dr, row, v, t1[v]);
+                for (int i = 0; i < VE; ++i) g[v][i] = x[i] + scale * (r * (g[v][i] - dot * h[v][i]));
+                if (has(v)) store(p.dr, row, v, g[v]);
                 if (!p.y) continue;
-                if (p.w_y) weight(p.w_y, v, w);
-                if (p.z) load(p.z, row, v, z);
+                unpack<E, VE>(cur.z[v], z);
 #pragma unroll
                 for (int i = 0; i < VE; ++i) {
-                    const float du = p.scale * t1[v][i];
                     float s = 1.0f, rest = 0.f;
+                    if (p.z) sigmoids<FAST>(z[i], s, rest);
                     y[v][i] *= ry;
-                    if (p.z) sigmoids(z[i], s, rest);
-                    dwy[v][i] += du * s * y[v][i];
-                    float dm = du * s;
-                    if (p.w_y) dm *= w[i];
+                    const float du = p.scale * g[v][i] * s;
+                    dwy[v][i] += du * y[v][i];
+                    const float dm = du * wy[v][i];
                     dz[i] = dm * y[v][i] * rest;
                     dot_y += dm * y[v][i];
-                    t1[v][i] = dm;
+                    g[v][i] = dm;
                 }
-                if (p.z) store(p.dz, row, v, dz);
+                if (p.z && has(v)) store(p.dz, row, v, dz);
             }
             if (p.y) {
-                if (p.norm_y) {
-                    sum(dot_y, none);
-                    dot_y *= inv;
-                }
+                if (p.norm_y) dot_y = sum(dot_y) * inv;
 #pragma unroll
                 for (int v = 0; v < NV; ++v) {
-                    if (!has(v)) continue;
                     if (p.norm_y) {
 #pragma unroll
-                        for (int i = 0; i < VE; ++i) t1[v][i] = yscale * (ry * (t1[v][i] - dot_y * y[v][i]));
+                        for (int i = 0; i < VE; ++i) g[v][i] = yscale * (ry * (g[v][i] - dot_y * y[v][i]));
                     }
-                    store(p.dy, row, v, t1[v]);
+                    if (has(v)) store(p.dy, row, v, g[v]);
                 }
             }
         }
@@ -229,63 +223,39 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void block_norm_kernel(Block
     }
 }
 
-// The sum of the row slots' partial weight gradients, 16 columns a workgroup.
-__global__ __launch_bounds__(256) void block_norm_dw_kernel(const float* __restrict__ part, int n, int D,
-                                                            float* __restrict__ dw_y, float* __restrict__ dw_n) {
-    __shared__ float s_t[16][17];
-    const int e = blockIdx.x * 16 + threadIdx.x % 16, row = threadIdx.x / 16;
-    float t = 0.f;
-#pragma unroll 16
-    for (int i = row; i < n; i += 16) t += part[(size_t)i * 2 * D + e];
-    s_t[row][threadIdx.x % 16] = t;
-    __syncthreads();
-    if (row == 0) {
-#pragma unroll
-        for (int i = 1; i < 16; ++i) t += s_t[i][threadIdx.x];
-        float* dw = e < D ? dw_y : dw_n;
-        if (dw) dw[e < D ? e : e - D] = t;
-    }
+// Threads of a row, so that each has at most two pieces of it (of the widest fp32
+// rows four).
+static int block_threads(int D, bool is_bf16) {
+    const int pieces = D / (is_bf16 ? 8 : 4);
+    return pieces <= 128 ? 64 : pieces <= 512 ? 256 : pieces <= 1024 ? 512 : 1024;
 }
-
-// Threads of a row and pieces of a thread: up to four pieces each.
-struct BlockShape {
-    int tpr, nv;
-};
-static BlockShape block_shape(int D, bool is_bf16) {
-    const int pieces = D / (is_bf16 ? 8 : 4), tpr = pieces <= 256 ? 64 : pieces <= 1024 ? 256 : 1024;
-    const int nv = (pieces + tpr - 1) / tpr;
-    return {tpr, nv > 2 ? 4 : nv};
-}
-static int block_groups(long long rows, int tpr, int most) {
-    const int rpw = tpr < 256 ? 256 / tpr : 1;
-    return (int)std::min<long long>((rows + rpw - 1) / rpw, most);
+static int block_groups(long long rows, int tpr, int most_waves) {
+    const int rpw = tpr < 256 ? 256 / tpr : 1, waves = std::max(tpr, 256) / kWave;
+    return (int)std::min<long long>((rows + rpw - 1) / rpw, most_waves / waves);
 }
 static int block_slots(long long rows, int tpr) {   // partial weight gradients
-    return block_groups(rows, tpr, kBlockBwdGroups) * (tpr < 256 ? 256 / tpr : 1);
+    return block_groups(rows, tpr, kBlockBwdWaves) * (tpr < 256 ? 256 / tpr : 1);
 }
 
 template <typename E, bool BWD, int TPR, int NV>
 static hipError_t launch_v(const BlockNorm& a, float* part, hipStream_t stream) {
-    const dim3 grid((unsigned)block_groups(a.rows, TPR, BWD ? kBlockBwdGroups : kBlockGroups)), block(TPR < 256 ? 256 : TPR);
+    const dim3 grid((unsigned)block_groups(a.rows, TPR, BWD ? kBlockBwdWaves : kBlockWaves)), block(TPR < 256 ? 256 : TPR);
     hipLaunchKernelGGL((block_norm_kernel<E, TPR, NV, BWD>), grid, block, 0, stream, a, part);
     return hipGetLastError();
 }
 
-template <typename E, bool BWD, int TPR>
-static hipError_t launch_t(const BlockNorm& a, float* part, int nv, hipStream_t stream) {
-    if constexpr (TPR == 64) {
-        if (nv == 1) return launch_v<E, BWD, TPR, 1>(a, part, stream);
-    }
-    return nv == 2 ? launch_v<E, BWD, TPR, 2>(a, part, stream) : launch_v<E, BWD, TPR, 4>(a, part, stream);
-}
-
 template <typename E, bool BWD>
 static hipError_t launch_e(const BlockNorm& a, float* part, hipStream_t stream) {
-    const BlockShape s = block_shape(a.D, sizeof(E) == 2);
-    switch (s.tpr) {
-        case 64: return launch_t<E, BWD, 64>(a, part, s.nv, stream);
-        case 256: return launch_t<E, BWD, 256>(a, part, s.nv, stream);
-        default: return launch_t<E, BWD, 1024>(a, part, s.nv, stream);
+    const int pieces = a.D / (sizeof(E) == 2 ? 8 : 4), tpr = block_threads(a.D, sizeof(E) == 2);
+    switch (tpr) {
+        case 64: return pieces <= 64 ? launch_v<E, BWD, 64, 1>(a, part, stream) : launch_v<E, BWD, 64, 2>(a, part, stream);
+        case 256: return pieces <= 256 ? launch_v<E, BWD, 256, 1>(a, part, stream) : launch_v<E, BWD, 256, 2>(a, part, stream);
+        case 512: return launch_v<E, BWD, 512, 2>(a, part, stream);
+        default:
+            if constexpr (sizeof(E) == 4) {
+                if (pieces > 2048) return launch_v<E, BWD, 1024, 4>(a, part, stream);
+            }
+            return launch_v<E, BWD, 1024, 2>(a, part, stream);
     }
 }
 
@@ -294,15 +264,15 @@ hipError_t launch_block_norm(const BlockNorm& a, hipStream_t stream) {
 }
 
 size_t block_norm_backward_ws_bytes(long long rows, int D, bool is_bf16) {
-    return (size_t)block_slots(rows, block_shape(D, is_bf16).tpr) * 2 * D * sizeof(float);
+    return (size_t)block_slots(rows, block_threads(D, is_bf16)) * 2 * D * sizeof(float);
 }
 
 hipError_t launch_block_norm_backward(const BlockNorm& a, void* ws, hipStream_t stream) {
     float* part = a.dw_y || a.dw_n ? (float*)ws : nullptr;
     const hipError_t e = a.is_bf16 ? launch_e<bf16, true>(a, part, stream) : launch_e<float, true>(a, part, stream);
     if (e != hipSuccess || !part) return e;
-    hipLaunchKernelGGL(block_norm_dw_kernel, dim3(2 * a.D / 16), dim3(256), 0, stream, part,
-                       block_slots(a.rows, block_shape(a.D, a.is_bf16).tpr), a.D, a.dw_y, a.dw_n);
+    hipLaunchKernelGGL(sum_parts_kernel, dim3((2 * a.D + 63) / 64), dim3(1024), 0, stream, part,
+                       block_slots(a.rows, block_threads(a.D, a.is_bf16)), 2 * a.D, a.D, a.dw_y, a.dw_n);
     return hipGetLastError();
 }
 

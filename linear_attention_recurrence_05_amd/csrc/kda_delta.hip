@@ -227,8 +227,11 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_chain_kerne
 // by window, the state carried in the workspace.
 constexpr size_t kDeltaWindowBytes = (size_t)192 << 20;
 
-// From so many heads on a workgroup takes a whole one (delta_wide_kernel).
-constexpr int kWideUnits = 64;
+// From so many heads of bf16 rows on a workgroup takes a whole one
+// (delta_wide_kernel), where fewer leave more than half of the device idle.  d 128,
+// T 4096, wide against eight workgroups of 16 columns: 64 heads 402 and 308 us, 128
+// heads 484 and 615 us, 256 heads 676 and 1,236 us.
+constexpr int kWideUnits = 128;
 
 struct DeltaWindows {
     int chunks, len, n;      // chunks of a sequence, of a window, windows

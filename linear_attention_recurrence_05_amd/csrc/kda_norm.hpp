@@ -34,11 +34,25 @@ __device__ __forceinline__ void store_row(E* p, const float (&x)[VE]) {
 }
 
 // Sigmoid(z) and 1 - Sigmoid(z) = Sigmoid(-z), each without cancellation and
-// without an overflow that matters.
+// without an overflow that matters.  For bf16 rows by the hardware's exp2 and
+// reciprocal (1 ulp each, |z| 2^-24 from the product: eight instructions, where the
+// full-range functions take forty and more and the norms become bound by them).
+template <bool FAST>
 __device__ __forceinline__ void sigmoids(float z, float& s, float& rest) {
-    const float e = expf(-fabsf(z)), big = 1.0f / (1.0f + e), small = e * big;
+    const float e = FAST ? fast_exp2(-fabsf(z) * kLog2e) : expf(-fabsf(z));
+    const float big = FAST ? fast_rcp(1.0f + e) : 1.0f / (1.0f + e), small = e * big;
     s = z >= 0.f ? big : small;
     rest = z >= 0.f ? small : big;
 }
+template <bool FAST>
+__device__ __forceinline__ float sigmoid(float z) {
+    return FAST ? fast_rcp(1.0f + fast_exp2(-z * kLog2e)) : 1.0f / (1.0f + expf(-z));
+}
+
+// out[e] = sum over i of part[i][e], i = 0 .. n - 1, for e of `width` columns: 64
+// columns a workgroup of 1024 threads, in fixed order.  Columns from `first` on go
+// to `b`; a null array is not wanted.
+__global__ __launch_bounds__(1024) void sum_parts_kernel(const float* __restrict__ part, int n, int width, int first,
+                                                         float* __restrict__ a, float* __restrict__ b);
 
 }  // namespace kda
