@@ -142,6 +142,19 @@ __device__ __forceinline__ void put_piece(bf16* dst, int plane, u32x4 v, bool on
     }
 }
 
+// Four values as N terms to LDS, `plane` elements apart.
+template <int N>
+__device__ __forceinline__ void put_words(bf16* dst, int plane, f32x4 x) {
+    float a[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+    for (int s = 0; s < N; ++s) {
+        u32x2 w;
+        w[0] = take_pair(a[0], a[1]);
+        w[1] = take_pair(a[2], a[3]);
+        *reinterpret_cast<u32x2*>(dst + s * plane) = w;
+    }
+}
+
 // Four elements from a buffer, and eight to it.
 template <typename E>
 __device__ __forceinline__ f32x4 buf_load4(Rsrc r, int off) {
@@ -171,6 +184,24 @@ __device__ __forceinline__ void store8(float* p, f32x4 lo, f32x4 hi) {
 // such stores are dropped.
 constexpr int kOffPast = -(1 << 16);
 
+// Elements from one row of DK channels to the next in LDS: 16 banks on (of 64), so
+// that the four rows of which col_terms reads every other 8 bytes with 16 lanes lie
+// beside each other (with DK + 8 elements they met in the same banks four times).
+template <int DK>
+constexpr int kRowLd = DK == 32 ? 32 : DK + 32;
+
+// mma, but of two operands of two terms without the product of both second ones
+// (2^-18 of the largest).
+template <int N, int M>
+__device__ __forceinline__ f32x4 mma_top(const Terms<N>& a, const Terms<M>& b, f32x4 c) {
+    if constexpr (N == 2 && M == 2) {
+        c = mma_bf16_k32(a.t[0], b.t[1], c);
+        c = mma_bf16_k32(a.t[1], b.t[0], c);
+        return mma_bf16_k32(a.t[0], b.t[0], c);
+    } else {
+        return mma(a, b, c);
+    }
+}
 template <int N, int M>
 __device__ __forceinline__ Terms<N> first_terms(const Terms<M>& a) {
     Terms<N> out;

@@ -2,16 +2,15 @@
 // depend on the state (kda_delta_chunk.hpp): the inverse of the triangular system
 // and the weights of pairs of tokens, as matrix operands in the workspace.
 //
-// One wave per chunk and head, and per system of the two that the gradients take
-// (T of I + N diag(beta) with P, and T of I + diag(beta) N with P^T).  K K^T and
-// Q K^T by MFMA with the decays applied in the accumulators; N in LDS as its ten
+// One wave per chunk and head.  K K^T and Q K^T by MFMA with the decays applied in the accumulators; N in LDS as its ten
 // tiles of 16 x 16.  The inverse: the four tiles on the diagonal by substitution, a
 // column a lane (stable for any beta in [0, 2] and keys of length 1, where a series
 // in powers of N is not: repeated keys make its terms grow to thousands before they
 // cancel), then those below, T_rc = -T_rr sum_q A_rq T_qc, in fp32 MFMA, in N's place.
 // (Four waves a chunk, each with 16 of its tokens, left three of four lanes idle in
 // the substitution and two waves in the products below, and took three times as
-// long: 42 us for the 2,048 chunks of B1 H32 T4096.)
+// long.)  The 2,048 chunks of B1 H32 T4096 d128 take 23 us, with the gradients'
+// operands 48 us, of which the 113 MB that they write are half.
 #include <algorithm>
 
 #include "kda_delta_chunk.hpp"
@@ -41,15 +40,15 @@ template <typename E, int DK, int NP, bool BACK>
 __global__ __launch_bounds__(256, 2) void delta_pairs_kernel(DeltaPairs p) {
     using Blk = DeltaBlock<NP, BACK>;
     constexpr int C = kDeltaChunk, NTL = kDeltaTiles, KM = DK / 32, NE = sizeof(E) == 2 ? 1 : 3, ES = sizeof(E), LD = kTileLd;
-    __shared__ __align__(16) float s_n[4][10 * kTileSize], s_hi[4][C], s_lo[4][C], s_beta[4][C];
+    constexpr int NB = NTL * (NTL + 1) / 2;                    // tiles on and below the diagonal
+    __shared__ __align__(16) float s_n[4][NB * kTileSize], s_hi[4][C], s_lo[4][C], s_beta[4][C];
     const int wv = wave_id(), W = p.c1 - p.c0;
     float *N = s_n[wv], *sh = s_hi[wv], *sl = s_lo[wv], *sb = s_beta[wv];
-    const long long all = (long long)p.B * W * p.H * (BACK ? 2 : 1);
-    for (long long it = (long long)blockIdx.x * 4 + wv; it < all; it += (long long)gridDim.x * 4) {
+    const unsigned all = (unsigned)(p.B * W * p.H);            // of blocks in memory: fewer than 2^31
+    for (unsigned it = blockIdx.x * 4 + wv; it < all; it += gridDim.x * 4) {
         const int lane = fresh_lane_id(), j = lane & 15, g = lane >> 4;
-        const bool other = BACK && (it & 1);                   // the system of the gradients alone
-        const long long at = BACK ? it >> 1 : it;
-        const int h = (int)(at % p.H), c = p.c0 + (int)(at / p.H % W), b = (int)(at / p.H / W);
+        const unsigned per = (unsigned)p.H, win = (unsigned)W;
+        const int h = (int)(it % per), c = p.c0 + (int)(it / per % win), b = (int)(it / per / win);
         const int n = seq_len(p.lens, b, p.T), t0 = c * C, rows = min(C, n - t0);
         if (rows <= 0 || p.S.skip(b)) continue;                // uniform over the wave
         char* blk = p.blocks + (((size_t)b * p.H + h) * W + (c - p.c0)) * Blk::bytes;
@@ -73,7 +72,7 @@ __global__ __launch_bounds__(256, 2) void delta_pairs_kernel(DeltaPairs p) {
         sh[lane] = (float)G;
         sl[lane] = (float)(G - (double)(float)G);
         sb[lane] = beta;
-        if (!other) {
+        {
             float* out = reinterpret_cast<float*>(blk + Blk::row);
             const float end = expf((float)(GC - G));
             out[kRowGrow + lane] = expf((float)G);
@@ -88,51 +87,136 @@ __global__ __launch_bounds__(256, 2) void delta_pairs_kernel(DeltaPairs p) {
             }
         }
         wave_fence();
-        auto tile = [&](int r, int c_) { return N + (r * (r + 1) / 2 + c_) * kTileSize; };
-        // ---- rows of K; N = (K K^T) * D below the diagonal, row: the later token; the
-        // pairs: P with the later token w's queries, or P^T with the key w
-        Terms<NE> k[NTL][KM];
-#pragma unroll
-        for (int a = 0; a < NTL; ++a)
-#pragma unroll
-            for (int m = 0; m < KM; ++m) k[a][m] = raw_terms(row(rk, a, m));
-        f32x4 kh[NTL], kl[NTL], kb[NTL];                       // of token 16 a + 4 g + i
+        auto at = [](int r, int c_) { return r * (r + 1) / 2 + c_; };
+        auto tile = [&](int r, int c_) { return N + at(r, c_) * kTileSize; };
+        // ---- N = (K K^T) * D below the diagonal, row: the later token w
+        f32x4 kh[NTL], kl[NTL];                                // of token 16 a + 4 g + i
 #pragma unroll
         for (int a = 0; a < NTL; ++a) {
             kh[a] = *reinterpret_cast<const f32x4*>(&sh[16 * a + 4 * g]);
             kl[a] = *reinterpret_cast<const f32x4*>(&sl[16 * a + 4 * g]);
-            kb[a] = *reinterpret_cast<const f32x4*>(&sb[16 * a + 4 * g]);
         }
+        auto put_n = [&](const f32x4 (&kk)[NB]) {
 #pragma unroll
-        for (int w = 0; w < NTL; ++w) {
-            const float hi = sh[16 * w + j], lo = sl[16 * w + j];
-            f32x4 P[NTL];
+            for (int w = 0; w < NTL; ++w) {
+                const float hi = sh[16 * w + j], lo = sl[16 * w + j];
 #pragma unroll
-            for (int a = 0; a < NTL; ++a) P[a] = zero4();
-            Terms<NE> q[KM];
-            if (!other) {
+                for (int a = 0; a <= w; ++a) {
+                    f32x4 v;
 #pragma unroll
-                for (int m = 0; m < KM; ++m) q[m] = raw_terms(row(rq, w, m));
-            }
-#pragma unroll
-            for (int a = 0; a <= w; ++a) {
-                f32x4 kk = zero4(), kq = zero4();
-#pragma unroll
-                for (int m = 0; m < KM; ++m) {
-                    kk = mma(k[a][m], k[w][m], kk);
-                    if (!other) kq = mma(k[a][m], q[m], kq);
+                    for (int i = 0; i < 4; ++i) {              // a value, then a selection: no branch
+                        const float x = __expf((hi - kh[a][i]) + (lo - kl[a][i])) * kk[at(w, a)][i];
+                        v[i] = a < w || j - 4 * g - i > 0 ? x : 0.f;
+                    }
+                    *reinterpret_cast<f32x4*>(tile(w, a) + j * LD + 4 * g) = v;
                 }
-                f32x4 v;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int d = 16 * (w - a) + j - 4 * g - i;   // later - key
-                    const float D = d >= 0 ? __expf((hi - kh[a][i]) + (lo - kl[a][i])) : 0.f;
-                    P[a][i] = p.scale * D * kb[a][i] * kq[i];
-                    v[i] = d > 0 ? D * kk[i] : 0.f;
-                }
-                *reinterpret_cast<f32x4*>(tile(w, a) + j * LD + 4 * g) = v;
             }
-            if (!other) {
+        };
+        // T = (I + N diag(beta))^{-1} in N's place, with the strengths in sb
+        auto invert = [&] {
+            // the tiles on the diagonal, one to 16 lanes: x = 1 - N diag(beta) x below it
+            {
+                float* M = N + (g * (g + 1) / 2 + g) * kTileSize;
+                float x[16], y[16];                            // y: what later rows take of x
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    float acc = 0.f;
+                    f32x4 a[4];
+                    if (r % 4 == 0) __builtin_amdgcn_sched_barrier(0);   // else all rows are read first: 144 registers
+#pragma unroll
+                    for (int q = 0; q < (r + 3) / 4; ++q) a[q] = *reinterpret_cast<const f32x4*>(M + r * LD + 4 * q);
+#pragma unroll
+                    for (int q = 0; q < r; ++q) acc += a[q / 4][q % 4] * y[q];
+                    x[r] = (r == j ? 1.f : 0.f) - acc;
+                    y[r] = sb[16 * g + r] * x[r];
+                }
+                wave_fence();
+#pragma unroll
+                for (int r = 0; r < 16; ++r) M[r * LD + j] = x[r];
+            }
+            wave_fence();
+            // those below, column by column: an accumulator is the next product's
+            // operand as it is (rows 4 g + s for both)
+            f32x4 kb[NTL];
+#pragma unroll
+            for (int a = 0; a < NTL; ++a) kb[a] = *reinterpret_cast<const f32x4*>(&sb[16 * a + 4 * g]);
+            auto add = [&](int r, int q, int c_, f32x4 acc) {  // N_rq diag(beta) T_qc
+                const f32x4 a = *reinterpret_cast<const f32x4*>(tile(r, q) + j * LD + 4 * g);
+                const float* t = tile(q, c_) + 4 * g * LD + j;
+#pragma unroll
+                for (int s = 0; s < 4; ++s) acc = mma_f32_k4(a[s], t[s * LD] * kb[q][s], acc);
+                return acc;
+            };
+            auto solve = [&](int r, int c_, f32x4 x) {         // T_rc = -T_rr x, in N_rc's place
+                const f32x4 a = *reinterpret_cast<const f32x4*>(tile(r, r) + j * LD + 4 * g);
+                f32x4 y = zero4();
+#pragma unroll
+                for (int s = 0; s < 4; ++s) y = mma_f32_k4(a[s], x[s], y);
+                wave_fence();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tile(r, c_)[(4 * g + i) * LD + j] = -y[i];
+                wave_fence();
+            };
+            solve(1, 0, add(1, 0, 0, zero4()));
+            solve(2, 0, add(2, 1, 0, add(2, 0, 0, zero4())));
+            solve(3, 0, add(3, 2, 0, add(3, 1, 0, add(3, 0, 0, zero4()))));
+            solve(2, 1, add(2, 1, 1, zero4()));
+            solve(3, 1, add(3, 2, 1, add(3, 1, 1, zero4())));
+            solve(3, 2, add(3, 2, 2, zero4()));
+        };
+        {
+            // bf16: every row of K and Q is loaded first, or (BACK) 32 channels ahead
+            Raw<E> ak[KM][NTL], aq[KM][NTL];
+            auto load = [&](int m) {
+#pragma unroll
+                for (int a = 0; a < NTL; ++a) {
+                    ak[m][a] = row(rk, a, m);
+                    aq[m][a] = row(rq, a, m);
+                }
+            };
+            constexpr int AHEAD = NE != 1 ? 0 : BACK ? 1 : KM;
+#pragma unroll
+            for (int m = 0; m < AHEAD && m < KM; ++m) load(m);
+            __builtin_amdgcn_sched_barrier(0);
+            f32x4 kk[NB], kq[NB], qk[NB];                      // of the later token's tile and the key's
+#pragma unroll
+            for (int t = 0; t < NB; ++t) kk[t] = kq[t] = qk[t] = zero4();
+#pragma unroll
+            for (int m = 0; m < KM; ++m) {
+                if (m + AHEAD < KM) load(m + AHEAD);
+                if (NE == 1) __builtin_amdgcn_sched_barrier(0);
+                Terms<NE> k[NTL];
+#pragma unroll
+                for (int a = 0; a < NTL; ++a) k[a] = raw_terms(ak[m][a]);
+#pragma unroll
+                for (int w = 0; w < NTL; ++w) {
+                    const Terms<NE> q = raw_terms(aq[m][w]);
+#pragma unroll
+                    for (int a = 0; a <= w; ++a) {
+                        kk[at(w, a)] = mma(k[a], k[w], kk[at(w, a)]);
+                        kq[at(w, a)] = mma(k[a], q, kq[at(w, a)]);
+                        if (BACK) qk[at(w, a)] = mma(q, k[a], qk[at(w, a)]);
+                    }
+                }
+            }
+            put_n(kk);
+            // ---- the pairs: P's columns with the later token w's queries, P^T's rows
+            // with the key w, its decays the other way round
+#pragma unroll
+            for (int w = 0; w < NTL; ++w) {
+                const float hi = sh[16 * w + j], lo = sl[16 * w + j];
+                f32x4 P[NTL];
+#pragma unroll
+                for (int a = 0; a < NTL; ++a) {
+                    P[a] = zero4();
+                    if (a > w) continue;
+                    const f32x4 kb = *reinterpret_cast<const f32x4*>(&sb[16 * a + 4 * g]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float x = p.scale * __expf((hi - kh[a][i]) + (lo - kl[a][i])) * kb[i] * kq[at(w, a)][i];
+                        P[a][i] = a < w || j - 4 * g - i >= 0 ? x : 0.f;
+                    }
+                }
 #pragma unroll
                 for (int half = 0; half <= w / 2; ++half) {
                     const Terms<NP> f = split_terms<NP>(P[2 * half], P[2 * half + 1]);
@@ -140,104 +224,95 @@ __global__ __launch_bounds__(256, 2) void delta_pairs_kernel(DeltaPairs p) {
                     for (int s = 0; s < NP; ++s)
                         reinterpret_cast<bf16x8*>(blk + Blk::pair + (lower(w, half) * NP + s) * kFragBytes)[lane] = f.t[s];
                 }
-            } else if constexpr (BACK) {
+            }
+            if constexpr (BACK) {
 #pragma unroll
-                for (int a = 0; a < NTL; ++a) P[a] = zero4();
+                for (int w = 0; w < NTL; ++w) {
+                    const float hi = sh[16 * w + j], lo = sl[16 * w + j];
+                    f32x4 P[NTL];
 #pragma unroll
-                for (int a = w; a < NTL; ++a) {
-                    f32x4 qk = zero4();                        // rows: queries of tile a, column: key of tile w
+                    for (int a = 0; a < NTL; ++a) {
+                        P[a] = zero4();
+                        if (a < w) continue;
 #pragma unroll
-                    for (int m = 0; m < KM; ++m) qk = mma(raw_terms(row(rq, a, m)), k[w][m], qk);
+                        for (int i = 0; i < 4; ++i) {
+                            const float x = p.scale * __expf((kh[a][i] - hi) + (kl[a][i] - lo)) * qk[at(a, w)][i];
+                            P[a][i] = a > w || 4 * g + i - j >= 0 ? x : 0.f;
+                        }
+                    }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int d = 16 * (a - w) + 4 * g + i - j;
-                        P[a][i] = d >= 0 ? p.scale * __expf((kh[a][i] - hi) + (kl[a][i] - lo)) * qk[i] : 0.f;
+                    for (int half = w / 2; half < 2; ++half) {
+                        const Terms<3> f = split_terms<3>(P[2 * half], P[2 * half + 1]);
+#pragma unroll
+                        for (int s = 0; s < 3; ++s)
+                            reinterpret_cast<bf16x8*>(blk + Blk::pairt + (upper(w, half) * 3 + s) * kFragBytes)[lane] = f.t[s];
                     }
                 }
-#pragma unroll
-                for (int half = w / 2; half < 2; ++half) {
-                    const Terms<3> f = split_terms<3>(P[2 * half], P[2 * half + 1]);
-#pragma unroll
-                    for (int s = 0; s < 3; ++s)
-                        reinterpret_cast<bf16x8*>(blk + Blk::pairt + (upper(w, half) * 3 + s) * kFragBytes)[lane] = f.t[s];
-                }
             }
         }
         wave_fence();
-        // ---- the tiles on the diagonal, one to 16 lanes: x = 1 - A x below it, with
-        // A = N diag(beta), or diag(beta) N
-        {
-            float* M = N + (g * (g + 1) / 2 + g) * kTileSize;
-            float x[16], y[16];                                // y: what later rows take of x
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                float acc = 0.f;
-                f32x4 a[4];
-                if (r % 4 == 0) __builtin_amdgcn_sched_barrier(0);   // else all rows are read first: 144 registers
-#pragma unroll
-                for (int q = 0; q < (r + 3) / 4; ++q) a[q] = *reinterpret_cast<const f32x4*>(M + r * LD + 4 * q);
-                const float br = sb[16 * g + r];
-#pragma unroll
-                for (int q = 0; q < r; ++q) acc += a[q / 4][q % 4] * y[q];
-                x[r] = (r == j ? 1.f : 0.f) - (other ? br * acc : acc);
-                y[r] = other ? x[r] : br * x[r];
-            }
-            wave_fence();
-#pragma unroll
-            for (int r = 0; r < 16; ++r) M[r * LD + j] = x[r];
-        }
-        wave_fence();
-        // ---- those below, column by column: an accumulator is the next product's
-        // operand as it is (rows 4 g + s for both)
-        auto add = [&](int r, int q, int c_, f32x4 acc) {      // A_rq T_qc
-            const f32x4 a = *reinterpret_cast<const f32x4*>(tile(r, q) + j * LD + 4 * g);
-            const float* t = tile(q, c_) + 4 * g * LD + j;
-#pragma unroll
-            for (int s = 0; s < 4; ++s) acc = mma_f32_k4(a[s], other ? t[s * LD] : t[s * LD] * kb[q][s], acc);
-            return acc;
-        };
-        auto solve = [&](int r, int c_, f32x4 x) {             // T_rc = -T_rr x, in N_rc's place
-            if (other) x *= kb[r];
-            const f32x4 a = *reinterpret_cast<const f32x4*>(tile(r, r) + j * LD + 4 * g);
-            f32x4 y = zero4();
-#pragma unroll
-            for (int s = 0; s < 4; ++s) y = mma_f32_k4(a[s], x[s], y);
-            wave_fence();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tile(r, c_)[(4 * g + i) * LD + j] = -y[i];
-            wave_fence();
-        };
-        solve(1, 0, add(1, 0, 0, zero4()));
-        solve(2, 0, add(2, 1, 0, add(2, 0, 0, zero4())));
-        solve(3, 0, add(3, 2, 0, add(3, 1, 0, add(3, 0, 0, zero4()))));
-        solve(2, 1, add(2, 1, 1, zero4()));
-        solve(3, 1, add(3, 2, 1, add(3, 1, 1, zero4())));
-        solve(3, 2, add(3, 2, 2, zero4()));
-        // ---- out: rows of the inverse, or columns of the other one
+        invert();
 #pragma unroll
         for (int w = 0; w < NTL; ++w)
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                f32x4 lo = zero4(), hi = zero4();
-                int to;
-                if (!other) {
-                    if (half > w / 2) continue;
-                    lo = *reinterpret_cast<const f32x4*>(tile(w, 2 * half) + j * LD + 4 * g);
-                    if (2 * half + 1 <= w) hi = *reinterpret_cast<const f32x4*>(tile(w, 2 * half + 1) + j * LD + 4 * g);
-                    to = Blk::inv + lower(w, half) * 3 * kFragBytes;
-                } else {
-                    if (half < w / 2) continue;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (2 * half >= w) lo[i] = tile(2 * half, w)[(4 * g + i) * LD + j];
-                        hi[i] = tile(2 * half + 1, w)[(4 * g + i) * LD + j];
-                    }
-                    to = Blk::invt + upper(w, half) * 3 * kFragBytes;
-                }
+            for (int half = 0; half <= w / 2; ++half) {
+                f32x4 lo = *reinterpret_cast<const f32x4*>(tile(w, 2 * half) + j * LD + 4 * g), hi = zero4();
+                if (2 * half + 1 <= w) hi = *reinterpret_cast<const f32x4*>(tile(w, 2 * half + 1) + j * LD + 4 * g);
                 const Terms<3> f = split_terms<3>(lo, hi);
 #pragma unroll
-                for (int s = 0; s < 3; ++s) reinterpret_cast<bf16x8*>(blk + to + s * kFragBytes)[lane] = f.t[s];
+                for (int s = 0; s < 3; ++s)
+                    reinterpret_cast<bf16x8*>(blk + Blk::inv + (lower(w, half) * 3 + s) * kFragBytes)[lane] = f.t[s];
             }
+        // ---- the gradients' ((I + diag(beta) N)^{-1})^T: its element (t, r) is T_rt
+        // beta_r / beta_t, whatever the strengths, for T_rt has beta_t as a factor.
+        // Where one is (next to) zero the quotient is taken at 2^-60 instead, which
+        // changes the others by less than a rounding.
+        if constexpr (BACK) {
+            const float least = 0x1p-60f;
+            if (__any(lane < rows && fabsf(beta) < least)) {
+                f32x4 kk[NB];
+#pragma unroll
+                for (int t = 0; t < NB; ++t) kk[t] = zero4();
+#pragma unroll
+                for (int m = 0; m < KM; ++m) {
+                    Terms<NE> k[NTL];
+#pragma unroll
+                    for (int a = 0; a < NTL; ++a) k[a] = raw_terms(row(rk, a, m));
+#pragma unroll
+                    for (int w = 0; w < NTL; ++w)
+#pragma unroll
+                        for (int a = 0; a <= w; ++a) kk[at(w, a)] = mma(k[a], k[w], kk[at(w, a)]);
+                }
+                wave_fence();
+                put_n(kk);
+                sb[lane] = fabsf(beta) < least ? copysignf(least, beta) : beta;
+                wave_fence();
+                invert();
+            }
+#pragma unroll
+            for (int w = 0; w < NTL; ++w) {
+                const float own = sb[16 * w + j], over = own != 0.f ? 1.0f / own : 0.f;
+#pragma unroll
+                for (int half = w / 2; half < 2; ++half) {
+                    f32x4 x[2] = {zero4(), zero4()};
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const int r = 2 * half + y;
+                        if (r < w) continue;
+                        const f32x4 kb = *reinterpret_cast<const f32x4*>(&sb[16 * r + 4 * g]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float t = tile(r, w)[(4 * g + i) * LD + j];
+                            x[y][i] = r == w && 4 * g + i == j ? 1.0f : t * over * kb[i];
+                        }
+                    }
+                    const Terms<3> f = split_terms<3>(x[0], x[1]);
+#pragma unroll
+                    for (int s = 0; s < 3; ++s)
+                        reinterpret_cast<bf16x8*>(blk + Blk::invt + (upper(w, half) * 3 + s) * kFragBytes)[lane] = f.t[s];
+                }
+            }
+        }
         wave_fence();
     }
 }
@@ -248,7 +323,7 @@ size_t delta_block_bytes(bool is_bf16, bool back) {
 
 template <typename E, int NP, bool BACK>
 static hipError_t launch_e(const DeltaPairs& a, hipStream_t stream) {
-    const long long all = ((long long)a.B * (a.c1 - a.c0) * a.H * (BACK ? 2 : 1) + 3) / 4;
+    const long long all = ((long long)a.B * (a.c1 - a.c0) * a.H + 3) / 4;
     const dim3 grid((unsigned)std::min(all, kPairGroups)), block(256);
     switch (a.dk) {
         case 32: hipLaunchKernelGGL((delta_pairs_kernel<E, 32, NP, BACK>), grid, block, 0, stream, a); break;
