@@ -7,8 +7,8 @@ import torch
 
 from linear_ref import HALF, MIN_G, _share, f64, lengths
 
-#: Tokens over which a state enters an output as a sum over tokens (at most): the prefill's
-#: chunks have 32, the gradients' 64.  A longer span only makes the magnitude larger.
+#: Tokens over which a state enters an output as a sum over tokens: a chunk of the prefill and of
+#: the gradients.
 SPAN = 64
 
 
