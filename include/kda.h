@@ -590,10 +590,12 @@ kda_status kda_qk_norm_rope_backward(const void *q, const void *k, const float *
  *   finite number ((0, 1) is usual; keys of length 1 keep the recurrence stable
  *   up to 2).
  * - B * H <= 2^19, and H times the larger head size <= 2^22.
- * - With bf16, an output's o, dq and dk take the state, the pairs' weights and
- *   what each token writes as one bf16 term on their way into the output; the
- *   states, dg, dbeta and dS0, and dv before its own rounding, are fp32
- *   throughout. */
+ * - With bf16, o takes the state and what each token writes as two bf16 terms
+ *   and the pairs' weights as one on their way into it, dq and dk the states and
+ *   their gradients as one and the others as two (off by 1.9e-3 to 2.3e-3 of the
+ *   norm, of which each output's own rounding is 1.7e-3); the states, dg, dbeta
+ *   and dS0, and dv before its own rounding, are fp32 throughout.  With fp32
+ *   everything is (3e-7 to 6e-7 of the norm). */
 
 /* Bytes of device workspace kda_delta_prefill and kda_delta_prefill_paged need
  * for these sizes (0: none; also 0 for arguments they would reject). */
