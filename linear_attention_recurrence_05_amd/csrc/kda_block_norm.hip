@@ -15,7 +15,8 @@
 // weights, twice a bf16 row's bytes each, in registers throughout: 4,096 bf16 rows
 // of 7,168 with norm, gate and weights take 54 us, 5.4 TB/s (85 us with one row of
 // a workgroup after the other and the weights read for each), the gradients of
-// 2,002 rows of 4,096 take 38.5 us (57.5 us).
+// 2,002 rows of 4,096 take 38.5 us (57.5 us), of 8,192 rows of 512 24 us (30 us with
+// a partial weight gradient for each row of a workgroup).
 #include <algorithm>
 
 #include "kda_delta.hpp"
@@ -23,9 +24,8 @@
 
 namespace kda {
 
-// Waves of a launch at most, about as many as a device holds: more rows loop.  Each
-// row slot of the gradients' workgroups leaves partial weight gradients.
-constexpr int kBlockWaves = 4096, kBlockBwdWaves = 2048;
+// Waves of a launch at most, about as many as a device holds: more rows loop.
+constexpr int kBlockWaves = 4096;
 
 // Sums over a row's TPR threads, the same in all of them.  With more than one
 // wave, a call uses buffer `at` of LDS, which the call after the next may reuse.
@@ -208,16 +208,38 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void block_norm_kernel(Block
             }
         }
     }
-    if (BWD && part) {
-        float* at = part + ((size_t)blockIdx.x * RPW + slot) * 2 * p.D;
+    if constexpr (BWD) {
+        if (!part) return;
+        float* to = part + (size_t)blockIdx.x * 2 * p.D;
+        if constexpr (RPW > 1) {                             // of the workgroup's rows, in order
+            constexpr int W = TPR * NV * VE;                 // >= D
+            __shared__ __align__(16) float s_dw[RPW][2][W];
 #pragma unroll
-        for (int v = 0; v < (BWD ? NV : 1); ++v) {
-            if (!has(v)) continue;
+            for (int v = 0; v < NV; ++v)
 #pragma unroll
-            for (int i = 0; i < VE; i += 4) {
-                const size_t e = (size_t)(v * TPR + t) * VE + i;
-                *reinterpret_cast<f32x4*>(at + e) = *reinterpret_cast<const f32x4*>(&dwy[v][i]);
-                *reinterpret_cast<f32x4*>(at + p.D + e) = *reinterpret_cast<const f32x4*>(&dwn[v][i]);
+                for (int i = 0; i < VE; i += 4) {
+                    const int e = (v * TPR + t) * VE + i;
+                    *reinterpret_cast<f32x4*>(&s_dw[slot][0][e]) = *reinterpret_cast<const f32x4*>(&dwy[v][i]);
+                    *reinterpret_cast<f32x4*>(&s_dw[slot][1][e]) = *reinterpret_cast<const f32x4*>(&dwn[v][i]);
+                }
+            __syncthreads();
+            for (int e = threadIdx.x; e < 2 * p.D; e += NT) {
+                const int of = e >= p.D, col = e - of * p.D;
+                float x = s_dw[0][of][col];
+#pragma unroll
+                for (int r = 1; r < RPW; ++r) x += s_dw[r][of][col];
+                to[e] = x;
+            }
+        } else {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                if (!has(v)) continue;
+#pragma unroll
+                for (int i = 0; i < VE; i += 4) {
+                    const size_t e = (size_t)(v * TPR + t) * VE + i;
+                    *reinterpret_cast<f32x4*>(to + e) = *reinterpret_cast<const f32x4*>(&dwy[v][i]);
+                    *reinterpret_cast<f32x4*>(to + p.D + e) = *reinterpret_cast<const f32x4*>(&dwn[v][i]);
+                }
             }
         }
     }
@@ -233,13 +255,16 @@ static int block_groups(long long rows, int tpr, int most_waves) {
     const int rpw = tpr < 256 ? 256 / tpr : 1, waves = std::max(tpr, 256) / kWave;
     return (int)std::min<long long>((rows + rpw - 1) / rpw, most_waves / waves);
 }
-static int block_slots(long long rows, int tpr) {   // partial weight gradients
-    return block_groups(rows, tpr, kBlockBwdWaves) * (tpr < 256 ? 256 / tpr : 1);
+// Of the gradients as many as a device holds with one piece a thread (120 registers),
+// half as many with two (228); each leaves partial weight gradients.
+static int block_bwd_groups(long long rows, int D, bool is_bf16) {
+    const int tpr = block_threads(D, is_bf16);
+    return block_groups(rows, tpr, D / (is_bf16 ? 8 : 4) <= tpr ? kBlockWaves : kBlockWaves / 2);
 }
 
 template <typename E, bool BWD, int TPR, int NV>
 static hipError_t launch_v(const BlockNorm& a, float* part, hipStream_t stream) {
-    const dim3 grid((unsigned)block_groups(a.rows, TPR, BWD ? kBlockBwdWaves : kBlockWaves)), block(TPR < 256 ? 256 : TPR);
+    const dim3 grid((unsigned)(BWD ? block_bwd_groups(a.rows, a.D, a.is_bf16) : block_groups(a.rows, TPR, kBlockWaves))), block(TPR < 256 ? 256 : TPR);
     hipLaunchKernelGGL((block_norm_kernel<E, TPR, NV, BWD>), grid, block, 0, stream, a, part);
     return hipGetLastError();
 }
@@ -264,7 +289,7 @@ hipError_t launch_block_norm(const BlockNorm& a, hipStream_t stream) {
 }
 
 size_t block_norm_backward_ws_bytes(long long rows, int D, bool is_bf16) {
-    return (size_t)block_slots(rows, block_threads(D, is_bf16)) * 2 * D * sizeof(float);
+    return (size_t)block_bwd_groups(rows, D, is_bf16) * 2 * D * sizeof(float);
 }
 
 hipError_t launch_block_norm_backward(const BlockNorm& a, void* ws, hipStream_t stream) {
@@ -272,7 +297,7 @@ hipError_t launch_block_norm_backward(const BlockNorm& a, void* ws, hipStream_t 
     const hipError_t e = a.is_bf16 ? launch_e<bf16, true>(a, part, stream) : launch_e<float, true>(a, part, stream);
     if (e != hipSuccess || !part) return e;
     hipLaunchKernelGGL(sum_parts_kernel, dim3((2 * a.D + 63) / 64), dim3(1024), 0, stream, part,
-                       block_slots(a.rows, block_threads(a.D, a.is_bf16)), 2 * a.D, a.D, a.dw_y, a.dw_n);
+                       block_bwd_groups(a.rows, a.D, a.is_bf16), 2 * a.D, a.D, a.dw_y, a.dw_n);
     return hipGetLastError();
 }
 
