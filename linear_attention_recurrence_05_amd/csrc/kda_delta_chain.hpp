@@ -7,7 +7,9 @@
 
 namespace kda {
 
-// Chunks from one anchor <S, Y> of dg (kda_delta_backward.hip) to the next.
+// Chunks from one anchor <S, Y> of dg (kda_delta_backward.hip) to the next.  Twice as
+// many cost dg a quarter of its accuracy (fp32 B3 T333: 6.5e-7 of the norm against
+// 4.8e-7) for 8 us of 560 (B1 H32 T4096 bf16).
 constexpr int kAnchorChunks = 4;
 
 // What the gradients' sweeps leave in the workspace, for unit u = b H + h, chunk

