@@ -135,12 +135,12 @@ __device__ __forceinline__ void delta_reverse(const DeltaReverse& p, int x, Reve
     for (int c = c_end - 1; c >= 0; --c) {
         const int rows = min(C, n - c * C);
         // ---- K Y of the wave's channels; Y itself, for dk, and at an anchor <S, Y>
-        buf_store8<E>(make_rsrc((E*)sw.Y + (((size_t)unit * sw.NC + c) * p.dv + 16 * tile) * DK, 16 * DK * ES),
+        buf_stream8<E>(make_rsrc((E*)sw.Y + (((size_t)unit * sw.NC + c) * p.dv + 16 * tile) * DK, 16 * DK * ES),
                       holds ? (j * DK + 32 * w + 8 * g) * ES : kOffPast, Y[0], Y[1]);
         const Rsrc ta = make_rsrc((f32x4*)sw.anchor + anchor_at(c) * 2 * kWave, 2 * kWave * 16);
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-            buf_store_u32x4(ta, is_anchor(c) ? (t * kWave + lane) * 16 : kOffPast, __builtin_bit_cast(u32x4, Y[t]));
+            buf_stream_u32x4(ta, is_anchor(c) ? (t * kWave + lane) * 16 : kOffPast, __builtin_bit_cast(u32x4, Y[t]));
         if (holds) {
             const Terms<3> yf = split_terms<3>(Y[0], Y[1]);
 #pragma unroll
@@ -182,7 +182,7 @@ __device__ __forceinline__ void delta_reverse(const DeltaReverse& p, int x, Reve
         // ---- out: Z; dv = beta Z; dv . v
         {
             const Rsrc tz = make_rsrc(sw.z + (((size_t)unit * sw.NC + c) * p.dv + 16 * tile) * C, 16 * C * 4);
-            buf_store_u32x4(tz, (j * C + 16 * w + 4 * g) * 4, __builtin_bit_cast(u32x4, z));
+            buf_stream_u32x4(tz, (j * C + 16 * w + 4 * g) * 4, __builtin_bit_cast(u32x4, z));
             const f32x4 r = beta_j * zt;
             float x = 0.f;
 #pragma unroll

@@ -172,7 +172,7 @@ __device__ __forceinline__ void delta_chain(const DeltaChain& p, int x, ChainLds
         // ---- K S of the wave's channels, and the channels' terms of S
         if constexpr (BACK) {
             const Rsrc to = make_rsrc((E*)sw.S + (((size_t)unit * sw.NC + c) * p.dv + 16 * tile) * DK, 16 * DK * ES);
-            buf_store8<E>(to, holds ? (j * DK + 32 * w + 8 * g) * ES : kOffPast, M[0], M[1]);
+            buf_stream8<E>(to, holds ? (j * DK + 32 * w + 8 * g) * ES : kOffPast, M[0], M[1]);
         }
         if (holds) {
             const Terms<3> sf = split_terms<3>(M[0], M[1]);
@@ -209,7 +209,7 @@ __device__ __forceinline__ void delta_chain(const DeltaChain& p, int x, ChainLds
         put_half<NO>(s.e[w >> 1], w & 1, e);
         if constexpr (BACK) {
             const Rsrc to = make_rsrc(sw.e + (((size_t)unit * sw.NC + c) * p.dv + 16 * tile) * C, 16 * C * 4);
-            buf_store_u32x4(to, (j * C + 16 * w + 4 * g) * 4, __builtin_bit_cast(u32x4, e));
+            buf_stream_u32x4(to, (j * C + 16 * w + 4 * g) * 4, __builtin_bit_cast(u32x4, e));
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) e[i] *= write[i];
@@ -245,7 +245,7 @@ __device__ __forceinline__ void delta_chain(const DeltaChain& p, int x, ChainLds
                                       2 * kWave * 16);
 #pragma unroll
             for (int t = 0; t < 2; ++t)
-                buf_store_u32x4(tm, anchor ? (t * kWave + lane) * 16 : kOffPast, __builtin_bit_cast(u32x4, M[t]));
+                buf_stream_u32x4(tm, anchor ? (t * kWave + lane) * 16 : kOffPast, __builtin_bit_cast(u32x4, M[t]));
         } else {
             const Rsrc to = rows_rsrc((char*)p.o + at_v + (int64_t)(c - p.c0) * C * ldv, rows, ldv, 16 * ES);
             const int off = 16 * w + j < rows ? (16 * w + j) * ldv + 4 * g * ES : kOffPast;
