@@ -13,8 +13,10 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_chain_kerne
 }
 
 // Chunks whose blocks the workspace holds at a time: longer sequences run window
-// by window, the state carried in the workspace.
-constexpr size_t kDeltaWindowBytes = (size_t)192 << 20;
+// by window, the state carried in the workspace.  Half as much, which the last-level
+// cache holds, costs more in launches than it saves: H32 d128 bf16, B4 T4096 461
+// against 490 us, B8 T8192 1,505 against 1,540, B1 T32768 1,166 against 1,196.
+constexpr size_t kDeltaWindowBytes = (size_t)384 << 20;
 
 // From so many heads of bf16 rows on a workgroup takes a whole one
 // (delta_wide_kernel), where fewer leave more than half of the device idle.  d 128,

@@ -38,18 +38,18 @@ def test_prefill_of_many_heads(B, T, H, Hk, dk, lens):
 @pytest.mark.parametrize("paged", [False, True])
 @pytest.mark.parametrize("B,H,dv,dtype", [(4, 24, 32, BF), (16, 8, 128, BF), (4, 24, 32, F32)])
 def test_long_sequences_are_the_pieces_one_after_the_other(B, H, dv, dtype, paged):
-    """A call whose chunks' operands pass 192 MiB goes window by window with the state between them in
+    """A call whose chunks' operands pass 384 MiB goes window by window with the state between them in
     the workspace: the same bits as a call for each window.  One sequence ends within the first
     window, one has no tokens; with pages, one is skipped."""
     need_gpu()
     import linear_attention_recurrence_05_amd as kda
-    chunks, dk = 100, 32
+    chunks, dk = 220, 32
     T = 64 * chunks - 7
     lens = [T, 1000, 0] + [T - 65] * (B - 3)
     x, gen = make(B, T, H, H, dk, dv, dtype, seed=H, lens=lens)
     kw = dict(dtype=torch.int32, device="cuda")
     one = kda.kda_delta_prefill_workspace_bytes(B, 64 * 8, H, H, dk, dv, dtype) // 8     # of a chunk
-    n = -(-chunks // ((192 << 20) // one))
+    n = -(-chunks // ((384 << 20) // one))
     assert n > 1
     step = 64 * -(-chunks // n)
     S, os = x["S0"], []
