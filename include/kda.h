@@ -595,7 +595,12 @@ kda_status kda_qk_norm_rope_backward(const void *q, const void *k, const float *
  *   their gradients as one and the others as two (off by 1.9e-3 to 2.3e-3 of the
  *   norm, of which each output's own rounding is 1.7e-3); the states, dg, dbeta
  *   and dS0, and dv before its own rounding, are fp32 throughout.  With fp32
- *   everything is (3e-7 to 6e-7 of the norm). */
+ *   everything is (3e-7 to 6e-7 of the norm).
+ * - dg is a sum of fp32 parts over up to 256 tokens, none of which outweighs dg
+ *   itself where decays are strong: off by up to 1e-5 of each head's norm (1e-6
+ *   to 4e-6 is usual), whatever the head's decays.  A token whose decay is far
+ *   stronger than those of the next 256 has the error of theirs beside its own
+ *   small dg; where exp(g) is 0 in fp32, dg is 0. */
 
 /* Bytes of device workspace kda_delta_prefill and kda_delta_prefill_paged need
  * for these sizes (0: none; also 0 for arguments they would reject). */

@@ -9,8 +9,18 @@
 // every decay from token t on scales what the outputs and the final state get out
 // of the state before t, so that
 //   dg_t = sum_{r >= t} (dO_r . o_r - dv_r . v_r) + <S_T, dS_T>
-// which is taken from t to the next anchor, a chunk's end at which <S, Y> is
-// formed anew: a sum over the whole sequence would carry its rounding along.
+// In each summand o holds p_r beta_r v_r of the token's own write (p = scale q . k)
+// and dv holds beta_r p_r dO_r of its own output.  These cancel, and behind a strong
+// decay they are all there is: left in, they cost dg its digits (8e-6 of its norm for a
+// head of decays e^-3, all of it for one of e^-15).  Without them a summand is
+//   dO_r . (o'_r - beta_r p_r s_r) - beta_r y_r . v_r
+// where o', s = S^T k and y = Y^T k are what the decayed state before r gives to the
+// output and to the key, and the gradient behind r to the key: the first part is the
+// forward sweep's, the second the reverse one's, and each has the decay of its token,
+// or of the next, as a factor.  The sum is taken from t to the next anchor, a chunk's
+// end at which <S, Y> is formed anew, for over a whole sequence it would carry its
+// rounding along; there S is (I - beta k k^T) times the decayed state before the last
+// token, whose y . v is left out, so that the anchor has its decay as a factor too.
 // The rest needs no chain and takes 64 tokens at a time, from the states and
 // gradients that the two sweeps left:
 //   dq = e^G dO S^T + ((dO U^T) * D) K
@@ -40,14 +50,17 @@ struct DeltaReverse {
 //   K Y of the wave's channels for all tokens                                    |
 //   dU of the wave's tokens, e^G dO                                              |
 //   Z = the inverse's transpose times dU of the wave's tokens, -e^G beta Z; and Z
-//   with a token a lane for what leaves the kernel                               |
+//   with a token a lane for dv                                                   |
 //   Y's update from all tokens
+// P and the inverse come without their diagonal, so that y = Z - p dO, what later
+// tokens alone give, is there before it is added.
 template <typename E, int DK>
 struct ReverseLds {
     static constexpr int C = kDeltaChunk, KM = DK / 32, NE = sizeof(E) == 2 ? 1 : 3;
     static constexpr int LK = NE == 1 ? 40 : 32, LV = 24;    // padded rows
     __align__(16) bf16 k[KM][NE][C * LK], q[KM][NE][C * LK]; // a wave's own channels
     __align__(16) bf16 o[NE][C * LV];                        // dO's tile
+    __align__(16) bf16 v[4][NE][16 * LV];                    // a wave's own tokens of V
     f32x4 part[KM][kDeltaTiles][kWave];
     __align__(16) char d[2][3 * kFragBytes], gq[2][3 * kFragBytes], gr[2][3 * kFragBytes];
 };
@@ -86,8 +99,8 @@ __device__ __forceinline__ void delta_reverse(const DeltaReverse& p, int x, Reve
     };
     auto blk_rsrc = [&](int c) { return make_rsrc(pb + (int64_t)max(c, 0) * Blk::bytes, c >= 0 ? Blk::bytes : 0); };
     Raw<E> rk[kDeltaTiles], rq[kDeltaTiles];
-    u32x4 ro;
-    f32x4 v, grow, end, beta;
+    u32x4 ro, rv;
+    f32x4 grow, end, beta, self;
     Terms<3> rt[2], rp[2];
     float beta_j, decay_f, decay_rest;
     auto load_rows = [&](int c) {                            // K, Q and dO
@@ -103,7 +116,7 @@ __device__ __forceinline__ void delta_reverse(const DeltaReverse& p, int x, Reve
         ro = buf_load<u32x4>(rows_rsrc(sw.dO, at_v, c, rows, ldv, 16 * ES),
                              lane < 16 * ES && row < rows ? row * ldv + lane % ES * 16 : kOffPast);
     };
-    auto is_anchor = [&](int c) { return holds && (c % kAnchorChunks == kAnchorChunks - 1 || c == c_end - 1); };
+    auto is_anchor = [&](int c) { return c % kAnchorChunks == kAnchorChunks - 1 || c == c_end - 1; };
     auto anchor_at = [&](int c) { return (((size_t)unit * sw.NA + c / kAnchorChunks) * tiles + tile) * KM + (holds ? w : 0); };
     auto load_pair = [&](int c) {
         const Rsrc r = blk_rsrc(c);
@@ -111,19 +124,26 @@ __device__ __forceinline__ void delta_reverse(const DeltaReverse& p, int x, Reve
         for (int x = 0; x < 2; ++x) rp[x] = load_terms<3>(r, x >= w / 2 ? Blk::pairt + upper(w, x) * 3 * kFragBytes : kOffPast);
         grow = __builtin_bit_cast(f32x4, buf_load<u32x4>(r, Blk::row + (kRowGrow + 16 * w + 4 * g) * 4));
         end = __builtin_bit_cast(f32x4, buf_load<u32x4>(r, Blk::row + (kRowEnd + 16 * w + 4 * g) * 4));
+        self = __builtin_bit_cast(f32x4, buf_load<u32x4>(r, Blk::row + (kRowSelf + 16 * w + 4 * g) * 4));
         const f32x4 d = __builtin_bit_cast(f32x4, buf_load<u32x4>(r, Blk::row + kRowDecay * 4));
         decay_f = d[0];
         decay_rest = d[1];
     };
-    auto load_inv = [&](int c) {                             // and what the outputs take: v of token 16 w + j
+    auto load_inv = [&](int c) {                             // and V
         const int rows = rows_of(c);
         const Rsrc r = blk_rsrc(c);
 #pragma unroll
         for (int x = 0; x < 2; ++x) rt[x] = load_terms<3>(r, x >= w / 2 ? Blk::invt + upper(w, x) * 3 * kFragBytes : kOffPast);
         beta = __builtin_bit_cast(f32x4, buf_load<u32x4>(r, Blk::row + (kRowBeta + 16 * w + 4 * g) * 4));
         beta_j = __builtin_bit_cast(float, buf_load<uint32_t>(r, Blk::row + (kRowBeta + 16 * w + j) * 4));
-        v = buf_load4<E>(rows_rsrc(p.v, at_v, c, rows, ldv, 16 * ES), 16 * w + j < rows ? (16 * w + j) * ldv + 4 * g * ES : kOffPast);
+        const int row = 16 * w + lane / ES;
+        rv = buf_load<u32x4>(rows_rsrc(p.v, at_v, c, rows, ldv, 16 * ES),
+                             lane < 16 * ES && row < rows ? row * ldv + lane % ES * 16 : kOffPast);
     };
+    // the wave's tokens of their half of a chunk, as an operand
+    Terms<1> own;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) own.t[0][i] = (bf16)(i == 4 * (w & 1) + (j & 3) && g == j >> 2 ? 1.f : 0.f);
 
     ChunkDecay decay;
     load_rows(c_end - 1);                                    // in the loop's order, as in delta_chain_kernel
@@ -140,7 +160,7 @@ __device__ __forceinline__ void delta_reverse(const DeltaReverse& p, int x, Reve
         const Rsrc ta = make_rsrc((f32x4*)sw.anchor + anchor_at(c) * 2 * kWave, 2 * kWave * 16);
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-            buf_stream_u32x4(ta, is_anchor(c) ? (t * kWave + lane) * 16 : kOffPast, __builtin_bit_cast(u32x4, Y[t]));
+            buf_stream_u32x4(ta, holds && is_anchor(c) ? (t * kWave + lane) * 16 : kOffPast, __builtin_bit_cast(u32x4, Y[t]));
         if (holds) {
             const Terms<3> yf = split_terms<3>(Y[0], Y[1]);
 #pragma unroll
@@ -164,33 +184,39 @@ __device__ __forceinline__ void delta_reverse(const DeltaReverse& p, int x, Reve
         u *= end;
         if (w < 2) u = mma(rp[0], col_terms<NE>(&s.o[0][0], C * LV, LV, 0, 4, j, g), u);
         u = mma(rp[1], col_terms<NE>(&s.o[0][32 * LV], C * LV, LV, 0, 4, j, g), u);
-        put_half<3>(s.d[w >> 1], w & 1, u);
-        put_half<3>(s.gq[w >> 1], w & 1, p.scale * grow * col4<NE>(&s.o[0][16 * w * LV], C * LV, LV, j, g));
+        const f32x4 dO = col4<NE>(&s.o[0][16 * w * LV], C * LV, LV, j, g), pdO = self * dO;
+        put_half<3>(s.d[w >> 1], w & 1, u + pdO);
+        put_half<3>(s.gq[w >> 1], w & 1, p.scale * grow * dO);
         const f32x4 eg = grow;
         const float f = decay(decay_f, decay_rest);
         load_pair(c - 1);
         __syncthreads();
         // ---- Z of the wave's tokens, a column a lane and (zt) a token a lane
         const Terms<3> d1 = frag_terms<3>(s.d[1]);
-        f32x4 z = mma(rt[1], d1, zero4()), zt = mma(d1, rt[1], zero4());
+        f32x4 y = mma(rt[1], d1, u), zt = mma(d1, rt[1], zero4());
         if (w < 2) {
             const Terms<3> d0 = frag_terms<3>(s.d[0]);
-            z = mma(rt[0], d0, z);
+            y = mma(rt[0], d0, y);
             zt = mma(d0, rt[0], zt);
+            zt = mma(d0, own, zt);
+        } else {
+            zt = mma(d1, own, zt);
         }
+        put_piece<E>(&s.v[w][0][min(lane / ES, 15) * LV + lane % ES * (16 / ES)], 16 * LV, rv, lane < 16 * ES);
+        wave_fence();
+        const f32x4 z = y + pdO;
         put_half<3>(s.gr[w >> 1], w & 1, -eg * (beta * z));
-        // ---- out: Z; dv = beta Z; dv . v
+        // ---- out: Z; dv = beta Z; beta y . v
         {
             const Rsrc tz = make_rsrc(sw.z + (((size_t)unit * sw.NC + c) * p.dv + 16 * tile) * C, 16 * C * 4);
             buf_stream_u32x4(tz, (j * C + 16 * w + 4 * g) * 4, __builtin_bit_cast(u32x4, z));
-            const f32x4 r = beta_j * zt;
-            float x = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x += r[i] * v[i];
-            x += __shfl_xor(x, 16);
-            x += __shfl_xor(x, 32);
+            const f32x4 v = col4<NE>(&s.v[w][0][0], 16 * LV, LV, j, g);
+            float x = row_sums(v * (beta * y), j);           // of token 16 w + 4 g + j % 4
+            if (is_anchor(c) && 16 * w + 4 * g + (j & 3) == rows - 1) x = 0.f;
+            wave_fence();                                    // before the next chunk's v
             buf_store_u32(make_rsrc(sw.dot + (((size_t)(tiles + tile) * units + unit) * sw.NC + c) * C, C * 4),
-                          g == 0 ? (16 * w + j) * 4 : kOffPast, __builtin_bit_cast(uint32_t, x));
+                          j < 4 ? (16 * w + 4 * g + j) * 4 : kOffPast, __builtin_bit_cast(uint32_t, x));
+            const f32x4 r = beta_j * zt;
             const Rsrc to = rows_rsrc(p.dv_out, at_v, c, rows, ldv, 16 * ES);
             const int off = 16 * w + j < rows ? (16 * w + j) * ldv + 4 * g * ES : kOffPast;
             if constexpr (ES == 2)
@@ -561,12 +587,14 @@ __global__ __launch_bounds__(256) void delta_qk_sum_kernel(DeltaQK p) {
 
 // ------------------------------------------------------------------ dg
 
-// One workgroup per (b, h) and anchor: 256 tokens, one a thread, sums in 64 bits.
-__global__ __launch_bounds__(256) void delta_gates_kernel(DeltaSweep sw, const int* __restrict__ lens, float* __restrict__ dg,
-                                                          int B, int T, int H, int tiles, int state) {
+// One workgroup per (b, h) and anchor: 256 tokens, one a thread, sums in 64 bits.  At a
+// token whose decay is zero in fp32 dg is zero, and the sums of tokens before it end.
+__global__ __launch_bounds__(256) void delta_gates_kernel(DeltaSweep sw, const float* __restrict__ g, const int* __restrict__ lens,
+                                                          float* __restrict__ dg, int B, int T, int H, int tiles, int state) {
     constexpr int N = kAnchorChunks * kDeltaChunk;
     static_assert(N == 256, "a token a thread");
     __shared__ double s_x[4], s_a[4];
+    __shared__ int s_end[4];
     const int units = B * H, unit = (int)(blockIdx.x % units), a = (int)(blockIdx.x / units), b = unit / H, h = unit % H;
     const int n = seq_len(lens, b, T), t = a * N + threadIdx.x, lane = lane_id(), wave = wave_id();
     if (a * N >= n) return;
@@ -582,26 +610,37 @@ __global__ __launch_bounds__(256) void delta_gates_kernel(DeltaSweep sw, const i
     }
 #pragma unroll
     for (int o = 1; o < kWave; o <<= 1) dot += __shfl_xor(dot, o);
-    // dO . o - dv . v of the token, and the sum from it to the wave's end
+    // the token's summand, and the sum from it to the wave's end or a zero decay
     double x = 0;
+    int end = 0;
     if (t < n) {
         const size_t plane = (size_t)units * sw.NC * kDeltaChunk;
         const float* at = sw.dot + (size_t)unit * sw.NC * kDeltaChunk + t;
 #pragma unroll 4
         for (int i = 0; i < tiles; ++i) x += (double)at[i * plane] - (double)at[(tiles + i) * plane];
+        end = expf(log_decay(g[((size_t)b * T + t) * H + h])) == 0.f;
+        x = end ? 0.0 : x;
     }
 #pragma unroll
     for (int o = 1; o < kWave; o <<= 1) {
         const double down = __shfl_down(x, o);
-        if (lane + o < kWave) x += down;
+        const int then = __shfl_down(end, o);
+        if (lane + o < kWave && !end) {
+            x += down;
+            end = then;
+        }
     }
     if (lane == 0) {
         s_x[wave] = x;
+        s_end[wave] = end;
         s_a[wave] = dot;
     }
     __syncthreads();
-    x += (s_a[0] + s_a[1]) + (s_a[2] + s_a[3]);
-    for (int i = wave + 1; i < 4; ++i) x += s_x[i];
+    for (int i = wave + 1; i < 4 && !end; ++i) {
+        x += s_x[i];
+        end = s_end[i];
+    }
+    if (!end) x += (s_a[0] + s_a[1]) + (s_a[2] + s_a[3]);
     if (t < n) dg[((size_t)b * T + t) * H + h] = (float)x;
 }
 
@@ -677,7 +716,7 @@ hipError_t launch_delta_backward(const DeltaBackward& a, void* ws, hipStream_t s
                     a.H > a.Hk ? (float*)(w + l.part) : nullptr, a.B, a.T, a.H, a.Hk, a.dk_, a.dv_};
     e = a.is_bf16 ? launch_e<bf16>(a, c, r, x, stream) : launch_e<float>(a, c, r, x, stream);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(delta_gates_kernel, dim3((unsigned)(a.B * a.H * l.NA)), dim3(256), 0, stream, sw, a.lens, a.dg, a.B, a.T, a.H,
+    hipLaunchKernelGGL(delta_gates_kernel, dim3((unsigned)(a.B * a.H * l.NA)), dim3(256), 0, stream, sw, a.g, a.lens, a.dg, a.B, a.T, a.H,
                        a.dv_ / 16, a.dk_ * a.dv_);
     return hipGetLastError();
 }

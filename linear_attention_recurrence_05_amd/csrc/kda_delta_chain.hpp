@@ -17,9 +17,11 @@ constexpr int kAnchorChunks = 4;
 //   e, z  [u][c][dv][64] fp32        e_t of every token, and its gradient Z
 //   S, Y  [u][c][dv][dk] of E        the state before a chunk, and the gradient of
 //                                    the one behind it, transposed
-//   end, anchor  [u][a][t] state tiles   the state at an anchor and its gradient, as
-//                                    the chains hold them
-//   dot   [2][t][u][64 NC] fp32      parts of dO . o, and of dv . v
+//   end, anchor  [u][a][t] state tiles   the state at an anchor, less what its last
+//                                    token wrote of v, and its gradient, as the chains
+//                                    hold them
+//   dot   [2][t][u][64 NC] fp32      parts of dg's summands (kda_delta_backward.hip),
+//                                    the forward sweep's and the reverse one's
 struct DeltaSweep {
     const void* dO;
     float *e, *z;
@@ -56,8 +58,9 @@ hipError_t launch_delta_wide(const DeltaChain& a, hipStream_t stream);
 // issues an instruction in about five cycles whatever it is, and what a chunk
 // costs is their number (64 tokens: about 400) and the barriers.  Registers that a
 // part has used are loaded for the next chunk at once, a chunk ahead.
-// BACK: the gradients' forward sweep, which leaves e, the states and the parts of
-// dO . o, whose sum over the sequence needs o with fp32's accuracy (three terms).
+// BACK: the gradients' forward sweep, which leaves e, the states and its part of dg's
+// summands: of o and K S what older tokens give alone (the block's matrices have no
+// diagonal there), with fp32's accuracy (three terms).
 template <typename E, int DK, bool BACK>
 struct ChainLds {
     static constexpr int C = kDeltaChunk, KM = DK / 32, NE = sizeof(E) == 2 ? 1 : 3;
@@ -70,6 +73,8 @@ struct ChainLds {
     __align__(16) char S[KM][NS * kFragBytes];
     f32x4 part[KM][kDeltaTiles][kWave];
     __align__(16) char r[2][3 * kFragBytes], u[2][3 * kFragBytes], e[2][NO * kFragBytes];
+    __align__(16) bf16 d[BACK ? 4 : 1][NE][16 * LV];         // a wave's own tokens of dO
+    float write[16];                                         // beta v of an anchor's last token
 };
 template <typename E, int DK, bool BACK>
 __device__ __forceinline__ void delta_chain(const DeltaChain& p, int x, ChainLds<E, DK, BACK>& s) {
@@ -114,7 +119,8 @@ __device__ __forceinline__ void delta_chain(const DeltaChain& p, int x, ChainLds
     Terms<NP> rp[2];
     f32x4 grow, write;
     float grow_j, decay_f, decay_rest;
-    f32x4 dO = zero4();
+    u32x4 rd = {0, 0, 0, 0};                                 // BACK: dO, as v
+    f32x4 self = zero4();                                    // beta p of the wave's tokens
     auto load_k = [&](int c) {
         const int rows = rows_of(c);
         const Rsrc r = rows_rsrc(pk + (int64_t)(c - p.c0) * C * ldk, holds ? rows : 0, ldk, DK * ES);
@@ -131,11 +137,10 @@ __device__ __forceinline__ void delta_chain(const DeltaChain& p, int x, ChainLds
         // v's tile of 16 rows of 16 elements: 16 bytes a lane (bf16: half the lanes)
         const Rsrc v = rows_rsrc((const char*)p.v + at_v + (int64_t)(c - p.c0) * C * ldv, rows, ldv, 16 * ES);
         const int row = 16 * w + lane / ES;
-        rv = buf_load<u32x4>(v, lane < 16 * ES && row < rows ? row * ldv + lane % ES * 16 : kOffPast);
-        if constexpr (BACK) {
-            const Rsrc d = rows_rsrc((const char*)p.sweep.dO + at_v + (int64_t)(c - p.c0) * C * ldv, rows, ldv, 16 * ES);
-            dO = buf_load4<E>(d, 16 * w + j < rows ? (16 * w + j) * ldv + 4 * g * ES : kOffPast);
-        }
+        const int at = lane < 16 * ES && row < rows ? row * ldv + lane % ES * 16 : kOffPast;
+        rv = buf_load<u32x4>(v, at);
+        if constexpr (BACK)
+            rd = buf_load<u32x4>(rows_rsrc((const char*)p.sweep.dO + at_v + (int64_t)(c - p.c0) * C * ldv, rows, ldv, 16 * ES), at);
     };
     auto blk_rsrc = [&](int c) { return make_rsrc(pb + (int64_t)(c - p.c0) * Blk::bytes, c < c_end ? Blk::bytes : 0); };
     auto load_inv = [&](int c) {
@@ -143,6 +148,7 @@ __device__ __forceinline__ void delta_chain(const DeltaChain& p, int x, ChainLds
 #pragma unroll
         for (int x = 0; x < 2; ++x) rt[x] = load_terms<3>(r, x <= w / 2 ? Blk::inv + lower(w, x) * 3 * kFragBytes : kOffPast);
         write = __builtin_bit_cast(f32x4, buf_load<u32x4>(r, Blk::row + (kRowWrite + 16 * w + 4 * g) * 4));
+        if constexpr (BACK) self = __builtin_bit_cast(f32x4, buf_load<u32x4>(r, Blk::row + (kRowBetaSelf + 16 * w + 4 * g) * 4));
     };
     auto load_pair = [&](int c) {
         const Rsrc r = blk_rsrc(c);
@@ -187,6 +193,8 @@ __device__ __forceinline__ void delta_chain(const DeltaChain& p, int x, ChainLds
             }
         }
         put_piece<E>(&s.v[w][0][min(lane / ES, 15) * LV + lane % ES * (16 / ES)], 16 * LV, rv, lane < 16 * ES);
+        if constexpr (BACK)
+            put_piece<E>(&s.d[w][0][min(lane / ES, 15) * LV + lane % ES * (16 / ES)], 16 * LV, rd, lane < 16 * ES);
         load_k(c + 1);
         __syncthreads();
         // ---- R of the wave's tokens; Q S
@@ -194,18 +202,36 @@ __device__ __forceinline__ void delta_chain(const DeltaChain& p, int x, ChainLds
 #pragma unroll
         for (int m = 1; m < KM; ++m) R += s.part[m][w][lane];
         const f32x4 v = col4<NE>(&s.v[w][0][0], 16 * LV, LV, j, g);
+        f32x4 ks = zero4(), dO = zero4(), dO_t = zero4();    // BACK: K S, dO of rows 4 g + i, and of token 16 w + j
+        if constexpr (BACK) {
+            ks = grow * R;
+            dO = col4<NE>(&s.d[w][0][0], 16 * LV, LV, j, g);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) R[i] = v[i] - grow[i] * R[i];
+            for (int x = NE - 1; x >= 0; --x) {
+                const bf16x4 t = *reinterpret_cast<const bf16x4*>(&s.d[w][x][j * LV + 4 * g]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) dO_t[i] += (float)t[i];
+            }
+            R = v - ks;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) R[i] = v[i] - grow[i] * R[i];
+        }
         put_half<3>(s.r[w >> 1], w & 1, R);
         f32x4 o = zero4();                                   // rows: columns 4 g + i, column: token 16 w + j
 #pragma unroll
         for (int m = 0; m < KM; ++m) o = mma(frag_terms<NS>(s.S[m]), raw_terms(rq[m]), o);
-        const f32x4 d = dO;
         load_qv(c + 1);
         __syncthreads();
         // ---- E of the wave's tokens
         f32x4 e = mma(rt[0], frag_terms<3>(s.r[0]), zero4());
         if (w >= 2) e = mma(rt[1], frag_terms<3>(s.r[1]), e);
+        float dot = 0.f;
+        if constexpr (BACK) {
+            ks -= e;                                         // all that older tokens give
+            e += R;
+            dot = row_sums(dO * (self * ks), j);             // of token 16 w + 4 g + j % 4
+        }
         put_half<NO>(s.e[w >> 1], w & 1, e);
         if constexpr (BACK) {
             const Rsrc to = make_rsrc(sw.e + (((size_t)unit * sw.NC + c) * p.dv + 16 * tile) * C, 16 * C * 4);
@@ -213,6 +239,15 @@ __device__ __forceinline__ void delta_chain(const DeltaChain& p, int x, ChainLds
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) e[i] *= write[i];
+        const bool anchor = BACK && (c % kAnchorChunks == kAnchorChunks - 1 || c == c_end - 1);
+        if (anchor) {                                        // its last token's v is written behind
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (16 * w + 4 * g + i != rows - 1) continue;
+                e[i] = -write[i] * ks[i];
+                s.write[j] = write[i] * v[i];
+            }
+        }
         put_half<3>(s.u[w >> 1], w & 1, e);
         load_inv(c + 1);
         __syncthreads();
@@ -233,19 +268,30 @@ __device__ __forceinline__ void delta_chain(const DeltaChain& p, int x, ChainLds
         o = mma(frag_terms<NO>(s.e[0]), rp[0], o);
         if (w >= 2) o = mma(frag_terms<NO>(s.e[1]), rp[1], o);
         if constexpr (BACK) {
-            float dot = 0.f;
+            float own = 0.f;                                 // dO . o of token 16 w + j
 #pragma unroll
-            for (int i = 0; i < 4; ++i) dot += d[i] * o[i];
-            dot += __shfl_xor(dot, 16);
-            dot += __shfl_xor(dot, 32);
+            for (int i = 0; i < 4; ++i) own += dO_t[i] * o[i];
+            own += __shfl_xor(own, 16);
+            own += __shfl_xor(own, 32);
+            own -= __shfl(dot, 16 * (j >> 2) + (j & 3));
             const Rsrc to = make_rsrc(sw.dot + (((size_t)tile * units + unit) * sw.NC + c) * C, C * 4);
-            buf_store_u32(to, g == 0 ? (16 * w + j) * 4 : kOffPast, __builtin_bit_cast(uint32_t, dot));
-            const bool anchor = holds && (c % kAnchorChunks == kAnchorChunks - 1 || c == c_end - 1);
-            const Rsrc tm = make_rsrc((f32x4*)sw.end + ((((size_t)unit * sw.NA + c / kAnchorChunks) * tiles + tile) * KM + w) * 2 * kWave,
-                                      2 * kWave * 16);
+            buf_store_u32(to, g == 0 ? (16 * w + j) * 4 : kOffPast, __builtin_bit_cast(uint32_t, own));
+            if (anchor && holds) {
+                const Rsrc tm = make_rsrc((f32x4*)sw.end + ((((size_t)unit * sw.NA + c / kAnchorChunks) * tiles + tile) * KM + w) * 2 * kWave,
+                                          2 * kWave * 16);
+                f32x4 k[2] = {zero4(), zero4()};             // the last token's key
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-                buf_stream_u32x4(tm, anchor ? (t * kWave + lane) * 16 : kOffPast, __builtin_bit_cast(u32x4, M[t]));
+                for (int x = NE - 1; x >= 0; --x) {
+                    const bf16x8 kx = *reinterpret_cast<const bf16x8*>(&s.k[w][x][(rows - 1) * LK + 8 * g]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) k[i / 4][i % 4] += (float)kx[i];
+                }
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    buf_stream_u32x4(tm, (t * kWave + lane) * 16, __builtin_bit_cast(u32x4, M[t]));
+                    M[t] += s.write[j] * k[t];
+                }
+            }
         } else {
             const Rsrc to = rows_rsrc((char*)p.o + at_v + (int64_t)(c - p.c0) * C * ldv, rows, ldv, 16 * ES);
             const int off = 16 * w + j < rows ? (16 * w + j) * ldv + 4 * g * ES : kOffPast;

@@ -31,18 +31,23 @@ constexpr int kDeltaChunk = 64, kDeltaTiles = kDeltaChunk / 16;
 //   row   [64] e^{G_i}, [64] e^{G_C - G_j} beta_j, [64] e^{G_C - G_j}, [64] beta_j,
 //         then e^{G_C} as a factor and what its rounding left out, relative to it
 // and, for the gradients (BACK),
+//   row   from [272] on p_i = scale q_i . k_i, from [336] on beta_i p_i
 //   invt  upper, 3 terms   rows of ((I + diag(beta) N)^{-1})^T
 //   pairt upper, 3 terms   rows (keys) of scale ((Q K^T) * D)^T
+// all four of them without their diagonal (1, p_i beta_i, 1 and p_i), which the
+// chains add: what a token takes from older tokens and later ones stays apart from
+// what it has of itself, as dg needs it (kda_delta_backward.hip).
 constexpr int kFragBytes = 1024;
 __host__ __device__ constexpr int lower(int tile, int half) { return tile < 2 ? tile : 2 * tile - 2 + half; }
 __host__ __device__ constexpr int upper(int tile, int half) { return tile < 2 ? 2 * tile + half : 2 + tile; }
 template <int NP, bool BACK>
 struct DeltaBlock {
     static constexpr int inv = 0, pair = inv + 18 * kFragBytes, row = pair + 6 * NP * kFragBytes;
-    static constexpr int invt = row + 1088, pairt = invt + 18 * kFragBytes;
+    static constexpr int invt = row + (BACK ? 1600 : 1088), pairt = invt + 18 * kFragBytes;
     static constexpr int bytes = BACK ? pairt + 18 * kFragBytes : invt;
 };
-enum DeltaRow { kRowGrow = 0, kRowWrite = 64, kRowEnd = 128, kRowBeta = 192, kRowDecay = 256 };   // floats from `row`
+enum DeltaRow { kRowGrow = 0, kRowWrite = 64, kRowEnd = 128, kRowBeta = 192, kRowDecay = 256,   // floats from `row`
+                kRowSelf = 272, kRowBetaSelf = 336 };
 
 // Chunks c0 .. c1 - 1 of every sequence, block ((b H + h) (c1 - c0) + c - c0).
 struct DeltaPairs {
@@ -187,6 +192,12 @@ __device__ __forceinline__ void store8(float* p, f32x4 lo, f32x4 hi) {
     reinterpret_cast<f32x4*>(p)[1] = hi;
 }
 
+// LDS of one wave: its writes are there for its reads.
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // An offset past any buffer's end, also some KB further: such loads give zeros and
 // such stores are dropped.
 constexpr int kOffPast = -(1 << 16);
@@ -232,6 +243,10 @@ __device__ __forceinline__ Terms<N> load_terms(Rsrc r, int off) {
     for (int i = 0; i < N; ++i) out.t[i] = __builtin_bit_cast(bf16x8, buf_load<u32x4>(r, off + i * kFragBytes + lane_id() * 16));
     return out;
 }
+template <int CTRL>
+__device__ __forceinline__ float dpp_move(float x) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xF, 0xF, false));
+}
 // A tile of 16 x 16 (rows 4 g + i of column j, an accumulator's layout) as N terms
 // to its half of an operand in LDS: half 0 is tokens 4 g .., half 1 16 + 4 g ..
 template <int N>
@@ -245,6 +260,17 @@ __device__ __forceinline__ void put_half(char* frag, int half, f32x4 x) {
         *reinterpret_cast<u32x2*>(frag + s * kFragBytes + lane_id() * 16 + half * 8) = w;
         x = f32x4{a[0], a[1], a[2], a[3]};
     }
+}
+// The sums of x over the 16 lanes of a group, of x[i] in the lanes whose j % 4 is i:
+// an accumulator's rows summed over its columns.
+__device__ __forceinline__ float row_sums(f32x4 x, int j) {
+    constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kRor4 = 0x124, kRor8 = 0x128;   // DPP controls
+    const bool odd = j & 1, high = j & 2;
+    const float a = (odd ? x[1] : x[0]) + dpp_move<kXor1>(odd ? x[0] : x[1]);
+    const float b = (odd ? x[3] : x[2]) + dpp_move<kXor1>(odd ? x[2] : x[3]);
+    float c = (high ? b : a) + dpp_move<kXor2>(high ? a : b);
+    c += dpp_move<kRor4>(c);
+    return c + dpp_move<kRor8>(c);
 }
 // Column step (j / 4) + j % 4 of rows 4 g .. 4 g + 3 of a [16][ld] tile kept as N
 // bf16 planes in LDS.

@@ -30,12 +30,6 @@ __device__ __forceinline__ double wave_scan(double x) {
     return x;
 }
 
-// LDS of one wave: its writes are there for its reads.
-__device__ __forceinline__ void wave_fence() {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
-
 template <typename E, int DK, int NP, bool BACK>
 __global__ __launch_bounds__(256, 2) void delta_pairs_kernel(DeltaPairs p) {
     using Blk = DeltaBlock<NP, BACK>;
@@ -214,7 +208,17 @@ __global__ __launch_bounds__(256, 2) void delta_pairs_kernel(DeltaPairs p) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float x = p.scale * __expf((hi - kh[a][i]) + (lo - kl[a][i])) * kb[i] * kq[at(w, a)][i];
-                        P[a][i] = a < w || j - 4 * g - i >= 0 ? x : 0.f;
+                        P[a][i] = a < w || j - 4 * g - i >= (BACK ? 1 : 0) ? x : 0.f;
+                    }
+                }
+                if constexpr (BACK) {                          // the diagonal, by the lane that has its element
+                    float self = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) self = 4 * g + i == j ? p.scale * kq[at(w, w)][i] : self;
+                    float* out = reinterpret_cast<float*>(blk + Blk::row) + 16 * w + j;
+                    if (g == j >> 2) {
+                        out[kRowSelf] = self;
+                        out[kRowBetaSelf] = self * sb[16 * w + j];
                     }
                 }
 #pragma unroll
@@ -237,7 +241,7 @@ __global__ __launch_bounds__(256, 2) void delta_pairs_kernel(DeltaPairs p) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const float x = p.scale * __expf((kh[a][i] - hi) + (kl[a][i] - lo)) * qk[at(a, w)][i];
-                            P[a][i] = a > w || 4 * g + i - j >= 0 ? x : 0.f;
+                            P[a][i] = a > w || 4 * g + i - j > 0 ? x : 0.f;
                         }
                     }
 #pragma unroll
@@ -258,6 +262,11 @@ __global__ __launch_bounds__(256, 2) void delta_pairs_kernel(DeltaPairs p) {
             for (int half = 0; half <= w / 2; ++half) {
                 f32x4 lo = *reinterpret_cast<const f32x4*>(tile(w, 2 * half) + j * LD + 4 * g), hi = zero4();
                 if (2 * half + 1 <= w) hi = *reinterpret_cast<const f32x4*>(tile(w, 2 * half + 1) + j * LD + 4 * g);
+                if (BACK && w / 2 == half) {
+                    f32x4& d = w % 2 ? hi : lo;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) d[i] = 4 * g + i == j ? 0.f : d[i];
+                }
                 const Terms<3> f = split_terms<3>(lo, hi);
 #pragma unroll
                 for (int s = 0; s < 3; ++s)
@@ -303,7 +312,7 @@ __global__ __launch_bounds__(256, 2) void delta_pairs_kernel(DeltaPairs p) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const float t = tile(r, w)[(4 * g + i) * LD + j];
-                            x[y][i] = r == w && 4 * g + i == j ? 1.0f : t * over * kb[i];
+                            x[y][i] = r == w && 4 * g + i == j ? 0.f : t * over * kb[i];
                         }
                     }
                     const Terms<3> f = split_terms<3>(x[0], x[1]);
