@@ -272,15 +272,15 @@ __device__ __forceinline__ float row_sums(f32x4 x, int j) {
     c += dpp_move<kRor4>(c);
     return c + dpp_move<kRor8>(c);
 }
-// Column step (j / 4) + j % 4 of rows 4 g .. 4 g + 3 of a [16][ld] tile kept as N
+// Column j of rows 4 g .. 4 g + 3 of a [16][ld] tile kept as N
 // bf16 planes in LDS.
 template <int N>
-__device__ __forceinline__ f32x4 col4(const bf16* s, int plane, int ld, int j, int g, int step = 4) {
+__device__ __forceinline__ f32x4 col4(const bf16* s, int plane, int ld, int j, int g) {
     typedef __attribute__((address_space(3))) i16x4 lds4;
     f32x4 x = zero4();
 #pragma unroll
     for (int n = N - 1; n >= 0; --n) {
-        const bf16* p = s + n * plane + (4 * g + (j >> 2)) * ld + step * (j & 3);
+        const bf16* p = s + n * plane + (4 * g + (j >> 2)) * ld + 4 * (j & 3);
         const bf16x4 v = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)p));
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] += (float)v[i];

@@ -14,10 +14,10 @@
 
 namespace kda {
 
-template <int DK, int DV, int NC>
-__global__ __launch_bounds__(DV / NC * 4, 2 / NC) void delta_wide_kernel(DeltaChain p) {
+template <int DK, int DV>
+__global__ __launch_bounds__(DV * 4, 2) void delta_wide_kernel(DeltaChain p) {
     typedef bf16 E;
-    constexpr int C = kDeltaChunk, KM = DK / 32, NT = DV / NC * 4, NS = 2, NO = 2, ES = 2;
+    constexpr int C = kDeltaChunk, KM = DK / 32, NT = DV * 4, NS = 2, NO = 2, ES = 2;
     using Blk = DeltaBlock<1, false>;
     // Padded rows of K: 12 (mod 16) banks apart, so that both 16 rows of 16 bytes and
     // the transposing reads of 8-byte groups spread over the banks.
@@ -33,19 +33,14 @@ __global__ __launch_bounds__(DV / NC * 4, 2 / NC) void delta_wide_kernel(DeltaCh
     const int n = seq_len(p.lens, b, p.T), c_end = min(p.c1, (n + C - 1) / C);
     const int tid = threadIdx.x, w = wave_id(), lane = lane_id(), j = lane & 15, g = lane >> 4;
 
-    // ---- the state: tile t, channel 32 (t / 2) + 8 g + 4 (t % 2) + i, column of lane j
-    // of column tile ct: a lane's rows of the column tiles of o^T are adjacent columns
-    const int cbase = 16 * NC * w;
-    auto col = [&](int ct) { return cbase + 4 * NC * (j >> 2) + 4 * ct + (j & 3); };
-    f32x4 M[2 * KM][NC];
+    // ---- the state: tile t, channel 32 (t / 2) + 8 g + 4 (t % 2) + i, column 16 w + j
+    f32x4 M[2 * KM];
     {
         const float* in = p.S.in ? p.S.in + ((size_t)(p.S.in_slot ? p.S.in_slot[b] : b) * p.H + h) * (DK * DV) : nullptr;
 #pragma unroll
         for (int t = 0; t < 2 * KM; ++t)
 #pragma unroll
-            for (int ct = 0; ct < NC; ++ct)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) M[t][ct][i] = in ? in[(32 * (t >> 1) + 8 * g + 4 * (t & 1) + i) * DV + col(ct)] : 0.f;
+            for (int i = 0; i < 4; ++i) M[t][i] = in ? in[(32 * (t >> 1) + 8 * g + 4 * (t & 1) + i) * DV + 16 * w + j] : 0.f;
     }
 
     const int ldk = p.Hk * DK * ES, ldv = p.H * DV * ES;
@@ -106,103 +101,69 @@ __global__ __launch_bounds__(DV / NC * 4, 2 / NC) void delta_wide_kernel(DeltaCh
         const char* blk = s_blk[buf];
         const float* row = reinterpret_cast<const float*>(blk + Blk::row);
         // K S (rows: tokens) and (Q S)^T (columns: tokens)
-        f32x4 ks[kDeltaTiles][NC], o[kDeltaTiles][NC];
+        f32x4 ks[kDeltaTiles], o[kDeltaTiles];
 #pragma unroll
-        for (int a = 0; a < kDeltaTiles; ++a)
-#pragma unroll
-            for (int ct = 0; ct < NC; ++ct) ks[a][ct] = o[a][ct] = zero4();
+        for (int a = 0; a < kDeltaTiles; ++a) ks[a] = o[a] = zero4();
 #pragma unroll
         for (int m = 0; m < KM; ++m) {
-            Terms<3> sf[NC];
-#pragma unroll
-            for (int ct = 0; ct < NC; ++ct) sf[ct] = split_terms<3>(M[2 * m][ct], M[2 * m + 1][ct]);
+            const Terms<3> sf = split_terms<3>(M[2 * m], M[2 * m + 1]);
 #pragma unroll
             for (int a = 0; a < kDeltaTiles; ++a) {
                 const Terms<1> kt = row_terms<1>(sk + (16 * a + j) * LK + 32 * m + 8 * g, 0),
                                qt = row_terms<1>(sq + (16 * a + j) * LQ + 32 * m + 8 * g, 0);
-#pragma unroll
-                for (int ct = 0; ct < NC; ++ct) {
-                    ks[a][ct] = mma(kt, sf[ct], ks[a][ct]);
-                    o[a][ct] = mma(first_terms<NS>(sf[ct]), qt, o[a][ct]);
-                }
+                ks[a] = mma(kt, sf, ks[a]);
+                o[a] = mma(first_terms<NS>(sf), qt, o[a]);
             }
         }
         // R = V - e^G K S, E = inv R
-        Terms<3> rt[2][NC];
+        Terms<3> rt[2];
 #pragma unroll
         for (int a = 0; a < kDeltaTiles; ++a) {
             const f32x4 eg = *reinterpret_cast<const f32x4*>(row + kRowGrow + 16 * a + 4 * g);
             const float eo = p.scale * row[kRowGrow + 16 * a + j];
+            const f32x4 v = col4<1>(sv + 16 * a * LV + 16 * w, 0, LV, j, g);
 #pragma unroll
-            for (int ct = 0; ct < NC; ++ct) {
-                const f32x4 v = col4<1>(sv + 16 * a * LV + cbase + 4 * ct, 0, LV, j, g, 4 * NC);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) ks[a][ct][i] = v[i] - eg[i] * ks[a][ct][i];
-                o[a][ct] *= eo;
-            }
+            for (int i = 0; i < 4; ++i) ks[a][i] = v[i] - eg[i] * ks[a][i];
+            o[a] *= eo;
         }
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int ct = 0; ct < NC; ++ct) rt[x][ct] = split_terms<3>(ks[2 * x][ct], ks[2 * x + 1][ct]);
-        f32x4 e[kDeltaTiles][NC];
+        for (int x = 0; x < 2; ++x) rt[x] = split_terms<3>(ks[2 * x], ks[2 * x + 1]);
+        f32x4 e[kDeltaTiles];
 #pragma unroll
         for (int a = 0; a < kDeltaTiles; ++a) {
+            e[a] = zero4();
 #pragma unroll
-            for (int ct = 0; ct < NC; ++ct) e[a][ct] = zero4();
-#pragma unroll
-            for (int x = 0; x <= a / 2; ++x) {
-                const Terms<3> t = frag_terms<3>(blk + Blk::inv + lower(a, x) * 3 * kFragBytes);
-#pragma unroll
-                for (int ct = 0; ct < NC; ++ct) e[a][ct] = mma(t, rt[x][ct], e[a][ct]);
-            }
+            for (int x = 0; x <= a / 2; ++x) e[a] = mma(frag_terms<3>(blk + Blk::inv + lower(a, x) * 3 * kFragBytes), rt[x], e[a]);
         }
-        // o, stored a row of 4 NC columns a lane
-        Terms<NO> et[2][NC];
+        // o, stored a row of four columns a lane
+        Terms<NO> et[2];
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int ct = 0; ct < NC; ++ct) et[x][ct] = split_terms<NO>(e[2 * x][ct], e[2 * x + 1][ct]);
+        for (int x = 0; x < 2; ++x) et[x] = split_terms<NO>(e[2 * x], e[2 * x + 1]);
         const Rsrc to = rows_rsrc(p.o, at_v, c, rows, ldv, DV * ES);
 #pragma unroll
         for (int a = 0; a < kDeltaTiles; ++a) {
 #pragma unroll
-            for (int x = 0; x <= a / 2; ++x) {
-                const Terms<1> pf = frag_terms<1>(blk + Blk::pair + lower(a, x) * kFragBytes);
-#pragma unroll
-                for (int ct = 0; ct < NC; ++ct) o[a][ct] = mma(et[x][ct], pf, o[a][ct]);
-            }
-            const int off = 16 * a + j < rows ? (16 * a + j) * ldv + (cbase + 4 * NC * g) * ES : kOffPast;
-            if constexpr (NC == 2)
-                buf_store_u32x4(to, off, __builtin_bit_cast(u32x4, pack8(o[a][0], o[a][1])));
-            else
-                buf_store_u32x2(to, off, __builtin_bit_cast(u32x2, pack4(o[a][0])));
+            for (int x = 0; x <= a / 2; ++x) o[a] = mma(et[x], frag_terms<1>(blk + Blk::pair + lower(a, x) * kFragBytes), o[a]);
+            const int off = 16 * a + j < rows ? (16 * a + j) * ldv + (16 * w + 4 * g) * ES : kOffPast;
+            buf_store_u32x2(to, off, __builtin_bit_cast(u32x2, pack4(o[a])));
         }
         // S' = e^{G_C} S + K^T (e^{G_C - G} beta E)
-        Terms<3> ut[2][NC];
+        Terms<3> ut[2];
 #pragma unroll
         for (int a = 0; a < kDeltaTiles; ++a) {
             const f32x4 wr = *reinterpret_cast<const f32x4*>(row + kRowWrite + 16 * a + 4 * g);
 #pragma unroll
-            for (int ct = 0; ct < NC; ++ct)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) e[a][ct][i] *= wr[i];
+            for (int i = 0; i < 4; ++i) e[a][i] *= wr[i];
         }
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int ct = 0; ct < NC; ++ct) ut[x][ct] = split_terms<3>(e[2 * x][ct], e[2 * x + 1][ct]);
+        for (int x = 0; x < 2; ++x) ut[x] = split_terms<3>(e[2 * x], e[2 * x + 1]);
         const float f = decay(row[kRowDecay], row[kRowDecay + 1]);
 #pragma unroll
         for (int t = 0; t < 2 * KM; ++t) {
+            M[t] *= f;
 #pragma unroll
-            for (int ct = 0; ct < NC; ++ct) M[t][ct] *= f;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const Terms<1> kc = col_terms<1>(sk + 32 * x * LK, 0, LK, 32 * (t >> 1) + 4 * (t & 1), 8, j, g);
-#pragma unroll
-                for (int ct = 0; ct < NC; ++ct) M[t][ct] = mma(kc, ut[x][ct], M[t][ct]);
-            }
+            for (int x = 0; x < 2; ++x)
+                M[t] = mma(col_terms<1>(sk + 32 * x * LK, 0, LK, 32 * (t >> 1) + 4 * (t & 1), 8, j, g), ut[x], M[t]);
         }
     }
     if (p.S.out) {
@@ -210,20 +171,16 @@ __global__ __launch_bounds__(DV / NC * 4, 2 / NC) void delta_wide_kernel(DeltaCh
 #pragma unroll
         for (int t = 0; t < 2 * KM; ++t)
 #pragma unroll
-            for (int ct = 0; ct < NC; ++ct)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) out[(32 * (t >> 1) + 8 * g + 4 * (t & 1) + i) * DV + col(ct)] = M[t][ct][i];
+            for (int i = 0; i < 4; ++i) out[(32 * (t >> 1) + 8 * g + 4 * (t & 1) + i) * DV + 16 * w + j] = M[t][i];
     }
 }
 
-constexpr int kWideTiles = 1;   // column tiles of a wave
-
 hipError_t launch_delta_wide(const DeltaChain& a, hipStream_t stream) {
-    const dim3 grid((unsigned)(a.B * a.H)), block(128 / kWideTiles * 4);
+    const dim3 grid((unsigned)(a.B * a.H)), block(512);
     switch (a.dk) {
-        case 32: hipLaunchKernelGGL((delta_wide_kernel<32, 128, kWideTiles>), grid, block, 0, stream, a); break;
-        case 64: hipLaunchKernelGGL((delta_wide_kernel<64, 128, kWideTiles>), grid, block, 0, stream, a); break;
-        default: hipLaunchKernelGGL((delta_wide_kernel<128, 128, kWideTiles>), grid, block, 0, stream, a); break;
+        case 32: hipLaunchKernelGGL((delta_wide_kernel<32, 128>), grid, block, 0, stream, a); break;
+        case 64: hipLaunchKernelGGL((delta_wide_kernel<64, 128>), grid, block, 0, stream, a); break;
+        default: hipLaunchKernelGGL((delta_wide_kernel<128, 128>), grid, block, 0, stream, a); break;
     }
     return hipGetLastError();
 }
