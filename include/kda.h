@@ -590,12 +590,13 @@ kda_status kda_qk_norm_rope_backward(const void *q, const void *k, const float *
  *   finite number ((0, 1) is usual; keys of length 1 keep the recurrence stable
  *   up to 2).
  * - B * H <= 2^19, and H times the larger head size <= 2^22.
- * - With bf16, o takes the state and what each token writes as two bf16 terms
- *   and the pairs' weights as one on their way into it, dq and dk the states and
- *   their gradients as one and the others as two (off by 1.9e-3 to 2.3e-3 of the
- *   norm, of which each output's own rounding is 1.7e-3); the states, dg, dbeta
+ * - With bf16, o has its own rounding alone (1.7e-3 of the norm): the state, the
+ *   pairs' weights and what each token writes enter it as two bf16 terms, which
+ *   hold 2^-17 of each.  dq and dk take the states and their gradients as one term
+ *   (half a bf16 step on those parts of their sums) and the others as two: 2.1e-3
+ *   to 2.6e-3 of the norm, more only where those parts cancel.  The states, dbeta
  *   and dS0, and dv before its own rounding, are fp32 throughout.  With fp32
- *   everything is (3e-7 to 6e-7 of the norm).
+ *   everything is (1e-7 to 7e-7 of each head's norm).
  * - dg is a sum of fp32 parts over up to 256 tokens, none of which outweighs dg
  *   itself where decays are strong: off by up to 1e-5 of each head's norm (1e-6
  *   to 4e-6 is usual), whatever the head's decays.  A token whose decay is far

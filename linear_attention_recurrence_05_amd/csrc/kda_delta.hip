@@ -19,9 +19,13 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_chain_kerne
 constexpr size_t kDeltaWindowBytes = (size_t)384 << 20;
 
 // From so many heads of bf16 rows on a workgroup takes a whole one
-// (delta_wide_kernel), where fewer leave more than half of the device idle.  d 128,
-// T 4096, wide against eight workgroups of 16 columns: 64 heads 402 and 308 us, 128
-// heads 484 and 615 us, 256 heads 676 and 1,236 us.
+// (delta_wide_kernel), where fewer leave more than half of the device idle.  Wide
+// against eight workgroups of 16 columns, d_v 128, d_k 128 / 64 / 32, us: T 4096, 64
+// heads 425 / 293 / 251 and 285 / 201 / 179, 96 heads 459 / 324 / 288 and 435 / 342 /
+// 295, 128 heads 488 / 346 / 313 and 569 / 455 / 403, 256 heads 671 / 502 / 435 and
+// 1,139 / 891 / 768; T 512, 128 heads 66 / 51 / 46 and 69 / 56 / 50; T 100, 128 heads
+// 32 / 26 / 23 and 34 / 28 / 25.  Fewer value columns would leave a workgroup two or
+// four waves, and fp32's three terms of K and Q need twice the LDS there is.
 constexpr int kWideUnits = 128;
 
 struct DeltaWindows {

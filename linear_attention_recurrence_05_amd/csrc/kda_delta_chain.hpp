@@ -64,9 +64,12 @@ hipError_t launch_delta_wide(const DeltaChain& a, hipStream_t stream);
 template <typename E, int DK, bool BACK>
 struct ChainLds {
     static constexpr int C = kDeltaChunk, KM = DK / 32, NE = sizeof(E) == 2 ? 1 : 3;
-    // Terms of the state in Q S, of E and of the pairs' weights in o.  With bf16 two,
-    // two and one leave the weights' rounding alone beside o's own.
-    static constexpr int NS = BACK || NE == 3 ? 3 : 2, NO = NS, NP = BACK || NE == 3 ? 3 : 1;
+    // Terms of the state in Q S, of E and of the pairs' weights in o.  With bf16 two of
+    // each leave o its own rounding.  One of the weights would do with half a step on
+    // each pair, and 6.5 us of B1 H32 T4096's 137 (70 of B8 H32 T8192's 1,320): 2.4e-3 of
+    // the norm instead of 1.7e-3 for rows at random, but up to 9e-3 where queries and
+    // keys have most of their length in common and the pairs' sum nearly cancels.
+    static constexpr int NS = BACK || NE == 3 ? 3 : 2, NO = NS, NP = NS;
     static constexpr int LK = NE == 1 ? 40 : 32, LV = 24;    // padded rows
     __align__(16) bf16 k[KM][NE][C * LK];                    // a wave's own channels of K
     __align__(16) bf16 v[4][NE][16 * LV];                    // a wave's own tokens of V
@@ -265,8 +268,8 @@ __device__ __forceinline__ void delta_chain(const DeltaChain& p, int x, ChainLds
             }
         }
         o *= p.scale * grow_j;
-        o = mma(frag_terms<NO>(s.e[0]), rp[0], o);
-        if (w >= 2) o = mma(frag_terms<NO>(s.e[1]), rp[1], o);
+        o = mma_top(frag_terms<NO>(s.e[0]), rp[0], o);
+        if (w >= 2) o = mma_top(frag_terms<NO>(s.e[1]), rp[1], o);
         if constexpr (BACK) {
             float own = 0.f;                                 // dO . o of token 16 w + j
 #pragma unroll

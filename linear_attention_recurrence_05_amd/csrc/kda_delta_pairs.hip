@@ -327,7 +327,7 @@ __global__ __launch_bounds__(256, 2) void delta_pairs_kernel(DeltaPairs p) {
 }
 
 size_t delta_block_bytes(bool is_bf16, bool back) {
-    return back ? DeltaBlock<3, true>::bytes : is_bf16 ? DeltaBlock<1, false>::bytes : DeltaBlock<3, false>::bytes;
+    return back ? DeltaBlock<3, true>::bytes : is_bf16 ? DeltaBlock<2, false>::bytes : DeltaBlock<3, false>::bytes;
 }
 
 template <typename E, int NP, bool BACK>
@@ -344,7 +344,7 @@ static hipError_t launch_e(const DeltaPairs& a, hipStream_t stream) {
 
 hipError_t launch_delta_pairs(const DeltaPairs& a, bool back, hipStream_t stream) {
     if (back) return a.is_bf16 ? launch_e<bf16, 3, true>(a, stream) : launch_e<float, 3, true>(a, stream);
-    return a.is_bf16 ? launch_e<bf16, 1, false>(a, stream) : launch_e<float, 3, false>(a, stream);
+    return a.is_bf16 ? launch_e<bf16, 2, false>(a, stream) : launch_e<float, 3, false>(a, stream);
 }
 
 }  // namespace kda

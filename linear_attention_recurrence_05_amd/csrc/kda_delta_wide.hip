@@ -3,11 +3,11 @@
 // (b, h), one wave for each 16 value columns.
 //
 // A wave holds its columns' whole state [DK, 16] in accumulators and needs no other
-// wave: K, Q, V and the chunk's block are staged in LDS for all of them, in two
-// buffers, one barrier a chunk.  Against delta_chain_kernel, which divides a chunk
-// among four waves, nothing but the staged rows passes through LDS, so that the CU's
-// waves fill its issue slots: 2.1 KB of LDS a token and 16 columns against 2.7, and
-// no exchange.
+// wave: K, Q and the chunk's block are staged in LDS for all of them, in two buffers,
+// one barrier a chunk, and V by each wave for itself.  Against delta_chain_kernel,
+// which divides a chunk among four waves, nothing but the staged rows passes through
+// LDS, so that the CU's waves fill its issue slots: 2.2 KB of LDS a token and 16
+// columns against 2.7, and no exchange.
 #include <algorithm>
 
 #include "kda_delta_chain.hpp"
@@ -18,14 +18,14 @@ template <int DK, int DV>
 __global__ __launch_bounds__(DV * 4, 2) void delta_wide_kernel(DeltaChain p) {
     typedef bf16 E;
     constexpr int C = kDeltaChunk, KM = DK / 32, NT = DV * 4, NS = 2, NO = 2, ES = 2;
-    using Blk = DeltaBlock<1, false>;
+    using Blk = DeltaBlock<2, false>;
     // Padded rows of K: 12 (mod 16) banks apart, so that both 16 rows of 16 bytes and
     // the transposing reads of 8-byte groups spread over the banks.
-    constexpr int LK = DK + 24, LQ = DK + 8, LV = DV + 16;
-    constexpr int PK = C * DK / 8, PV = C * DV / 8, PB = Blk::bytes / 16;    // 16-byte pieces
-    constexpr int RK = (PK + NT - 1) / NT, RV = PV / NT, RB = (PB + NT - 1) / NT;   // of a thread
-    static_assert(PV % NT == 0 && (PK % NT == 0 || PK < NT), "pieces");
-    __shared__ __align__(16) bf16 s_k[2][C * LK], s_q[2][C * LQ], s_v[2][C * LV];
+    constexpr int LK = DK + 24, LQ = DK + 8, LV = 24;
+    constexpr int PK = C * DK / 8, PB = Blk::bytes / 16;    // 16-byte pieces
+    constexpr int RK = (PK + NT - 1) / NT, RV = 2, RB = (PB + NT - 1) / NT;   // of a thread
+    static_assert(PK % NT == 0 || PK < NT, "pieces");
+    __shared__ __align__(16) bf16 s_k[2][C * LK], s_q[2][C * LQ], s_v[DV / 16][C * LV];
     __shared__ __align__(16) char s_blk[2][Blk::bytes];
 
     const int unit = blockIdx.x, b = unit / p.H, h = unit % p.H, hk = h / (p.H / p.Hk);
@@ -64,8 +64,8 @@ __global__ __launch_bounds__(DV * 4, 2) void delta_wide_kernel(DeltaChain p) {
         }
 #pragma unroll
         for (int i = 0; i < RV; ++i) {
-            const int row = (tid + i * NT) / (DV / 8);
-            xv[i] = buf_load<u32x4>(v, row < rows ? row * ldv + (tid + i * NT) % (DV / 8) * 16 : kOffPast);
+            const int row = 32 * i + lane / 2;               // the wave's own columns
+            xv[i] = buf_load<u32x4>(v, row < rows ? row * ldv + (32 * w + lane % 2 * 16) : kOffPast);
         }
 #pragma unroll
         for (int i = 0; i < RB; ++i) xb[i] = buf_load<u32x4>(r, (tid + i * NT) * 16);
@@ -79,25 +79,33 @@ __global__ __launch_bounds__(DV * 4, 2) void delta_wide_kernel(DeltaChain p) {
             *reinterpret_cast<u32x4*>(&s_q[buf][row * LQ + col]) = xq[i];
         }
 #pragma unroll
-        for (int i = 0; i < RV; ++i)
-            *reinterpret_cast<u32x4*>(&s_v[buf][(tid + i * NT) / (DV / 8) * LV + (tid + i * NT) % (DV / 8) * 8]) = xv[i];
-#pragma unroll
         for (int i = 0; i < RB; ++i)
             if (PB % NT == 0 || tid + i * NT < PB) reinterpret_cast<u32x4*>(s_blk[buf])[tid + i * NT] = xb[i];
     };
 
+    auto stage_v = [&] {
+#pragma unroll
+        for (int i = 0; i < RV; ++i) *reinterpret_cast<u32x4*>(&s_v[w][(32 * i + lane / 2) * LV + lane % 2 * 8]) = xv[i];
+    };
+
     ChunkDecay decay;
     load(p.c0);
+    stage_v();
     stage(0);
     load(p.c0 + 1);
     int buf = 0;
     for (int c = p.c0; c < c_end; ++c, buf ^= 1) {
         const int rows = min(C, n - c * C);
         __syncthreads();                                     // this chunk is staged, the last one read
+        f32x4 v[kDeltaTiles];                                // the wave's own columns, whose place the next chunk's take
+#pragma unroll
+        for (int a = 0; a < kDeltaTiles; ++a) v[a] = col4<1>(&s_v[w][16 * a * LV], 0, LV, j, g);
+        wave_fence();
+        stage_v();
         stage(buf ^ 1);
         load(c + 2);
         __builtin_amdgcn_sched_barrier(0);                   // not later: they have this chunk's time to come
-        const bf16 *sk = s_k[buf], *sq = s_q[buf], *sv = s_v[buf];
+        const bf16 *sk = s_k[buf], *sq = s_q[buf];
         const char* blk = s_blk[buf];
         const float* row = reinterpret_cast<const float*>(blk + Blk::row);
         // K S (rows: tokens) and (Q S)^T (columns: tokens)
@@ -121,9 +129,8 @@ __global__ __launch_bounds__(DV * 4, 2) void delta_wide_kernel(DeltaChain p) {
         for (int a = 0; a < kDeltaTiles; ++a) {
             const f32x4 eg = *reinterpret_cast<const f32x4*>(row + kRowGrow + 16 * a + 4 * g);
             const float eo = p.scale * row[kRowGrow + 16 * a + j];
-            const f32x4 v = col4<1>(sv + 16 * a * LV + 16 * w, 0, LV, j, g);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) ks[a][i] = v[i] - eg[i] * ks[a][i];
+            for (int i = 0; i < 4; ++i) ks[a][i] = v[a][i] - eg[i] * ks[a][i];
             o[a] *= eo;
         }
 #pragma unroll
@@ -143,7 +150,7 @@ __global__ __launch_bounds__(DV * 4, 2) void delta_wide_kernel(DeltaChain p) {
 #pragma unroll
         for (int a = 0; a < kDeltaTiles; ++a) {
 #pragma unroll
-            for (int x = 0; x <= a / 2; ++x) o[a] = mma(et[x], frag_terms<1>(blk + Blk::pair + lower(a, x) * kFragBytes), o[a]);
+            for (int x = 0; x <= a / 2; ++x) o[a] = mma_top(et[x], frag_terms<2>(blk + Blk::pair + lower(a, x) * 2 * kFragBytes), o[a]);
             const int off = 16 * a + j < rows ? (16 * a + j) * ldv + (16 * w + 4 * g) * ES : kOffPast;
             buf_store_u32x2(to, off, __builtin_bit_cast(u32x2, pack4(o[a])));
         }

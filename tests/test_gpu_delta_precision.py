@@ -1,0 +1,47 @@
+"""The error in norm of each head's results of the gated delta rule against 64 bits, with limits
+that tell an operand in two bf16 terms from one in three, and one term from two in bf16's o."""
+import pytest
+import torch
+
+import delta_ref as ref
+from delta_precision import errors, inputs, limit
+from gpu_common import need_gpu, say
+from test_gpu_delta import ARGS, BF, F32
+
+pytestmark = pytest.mark.gpu
+
+HEADS = dict(o=2, S_T=1, dq=2, dk=2, dv=2, dbeta=2, dS0=1)
+
+
+def run(x):
+    import linear_attention_recurrence_05_amd as kda
+    y = {n: t.cuda() if isinstance(t, torch.Tensor) else t for n, t in x.items()}
+    o, S_T = kda.delta_prefill(*(y[n] for n in ARGS), y["S0"])
+    got = kda.delta_backward(*(y[n] for n in ARGS[:5]), y["dO"], y["scale"], y["S0"], y["dS_T"])
+    torch.cuda.synchronize()
+    return {**got, "o": o, "S_T": S_T}
+
+
+def check(x, names=tuple(HEADS)):
+    got = run(x)
+    out = ref.prefill(*(x[n] for n in ARGS), x["S0"])
+    want = {"o": out["o"], "S_T": out["S_T"]}
+    if set(names) - set(want):
+        want.update(ref.backward(*(x[n] for n in ARGS), x["dO"], x["S0"], x["dS_T"])[0])
+    err = {n: errors(got[n], want[n], HEADS[n]) for n in names}
+    say({n: f"{e:.1e}" for n, e in err.items()})
+    for n, e in err.items():
+        assert e < limit(n, x["q"].dtype), (n, e)
+
+
+@pytest.mark.parametrize("size", [(1, 1, 1, 1, 128, 128), (1, 1, 32, 32, 128, 128), (2, 3, 4, 2, 64, 64), (1, 64, 8, 8, 32, 32),
+                                  (1, 300, 4, 4, 64, 64), (1, 256, 4, 4, 128, 128), (1, 333, 4, 1, 32, 128)])
+def test_bf16_outputs_have_their_own_rounding_alone(size):
+    """Also of prompts of a token and of a chunk without a state, and where queries and keys have most
+    of their length in common."""
+    need_gpu()
+    say("precision of o", size)
+    for queries in (False, True):
+        x = inputs(*size, BF, seed=size[1], queries=queries)
+        x["S0"].zero_()
+        check(x, ("o", "S_T"))
