@@ -34,6 +34,25 @@ def check(x, names=tuple(HEADS)):
         assert e < limit(n, x["q"].dtype), (n, e)
 
 
+# The last three have three and more of dg's anchors.
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("size", [  # B, T, H, Hk, dk, dv
+    (1, 16, 8, 8, 32, 32), (1, 300, 4, 4, 64, 64), (2, 161, 3, 3, 128, 32), (1, 200, 4, 2, 32, 128), (1, 900, 2, 1, 128, 128),
+    (1, 1300, 2, 2, 64, 32), (2, 700, 3, 3, 32, 64)])
+def test_prefill_and_gradients(size, dtype):
+    need_gpu()
+    say("precision", size, dtype)
+    check(inputs(*size, dtype, seed=size[1]))
+
+
+@pytest.mark.parametrize("dk", [32, 64, 128])
+def test_many_heads(dk):
+    """A workgroup for each head (from 128 of them and 128 value columns on)."""
+    need_gpu()
+    say("precision, many heads", dk)
+    check(inputs(4, 130, 32, 16, dk, 128, BF, seed=dk, queries=True), ("o", "S_T"))
+
+
 @pytest.mark.parametrize("size", [(1, 1, 1, 1, 128, 128), (1, 1, 32, 32, 128, 128), (2, 3, 4, 2, 64, 64), (1, 64, 8, 8, 32, 32),
                                   (1, 300, 4, 4, 64, 64), (1, 256, 4, 4, 128, 128), (1, 333, 4, 1, 32, 128)])
 def test_bf16_outputs_have_their_own_rounding_alone(size):
