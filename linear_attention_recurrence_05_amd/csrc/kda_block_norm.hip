@@ -255,11 +255,12 @@ static int block_groups(long long rows, int tpr, int most_waves) {
     const int rpw = tpr < 256 ? 256 / tpr : 1, waves = std::max(tpr, 256) / kWave;
     return (int)std::min<long long>((rows + rpw - 1) / rpw, most_waves / waves);
 }
-// Of the gradients as many as a device holds with one piece a thread (120 registers),
-// half as many with two (228); each leaves partial weight gradients.
+// Of the gradients as many as a device holds: half as many waves with two pieces a
+// thread (228 registers) as with one (120), but for rows of 1,024 threads, which have
+// 128 registers whatever they hold.  Each leaves partial weight gradients.
 static int block_bwd_groups(long long rows, int D, bool is_bf16) {
     const int tpr = block_threads(D, is_bf16);
-    return block_groups(rows, tpr, D / (is_bf16 ? 8 : 4) <= tpr ? kBlockWaves : kBlockWaves / 2);
+    return block_groups(rows, tpr, D / (is_bf16 ? 8 : 4) <= tpr || tpr == 1024 ? kBlockWaves : kBlockWaves / 2);
 }
 
 template <typename E, bool BWD, int TPR, int NV>
