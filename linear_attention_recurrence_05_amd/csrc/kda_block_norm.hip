@@ -16,7 +16,9 @@
 // of 7,168 with norm, gate and weights take 54 us, 5.4 TB/s (85 us with one row of
 // a workgroup after the other and the weights read for each), the gradients of
 // 2,002 rows of 4,096 take 38.5 us (57.5 us), of 8,192 rows of 512 24 us (30 us with
-// a partial weight gradient for each row of a workgroup).
+// a partial weight gradient for each row of a workgroup).  Of the widest rows they take
+// 126 us for 2,002 bf16 ones of 16,384, 4.2 TB/s (236 with spills), 113 us for 1,000 fp32
+// ones (198).
 #include <algorithm>
 
 #include "kda_delta.hpp"
@@ -54,21 +56,33 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void block_norm_kernel(Block
     constexpr int VE = 16 / sizeof(E), NT = TPR < 256 ? 256 : TPR, RPW = NT / TPR;
     constexpr bool FAST = sizeof(E) == 2;
     constexpr bool AHEAD = TPR < 1024;   // 1,024 threads have half the registers
+    // Sixteen elements a thread do not leave room for their weights and for the sums of
+    // the weights' gradients in 128 registers (120 and 151 of them were spilled): such
+    // rows read the weights again, from L2, and keep the sums in LDS, each thread its own
+    // columns; of fp32 rows z and dh are loaded where they are used.
+    constexpr bool LEAN = BWD && TPR == 1024 && NV * VE > 8, LATE = LEAN && sizeof(E) == 4;
     __shared__ float s_sum[2 * TPR / kWave];
     RowSum<TPR> sum{s_sum};
     const int t = threadIdx.x % TPR, slot = TPR < 256 ? wave_id() : 0, pieces = p.D / VE;
     const float inv = 1.0f / (float)p.D;
     auto has = [&](int v) { return v * TPR + t < pieces; };
-    float wy[NV][VE], wn[NV][VE];
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
+    __shared__ __align__(16) float s_lean[LEAN ? 2 : 1][LEAN ? TPR * NV * VE : 1];
+    constexpr int NW = LEAN ? 1 : NV;
+    float wy[NW][VE], wn[NW][VE];
+    auto weights = [&](const float* w, int v, float (&x)[VE]) {
 #pragma unroll
         for (int i = 0; i < VE; i += 4) {
             const size_t e = (size_t)(v * TPR + t) * VE + i;
-            const f32x4 one = {1.f, 1.f, 1.f, 1.f};
-            *reinterpret_cast<f32x4*>(&wy[v][i]) = p.w_y && has(v) ? *reinterpret_cast<const f32x4*>(p.w_y + e) : one;
-            *reinterpret_cast<f32x4*>(&wn[v][i]) = p.w_n && has(v) ? *reinterpret_cast<const f32x4*>(p.w_n + e) : one;
+            *reinterpret_cast<f32x4*>(&x[i]) = w && has(v) ? *reinterpret_cast<const f32x4*>(w + e) : f32x4{1.f, 1.f, 1.f, 1.f};
         }
+    };
+    if constexpr (!LEAN) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            weights(p.w_y, v, wy[v]);
+            weights(p.w_n, v, wn[v]);
+        }
+    }
     struct Row {
         u32x4 y[NV], h[NV], z[NV], dn[BWD ? NV : 1], dh[BWD ? NV : 1];
     };
@@ -82,12 +96,16 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void block_norm_kernel(Block
             };
             x.y[v] = get(p.y);
             x.h[v] = get(BWD ? p.h_in : p.r);
-            x.z[v] = get(p.z);
+            if constexpr (!LATE) x.z[v] = get(p.z);
             if constexpr (BWD) {
                 x.dn[v] = get(p.dn);
-                x.dh[v] = get(p.dh);
+                if constexpr (!LATE) x.dh[v] = get(p.dh);
             }
         }
+    };
+    auto late = [&](const void* base, long long row, int v) {
+        const size_t at = ((size_t)row * p.D) / VE + v * TPR + t;
+        return base && has(v) ? __builtin_nontemporal_load((const u32x4*)base + at) : u32x4{0, 0, 0, 0};
     };
     auto store = [&](void* base, long long row, int v, const float (&x)[VE]) {
         store_row<E, VE>((E*)base + (size_t)row * p.D + (size_t)(v * TPR + t) * VE, x);
@@ -114,11 +132,25 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void block_norm_kernel(Block
         }
         return 1.0f / sqrtf(m);
     };
-    float dwy[BWD ? NV : 1][VE], dwn[BWD ? NV : 1][VE];
+    float dwy[BWD ? NW : 1][VE], dwn[BWD ? NW : 1][VE];      // LEAN: of the piece at hand
 #pragma unroll
-    for (int v = 0; v < (BWD ? NV : 1); ++v)
+    for (int v = 0; v < (BWD ? NW : 1); ++v)
 #pragma unroll
         for (int i = 0; i < VE; ++i) dwy[v][i] = dwn[v][i] = 0.f;
+    auto to_lds = [&](int of, int v, float (&x)[VE]) {       // adds x to piece v's sums, and clears it
+#pragma unroll
+        for (int i = 0; i < VE; i += 4) {
+            if (part) *reinterpret_cast<f32x4*>(&s_lean[of][(v * TPR + t) * VE + i]) += *reinterpret_cast<const f32x4*>(&x[i]);
+            *reinterpret_cast<f32x4*>(&x[i]) = zero4();
+        }
+    };
+    if constexpr (LEAN) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int i = 0; i < VE; i += 4)
+                *reinterpret_cast<f32x4*>(&s_lean[0][(v * TPR + t) * VE + i]) = *reinterpret_cast<f32x4*>(&s_lean[1][(v * TPR + t) * VE + i]) = zero4();
+    }
     const long long step = (long long)gridDim.x * RPW;
     long long row = (long long)blockIdx.x * RPW + slot;
     Row next;
@@ -162,37 +194,43 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void block_norm_kernel(Block
             float g[NV][VE], dot = 0.f, dot_y = 0.f;
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
+                const int k = LEAN ? 0 : v;
                 unpack<E, VE>(cur.dn[v], g[v]);
+                if constexpr (LEAN) weights(p.w_n, v, wn[0]);
 #pragma unroll
                 for (int i = 0; i < VE; ++i) {
                     h[v][i] *= r;
-                    dwn[v][i] += g[v][i] * h[v][i];
-                    g[v][i] *= wn[v][i];
+                    dwn[k][i] += g[v][i] * h[v][i];
+                    g[v][i] *= wn[k][i];
                     dot += g[v][i] * h[v][i];
                 }
+                if constexpr (LEAN) to_lds(1, v, dwn[0]);
             }
             dot = sum(dot) * inv;
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
                 float x[VE], z[VE], dz[VE];
-                unpack<E, VE>(cur.dh[v], x);
+                unpack<E, VE>(LATE ? late(p.dh, row, v) : cur.dh[v], x);
 #pragma unroll
                 for (int i = 0; i < VE; ++i) g[v][i] = x[i] + scale * (r * (g[v][i] - dot * h[v][i]));
                 if (has(v)) store(p.dr, row, v, g[v]);
                 if (!p.y) continue;
-                unpack<E, VE>(cur.z[v], z);
+                const int k = LEAN ? 0 : v;
+                unpack<E, VE>(LATE ? late(p.z, row, v) : cur.z[v], z);
+                if constexpr (LEAN) weights(p.w_y, v, wy[0]);
 #pragma unroll
                 for (int i = 0; i < VE; ++i) {
                     float s = 1.0f, rest = 0.f;
                     if (p.z) sigmoids<FAST>(z[i], s, rest);
                     y[v][i] *= ry;
                     const float du = p.scale * g[v][i] * s;
-                    dwy[v][i] += du * y[v][i];
-                    const float dm = du * wy[v][i];
+                    dwy[k][i] += du * y[v][i];
+                    const float dm = du * wy[k][i];
                     dz[i] = dm * y[v][i] * rest;
                     dot_y += dm * y[v][i];
                     g[v][i] = dm;
                 }
+                if constexpr (LEAN) to_lds(0, v, dwy[0]);
                 if (p.z && has(v)) store(p.dz, row, v, dz);
             }
             if (p.y) {
@@ -237,8 +275,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void block_norm_kernel(Block
 #pragma unroll
                 for (int i = 0; i < VE; i += 4) {
                     const size_t e = (size_t)(v * TPR + t) * VE + i;
-                    *reinterpret_cast<f32x4*>(to + e) = *reinterpret_cast<const f32x4*>(&dwy[v][i]);
-                    *reinterpret_cast<f32x4*>(to + p.D + e) = *reinterpret_cast<const f32x4*>(&dwn[v][i]);
+                    *reinterpret_cast<f32x4*>(to + e) = *reinterpret_cast<const f32x4*>(LEAN ? &s_lean[0][e] : &dwy[LEAN ? 0 : v][i]);
+                    *reinterpret_cast<f32x4*>(to + p.D + e) = *reinterpret_cast<const f32x4*>(LEAN ? &s_lean[1][e] : &dwn[LEAN ? 0 : v][i]);
                 }
             }
         }
