@@ -175,9 +175,10 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void block_norm_kernel(Block
                     unpack<E, VE>(cur.z[v], z);
 #pragma unroll
                     for (int i = 0; i < VE; ++i) {
-                        float u = y[v][i] * ry * wy[v][i];
-                        if (p.z) u *= sigmoid<FAST>(z[i]);
-                        h[v][i] += p.scale * u;
+                        // the factors first: y, and y w_y, may be beyond fp32 where u is not
+                        float c = p.scale * wy[v][i];
+                        if (p.z) c *= sigmoid<FAST>(z[i]);
+                        h[v][i] += y[v][i] * ry * c;
                     }
                     if (has(v)) store(p.h, row, v, h[v]);
                 }
@@ -226,7 +227,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void block_norm_kernel(Block
                     const float du = p.scale * g[v][i] * s;
                     dwy[k][i] += du * y[v][i];
                     const float dm = du * wy[k][i];
-                    dz[i] = dm * y[v][i] * rest;
+                    dz[i] = dm * rest * y[v][i];             // in this order, as above
                     dot_y += dm * y[v][i];
                     g[v][i] = dm;
                 }
