@@ -598,7 +598,7 @@ kda_status kda_qk_norm_rope_backward(const void *q, const void *k, const float *
  *   and dS0, and dv before its own rounding, are fp32 throughout.  With fp32
  *   everything is (1e-7 to 7e-7 of each head's norm).
  * - dg is a sum of fp32 parts over up to 256 tokens, none of which outweighs dg
- *   itself where decays are strong: off by up to 1e-5 of each head's norm (1e-6
+ *   itself where decays are strong: off by up to 1e-5 of each head's norm (2e-7
  *   to 4e-6 is usual), whatever the head's decays.  A token whose decay is far
  *   stronger than those of the next 256 has the error of theirs beside its own
  *   small dg; where exp(g) is 0 in fp32, dg is 0. */

@@ -184,8 +184,11 @@ __device__ __forceinline__ void delta_reverse(const DeltaReverse& p, int x, Reve
         u *= end;
         if (w < 2) u = mma(rp[0], col_terms<NE>(&s.o[0][0], C * LV, LV, 0, 4, j, g), u);
         u = mma(rp[1], col_terms<NE>(&s.o[0][32 * LV], C * LV, LV, 0, 4, j, g), u);
-        const f32x4 dO = col4<NE>(&s.o[0][16 * w * LV], C * LV, LV, j, g), pdO = self * dO;
-        put_half<3>(s.d[w >> 1], w & 1, u + pdO);
+        const f32x4 dO = col4<NE>(&s.o[0][16 * w * LV], C * LV, LV, j, g), p_own = self;
+        f32x4 all;                                           // one rounding, not two
+#pragma unroll
+        for (int i = 0; i < 4; ++i) all[i] = u[i] + p_own[i] * dO[i];
+        put_half<3>(s.d[w >> 1], w & 1, all);
         put_half<3>(s.gq[w >> 1], w & 1, p.scale * grow * dO);
         const f32x4 eg = grow;
         const float f = decay(decay_f, decay_rest);
@@ -193,10 +196,12 @@ __device__ __forceinline__ void delta_reverse(const DeltaReverse& p, int x, Reve
         __syncthreads();
         // ---- Z of the wave's tokens, a column a lane and (zt) a token a lane
         const Terms<3> d1 = frag_terms<3>(s.d[1]);
-        f32x4 y = mma(rt[1], d1, u), zt = mma(d1, rt[1], zero4());
+        Sum2 ys;
+        ys.add(rt[1], d1);
+        f32x4 zt = mma(d1, rt[1], zero4());
         if (w < 2) {
             const Terms<3> d0 = frag_terms<3>(s.d[0]);
-            y = mma(rt[0], d0, y);
+            ys.add(rt[0], d0);
             zt = mma(d0, rt[0], zt);
             zt = mma(d0, own, zt);
         } else {
@@ -204,14 +209,17 @@ __device__ __forceinline__ void delta_reverse(const DeltaReverse& p, int x, Reve
         }
         put_piece<E>(&s.v[w][0][min(lane / ES, 15) * LV + lane % ES * (16 / ES)], 16 * LV, rv, lane < 16 * ES);
         wave_fence();
-        const f32x4 z = y + pdO;
+        const f32x4 y = u + ys.sum();
+        f32x4 z;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] = y[i] + p_own[i] * dO[i];
         put_half<3>(s.gr[w >> 1], w & 1, -eg * (beta * z));
         // ---- out: Z; dv = beta Z; beta y . v
         {
             const Rsrc tz = make_rsrc(sw.z + (((size_t)unit * sw.NC + c) * p.dv + 16 * tile) * C, 16 * C * 4);
             buf_stream_u32x4(tz, (j * C + 16 * w + 4 * g) * 4, __builtin_bit_cast(u32x4, z));
             const f32x4 v = col4<NE>(&s.v[w][0][0], 16 * LV, LV, j, g);
-            float x = row_sums(v * (beta * y), j);           // of token 16 w + 4 g + j % 4
+            float x = lane_row(beta, j) * row_sums(v * y, j);   // of token 16 w + 4 g + j % 4
             if (is_anchor(c) && 16 * w + 4 * g + (j & 3) == rows - 1) x = 0.f;
             wave_fence();                                    // before the next chunk's v
             buf_store_u32(make_rsrc(sw.dot + (((size_t)(tiles + tile) * units + unit) * sw.NC + c) * C, C * 4),
@@ -228,17 +236,20 @@ __device__ __forceinline__ void delta_reverse(const DeltaReverse& p, int x, Reve
         __syncthreads();
         // ---- Y' = e^{G_C} Y + Q^T (e^G dO) - K^T (e^G beta Z)
         if (holds) {
-#pragma unroll
-            for (int t = 0; t < 2; ++t) Y[t] *= f;
+            Sum2 sum[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const Terms<3> gq = frag_terms<3>(s.gq[x]), gr = frag_terms<3>(s.gr[x]);
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    Y[t] = mma(col_terms<NE>(&s.q[w][0][32 * x * LK], C * LK, LK, 4 * t, 8, j, g), gq, Y[t]);
-                    Y[t] = mma(col_terms<NE>(&s.k[w][0][32 * x * LK], C * LK, LK, 4 * t, 8, j, g), gr, Y[t]);
+                    sum[t].add(col_terms<NE>(&s.q[w][0][32 * x * LK], C * LK, LK, 4 * t, 8, j, g), gq);
+                    sum[t].add(col_terms<NE>(&s.k[w][0][32 * x * LK], C * LK, LK, 4 * t, 8, j, g), gr);
                 }
             }
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) Y[t][i] = f * Y[t][i] + sum[t].sum()[i];
         }
     }
     if (holds && p.dS0) {

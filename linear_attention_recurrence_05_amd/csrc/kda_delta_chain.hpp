@@ -215,11 +215,9 @@ __device__ __forceinline__ void delta_chain(const DeltaChain& p, int x, ChainLds
 #pragma unroll
                 for (int i = 0; i < 4; ++i) dO_t[i] += (float)t[i];
             }
-            R = v - ks;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) R[i] = v[i] - grow[i] * R[i];
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) R[i] = v[i] - grow[i] * R[i];
         put_half<3>(s.r[w >> 1], w & 1, R);
         f32x4 o = zero4();                                   // rows: columns 4 g + i, column: token 16 w + j
 #pragma unroll
@@ -227,13 +225,18 @@ __device__ __forceinline__ void delta_chain(const DeltaChain& p, int x, ChainLds
         load_qv(c + 1);
         __syncthreads();
         // ---- E of the wave's tokens
-        f32x4 e = mma(rt[0], frag_terms<3>(s.r[0]), zero4());
-        if (w >= 2) e = mma(rt[1], frag_terms<3>(s.r[1]), e);
+        f32x4 e;
         float dot = 0.f;
         if constexpr (BACK) {
-            ks -= e;                                         // all that older tokens give
-            e += R;
-            dot = row_sums(dO * (self * ks), j);             // of token 16 w + 4 g + j % 4
+            Sum2 x;
+            x.add(rt[0], frag_terms<3>(s.r[0]));
+            if (w >= 2) x.add(rt[1], frag_terms<3>(s.r[1]));
+            ks -= x.sum();                                   // all that older tokens give
+            e = x.sum() + R;
+            dot = lane_row(self, j) * row_sums(dO * ks, j);  // of token 16 w + 4 g + j % 4
+        } else {
+            e = mma(rt[0], frag_terms<3>(s.r[0]), zero4());
+            if (w >= 2) e = mma(rt[1], frag_terms<3>(s.r[1]), e);
         }
         put_half<NO>(s.e[w >> 1], w & 1, e);
         if constexpr (BACK) {
@@ -256,7 +259,19 @@ __device__ __forceinline__ void delta_chain(const DeltaChain& p, int x, ChainLds
         __syncthreads();
         // ---- the state's update; o of the wave's tokens
         const float f = decay(decay_f, decay_rest);
-        if (holds) {
+        if (BACK && holds) {
+            Sum2 sum[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const Terms<3> u = frag_terms<3>(s.u[x]);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) sum[t].add(col_terms<NE>(&s.k[w][0][32 * x * LK], C * LK, LK, 4 * t, 8, j, g), u);
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) M[t][i] = f * M[t][i] + sum[t].sum()[i];
+        } else if (holds) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) M[t] *= f;
 #pragma unroll
