@@ -13,7 +13,7 @@
 // workgroup, no LDS) or a workgroup, which sums through LDS in fixed order.  A
 // workgroup takes several rows, with the next one's pieces in flight and the
 // weights, twice a bf16 row's bytes each, in registers throughout: 4,096 bf16 rows
-// of 7,168 with norm, gate and weights take 54 us, 5.4 TB/s (85 us with one row of
+// of 7,168 with norm, gate and weights take 52 us, 5.7 TB/s (85 us with one row of
 // a workgroup after the other and the weights read for each), the gradients of
 // 2,002 rows of 4,096 take 38.5 us (57.5 us), of 8,192 rows of 512 24 us (30 us with
 // a partial weight gradient for each row of a workgroup).  Of the widest rows they take

@@ -14,8 +14,10 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_chain_kerne
 
 // Chunks whose blocks the workspace holds at a time: longer sequences run window
 // by window, the state carried in the workspace.  Half as much, which the last-level
-// cache holds, costs more in launches than it saves: H32 d128 bf16, B4 T4096 461
-// against 490 us, B8 T8192 1,505 against 1,540, B1 T32768 1,166 against 1,196.
+// cache holds, costs more in launches than it saves, and twice as much saves no more
+// than 3 %: H32 d128 bf16, 192 / 384 / 768 MiB, B4 T4096 505 / 490 / 489 us, B8 T8192
+// 1,367 / 1,340 / 1,303, B1 T32768 1,215 / 1,192 / 1,174.  At least eight chunks: 2 GiB
+// for 8,192 heads.
 constexpr size_t kDeltaWindowBytes = (size_t)384 << 20;
 
 // From so many heads of bf16 rows on a workgroup takes a whole one

@@ -261,10 +261,10 @@ __device__ __forceinline__ void delta_reverse(const DeltaReverse& p, int x, Reve
 }
 
 // Both sweeps at once, for neither needs the other.  Where they leave CUs idle this
-// hides the shorter one (fp32 B3 H8 T333 d64: 27 us against 21 and 28 one after the
+// hides the shorter one (fp32 B3 H8 T333 d64: 28 us against 23 and 28 one after the
 // other); where each fills the device with a workgroup a CU, the other's waves issue
-// while one's wait (B1 H32 T4096 d128 bf16: 375 us against 182 and 217; with every
-// chunk's operands in L2 it would be 285).  Eight waves a workgroup, which halve what
+// while one's wait (B1 H32 T4096 d128 bf16: 373 us against 193 and 233; with every
+// chunk's operands in L2 it was 285).  Eight waves a workgroup, which halve what
 // a wave does, took 460 us there, for two of them find no registers beside each other.
 template <typename E, int DK>
 __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_sweeps_kernel(DeltaChain f, DeltaReverse r) {
@@ -302,8 +302,9 @@ struct DeltaQK {
 // leave out is half a step on a part of the sum, beside the result's own rounding:
 // dq and dk are off by 2.3e-3 of their norm, 1.7e-3 of it that rounding; with all of
 // them one by 3.0e-3).  Bound by the latency of what it reads, 180 KB a chunk and
-// head with one workgroup a CU: B1 H32 T4096 d128 takes 133 us, 3.2 TB/s.  32 columns
-// of 64, with 168 registers; two workgroups a CU (128 registers) spilled and took 287 us.
+// head with one workgroup a CU: B1 H32 T4096 d128 takes 124 us, 3.2 TB/s.  32 columns
+// of 64, with 168 registers (64 of them took 3 us more); two workgroups a CU (128
+// registers) spilled and took 287 us.
 template <typename E, int DK>
 __global__ __launch_bounds__(512, 2) void delta_qk_kernel(DeltaQK p) {
     constexpr int NE = sizeof(E) == 2 ? 1 : 3, NU = NE == 1 ? 2 : 3, ES = sizeof(E), PE = 16 / ES, L = kDeltaChunk, NT = 512;

@@ -2,15 +2,17 @@
 // depend on the state (kda_delta_chunk.hpp): the inverse of the triangular system
 // and the weights of pairs of tokens, as matrix operands in the workspace.
 //
-// One wave per chunk and head.  K K^T and Q K^T by MFMA with the decays applied in the accumulators; N in LDS as its ten
-// tiles of 16 x 16.  The inverse: the four tiles on the diagonal by substitution, a
-// column a lane (stable for any beta in [0, 2] and keys of length 1, where a series
-// in powers of N is not: repeated keys make its terms grow to thousands before they
-// cancel), then those below, T_rc = -T_rr sum_q A_rq T_qc, in fp32 MFMA, in N's place.
-// (Four waves a chunk, each with 16 of its tokens, left three of four lanes idle in
-// the substitution and two waves in the products below, and took three times as
-// long.)  The 2,048 chunks of B1 H32 T4096 d128 take 23 us, with the gradients'
-// operands 48 us, of which the 113 MB that they write are half.
+// One wave per chunk and head.  K K^T and Q K^T by MFMA with the decays applied in the
+// accumulators; N in LDS as its ten tiles of 16 x 16.  The inverse: the four tiles on
+// the diagonal by substitution, a column a lane (stable for any beta in [0, 2] and keys
+// of length 1, where a series in powers of N is not: repeated keys make its terms grow
+// to thousands before they cancel), then those below, T_rc = -T_rr sum_q A_rq T_qc, in
+// fp32 MFMA, in N's place.  (Four waves a chunk, each with 16 of its tokens, left three
+// of four lanes idle in the substitution and two waves in the products below, and took
+// three times as long.)  The 2,048 chunks of B1 H32 T4096 d128 bf16 take 24 us (64 MB
+// written), with the gradients' operands 49 us, of which the 154 MB that they write are
+// two thirds.  Two waves a SIMD, for the accumulators of up to three products; with the
+// gradients' operands 12 to 24 registers of d_k 64 and 128 go through scratch.
 #include <algorithm>
 
 #include "kda_delta_chunk.hpp"
