@@ -11,8 +11,9 @@
 //   dg_t = sum_{r >= t} (dO_r . o_r - dv_r . v_r) + <S_T, dS_T>
 // In each summand o holds p_r beta_r v_r of the token's own write (p = scale q . k)
 // and dv holds beta_r p_r dO_r of its own output.  These cancel, and behind a strong
-// decay they are all there is: left in, they cost dg its digits (8e-6 of its norm for a
-// head of decays e^-3, all of it for one of e^-15).  Without them a summand is
+// decay they are all there is: left in, they cost dg its digits (of a head's norm 2e-5
+// to 2e-4 with decays of e^-3, 5e-3 to 3e-2 with e^-10, many times it with e^-20, where
+// it is 1e-6 to 8e-6 without them).  Without them a summand is
 //   dO_r . (o'_r - beta_r p_r s_r) - beta_r y_r . v_r
 // where o', s = S^T k and y = Y^T k are what the decayed state before r gives to the
 // output and to the key, and the gradient behind r to the key: the first part is the

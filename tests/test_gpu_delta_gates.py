@@ -16,8 +16,8 @@ pytestmark = pytest.mark.gpu
 # over channels and columns.  512 such errors at random make sqrt(512) 8 2^-24 = 1.1e-5 of a summand,
 # which is of a head's typical dg; the anchor's, which all tokens of a window share and which is larger
 # where dS_T is, is 2^-24 of the state's norms times the square root of 256 tokens: 16 2^-24 = 1e-6 times
-# what it exceeds a typical dg by (here up to 10).  Parts that cancel would lose more: 8e-6 at g = -3 is the
-# start of it, 6e-3 at -10, all at -20.
+# what it exceeds a typical dg by (here up to 10).  Parts that cancel lose more: 2e-5 to
+# 2e-4 at g = -3, 5e-3 to 3e-2 at -10, many times the norm at -20.
 LIMIT = 1.1e-5
 RATES = (0.01, 0.3, 3.0, 5.0, 10.0, 20.0)
 
