@@ -71,32 +71,38 @@ def decode_alg_bytes(B, H, d, es=2):
     return B * H * (2 * d * d * 4 + 5 * d * es + 4)
 
 
-def measured_traffic(key):
-    """HBM bytes per launch (or pass) recorded under profiles/traffic.json
-    (calibrated FETCH_SIZE + WRITE_SIZE), or None if the record is missing or
-    the kernel sources it was taken on have changed since."""
+def source_fingerprint(sources):
+    """A hash of kernel sources and of the flags each is compiled with.  (Not of
+    the build script, whose list of other sources says nothing about these.)"""
     import hashlib
+    from linear_attention_recurrence_05_amd import build
+    parts = []
+    for s in sources:
+        parts.append(open(os.path.join(ROOT, s), "rb").read())
+        if s.endswith(".hip"):
+            flags = build.source_flags(os.path.basename(s))
+            parts.append("\n".join(f.replace(build.ROOT, "") for f in flags).encode())
+    return hashlib.sha256(b"\0".join(parts)).hexdigest()[:16]
+
+
+def recorded(key, field):
+    """A figure recorded under profiles/traffic.json, or None if the record is
+    missing or what it was taken on has changed since."""
     try:
         rec = json.load(open(os.path.join(ROOT, "profiles", "traffic.json")))["records"][key]
-        h = hashlib.sha256(b"".join(open(os.path.join(ROOT, s), "rb").read()
-                                    for s in rec["sources"])).hexdigest()[:16]
-        return rec["bytes"] if h == rec["sha256_16"] else None
+        return rec[field] if source_fingerprint(rec["sources"]) == rec["sha256_16"] else None
     except (OSError, KeyError, ValueError):
         return None
+
+
+def measured_traffic(key):
+    """HBM bytes per launch (or pass) (calibrated FETCH_SIZE + WRITE_SIZE)."""
+    return recorded(key, "bytes")
 
 
 def measured_record(key):
-    """A figure recorded under profiles/traffic.json (e.g. an MFMA-busy
-    fraction from counters), or None if it is missing or the kernel sources
-    it was taken on have changed since."""
-    import hashlib
-    try:
-        rec = json.load(open(os.path.join(ROOT, "profiles", "traffic.json")))["records"][key]
-        h = hashlib.sha256(b"".join(open(os.path.join(ROOT, s), "rb").read()
-                                    for s in rec["sources"])).hexdigest()[:16]
-        return rec["value"] if h == rec["sha256_16"] else None
-    except (OSError, KeyError, ValueError):
-        return None
+    """Another figure, e.g. an MFMA-busy fraction from counters."""
+    return recorded(key, "value")
 
 
 def cpu_model():
