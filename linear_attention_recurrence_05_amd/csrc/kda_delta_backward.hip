@@ -301,8 +301,10 @@ struct DeltaQK {
 // as operands.  dbeta = Z . E on the way.
 // With bf16 U, R and the pairs' weights are two bf16 terms, S and Y one (what they
 // leave out is half a step on a part of the sum, beside the result's own rounding:
-// dq and dk are off by 2.3e-3 of their norm, 1.7e-3 of it that rounding; with all of
-// them one by 3.0e-3).  Bound by the latency of what it reads, 180 KB a chunk and
+// dq and dk are off by 2.1e-3 to 2.6e-3 of their norm, 1.7e-3 of it that rounding, more
+// only where a large state is undone by the chunk's own tokens; with all of them one
+// term they were off by 3.0e-3, with S and Y two by that rounding alone, for 628 us of
+// the whole call instead of 551).  Bound by the latency of what it reads, 180 KB a chunk and
 // head with one workgroup a CU: B1 H32 T4096 d128 takes 124 us, 3.2 TB/s.  32 columns
 // of 64, with 168 registers (64 of them took 3 us more); two workgroups a CU (128
 // registers) spilled and took 287 us.

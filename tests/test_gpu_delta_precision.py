@@ -45,6 +45,13 @@ def test_prefill_and_gradients(size, dtype):
     check(inputs(*size, dtype, seed=size[1]))
 
 
+@pytest.mark.parametrize("size", [(1, 300, 4, 4, 64, 64), (1, 256, 4, 2, 128, 128), (2, 90, 4, 4, 32, 32)])
+def test_gradients_where_queries_and_keys_are_alike(size):
+    need_gpu()
+    say("precision, alike", size)
+    check(inputs(*size, BF, seed=size[1], queries=True))
+
+
 @pytest.mark.parametrize("dk", [32, 64, 128])
 def test_many_heads(dk):
     """A workgroup for each head (from 128 of them and 128 value columns on)."""
