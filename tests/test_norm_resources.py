@@ -18,7 +18,7 @@ def test_block_norm_gradients_use_every_cu(dtype):
     kda = pytest.importorskip("linear_attention_recurrence_05_amd")
     if not os.path.exists(kbuild.library_path()):
         pytest.skip("library not built")
-    for D in range(8, kda.KDA_MAX_NORM_WIDTH + 1, 8):
+    for D in (8, 256, 264, 504, 520, 1024, 1032, 2048, 2056, 4096, 4104, 8192, 8200, 12288, kda.KDA_MAX_NORM_WIDTH):
         groups = kda.kda_block_norm_backward_workspace_bytes(1 << 20, D, dtype) / (2 * D * 4)
         assert groups % CUS == 0 and groups >= CUS, (D, groups)
 
